@@ -442,7 +442,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int a0 = (tree_first + j - nprefix) * BN;
             const int lim_t = is_tree ? (n + 1 - a0) : (P - (t_begin + j) * BN);
             const bool key_r_valid = r < lim_t;
-            const int lim = lim_t - key0;  // valid keys among the group's columns
+            // valid keys among the group's columns (a lone tile's group owns 64: its
+            // other columns hold whatever the tensor memory held before)
+            const int lim = min(lim_t - key0, ncol);
             const bool full = !is_tree && lim >= ncol;
             uint32_t vm[4];
 #pragma unroll
