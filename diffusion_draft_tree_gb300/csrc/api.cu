@@ -1,6 +1,8 @@
 // api.cu -- the C ABI (include/ddtree.h): host-side validation, the per-device
 // error word, and dispatch to the kernel launchers.  No allocation, no
 // synchronisation except in ddtree_device_check().
+#include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <mutex>
 
@@ -93,6 +95,11 @@ size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, in
             if (B <= 0 || N < 0 || V <= 0 || (dtype != DDTREE_BF16 && dtype != DDTREE_FP32))
                 return 0;
             return ddt::accept_workspace_bytes(B, N, V, dtype);
+        case DDTREE_OP_TREE_ATTN_PAGED:
+            if (B <= 0 || N < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128 || D <= 0 ||
+                cache_cap < 0 || cache_cap > INT32_MAX)
+                return 0;
+            return ddt::paged_attn_workspace_bytes(B, N, Hq, Hkv, D, cache_cap);
     }
     return 0;
 }
@@ -250,6 +257,206 @@ ddtree_status ddtree_commit(void* k_cache, void* v_cache, int64_t cache_cap, con
     ddt::CommitArgs a{k_cache, v_cache, cache_cap, k_tree, v_tree, accept_len, accepted_nodes,
                       prefix_len, B, L, N, Hkv, D, error_word()};
     return launched(ddt::launch_commit(a, (cudaStream_t)stream));
+}
+
+// ---- the round over a paged cache ----------------------------------------------
+
+namespace {
+
+int esize(int dtype) { return dtype == DDTREE_FP32 ? 4 : 2; }
+bool dtype16(int dtype) { return dtype == DDTREE_BF16 || dtype == DDTREE_FP16; }
+
+// A ddtree_rows that can be read (out: written) as rows of D elements: not null,
+// on the element grid, strides sane.
+bool rows_ok(const ddtree_rows* r, int dtype, int D, bool out) {
+    if (!r || !r->data || r->heads <= 0 || !aligned(r->data, esize(dtype))) return false;
+    const int64_t least = out ? D : 0;
+    return r->token_stride >= least && (r->heads == 1 || r->head_stride >= least);
+}
+// ... and also by 16-byte accesses.
+bool rows16(const ddtree_rows* r) {
+    return aligned(r->data, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+// q_out: as many heads as q; the same tensor only with the same strides.
+bool pair_ok(const ddtree_rows* in, const ddtree_rows* out, int dtype, int D) {
+    if (!rows_ok(in, dtype, D, false) || !rows_ok(out, dtype, D, true)) return false;
+    if (in->heads != out->heads) return false;
+    return in->data != out->data || (in->token_stride == out->token_stride &&
+                                     (in->heads == 1 || in->head_stride == out->head_stride));
+}
+ddt::RowsArg rows_arg(const ddtree_rows* r) {
+    return r ? ddt::RowsArg{r->data, r->heads, r->token_stride, r->head_stride} : ddt::RowsArg{};
+}
+
+ddtree_status cache_status(const ddtree_paged_cache* c) {
+    if (!c || !c->k_pages || !c->v_pages || !c->page_table) return DDTREE_ERR_INVALID_ARG;
+    if (!dtype16(c->dtype) || c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0 || c->D <= 0 ||
+        c->max_pages <= 0 || c->table_stride < c->max_pages ||
+        (int64_t)c->max_pages * c->page_size > INT32_MAX)
+        return DDTREE_ERR_INVALID_ARG;
+    if ((c->num_pages > 1 && c->page_stride < c->D) || (c->Hkv > 1 && c->head_stride < c->D) ||
+        (c->page_size > 1 && c->slot_stride < c->D))
+        return DDTREE_ERR_INVALID_ARG;
+    if (c->page_stride < 0 || c->head_stride < 0 || c->slot_stride < 0)
+        return DDTREE_ERR_INVALID_ARG;
+    if (!aligned(c->k_pages, 2) || !aligned(c->v_pages, 2) || !aligned(c->page_table, 4))
+        return DDTREE_ERR_INVALID_ARG;
+    return DDTREE_OK;
+}
+bool cache16(const ddtree_paged_cache* c) {
+    return aligned(c->k_pages, 16) && aligned(c->v_pages, 16) && c->page_stride % 8 == 0 &&
+           c->head_stride % 8 == 0 && c->slot_stride % 8 == 0;
+}
+ddt::PagedArgs cache_arg(const ddtree_paged_cache* c) {
+    return {c->k_pages, c->v_pages, c->dtype, c->num_pages, c->page_size, c->Hkv, c->D,
+            c->page_stride, c->head_stride, c->slot_stride, c->page_table, c->max_pages,
+            c->table_stride};
+}
+
+bool rotary_ok(const ddtree_rotary* r, int D) {
+    return r && r->turns && aligned(r->turns, 8) && r->rot_dim >= 2 && r->rot_dim % 2 == 0 &&
+           r->rot_dim <= D && std::isfinite(r->scale);
+}
+
+}  // namespace
+
+ddtree_status ddtree_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                      double orig_len, double low, double high,
+                                      double* inv_freq, float* scale) {
+    if (!inv_freq || !scale || rot_dim < 2 || rot_dim % 2) return DDTREE_ERR_INVALID_ARG;
+    if (rot_dim > DDTREE_MAX_ROPE_D) return DDTREE_ERR_UNSUPPORTED;
+    if (scaling < DDTREE_ROPE_NONE || scaling > DDTREE_ROPE_YARN || !(base > 0) ||
+        !std::isfinite(base) || (scaling != DDTREE_ROPE_NONE && !(factor > 0 && std::isfinite(factor))))
+        return DDTREE_ERR_INVALID_ARG;
+    if (scaling >= DDTREE_ROPE_BANDED &&
+        !(orig_len > 0 && std::isfinite(orig_len) && low > 0 && high > low && std::isfinite(high)))
+        return DDTREE_ERR_INVALID_ARG;
+    if (scaling == DDTREE_ROPE_YARN && !(base > 1)) return DDTREE_ERR_INVALID_ARG;
+    if (scaling == DDTREE_ROPE_NTK) {
+        if (rot_dim < 4) return DDTREE_ERR_INVALID_ARG;
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    }
+    constexpr double kTwoPi = 6.283185307179586476925;
+    double lo = 0, hi = 0;
+    if (scaling == DDTREE_ROPE_YARN) {
+        auto dim = [&](double t) {
+            return rot_dim * std::log(orig_len / (kTwoPi * t)) / (2 * std::log(base));
+        };
+        lo = std::max(std::floor(dim(high)), 0.0);
+        hi = std::min(std::ceil(dim(low)), (double)rot_dim - 1);
+    }
+    *scale = scaling == DDTREE_ROPE_YARN && factor > 1 ? (float)(0.1 * std::log(factor) + 1) : 1.f;
+    for (int j = 0; j < rot_dim / 2; ++j) {
+        const double f = std::pow(base, -2.0 * j / rot_dim);
+        double s = 1;  // share of the unscaled frequency
+        if (scaling == DDTREE_ROPE_LINEAR) s = 0;
+        if (scaling == DDTREE_ROPE_BANDED) s = (orig_len * f / kTwoPi - low) / (high - low);
+        if (scaling == DDTREE_ROPE_YARN) s = 1 - (j - lo) / std::max(hi - lo, 1e-3);
+        s = std::min(std::max(s, 0.0), 1.0);
+        inv_freq[j] = s == 1 ? f : (1 - s) * (f / factor) + s * f;
+    }
+    return DDTREE_OK;
+}
+
+ddtree_status ddtree_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
+    if (!inv_freq || !turns || n < 1) return DDTREE_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j)
+        if (!std::isfinite(inv_freq[j])) return DDTREE_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+        const double t = inv_freq[j] / 6.283185307179586476925;
+        const double frac = t - std::floor(t);  // [0, 1], 1 only for a tiny negative t
+        turns[j] = frac < 1 ? (uint64_t)std::ldexp(frac, 64) : 0;
+    }
+    return DDTREE_OK;
+}
+
+ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const ddtree_rows* k,
+                          const ddtree_rows* k_out, int dtype, int T, int D, const int32_t* pos,
+                          const ddtree_rotary* rot, int inverse, void* stream) {
+    if ((dtype != DDTREE_FP32 && !dtype16(dtype)) || T < 0 || D < 1 ||
+        (inverse != 0 && inverse != 1))
+        return DDTREE_ERR_INVALID_ARG;
+    if (D > DDTREE_MAX_ROPE_D) return DDTREE_ERR_UNSUPPORTED;
+    if (T == 0) return DDTREE_OK;
+    if (!pos || !aligned(pos, 4) || !pair_ok(q, q_out, dtype, D) || (k || k_out ? !pair_ok(k, k_out, dtype, D) : false) ||
+        !rotary_ok(rot, D))
+        return DDTREE_ERR_INVALID_ARG;
+    if (k && ((int64_t)q->heads + k->heads > 65535)) return DDTREE_ERR_UNSUPPORTED;
+    ddt::RopeArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(k_out), dtype, T, D, pos,
+                    rot->turns, rot->rot_dim, rot->interleaved != 0, rot->scale, inverse};
+    return launched(ddt::launch_rope(a, (cudaStream_t)stream));
+}
+
+ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, int T,
+                                  const int32_t* seq, const int32_t* pos, int B,
+                                  const ddtree_paged_cache* cache, const ddtree_rotary* rot,
+                                  const ddtree_rows* q, const ddtree_rows* q_out, void* stream) {
+    if (ddtree_status st = cache_status(cache)) return st;
+    const int dt = cache->dtype, D = cache->D;
+    if (T < 0 || B <= 0) return DDTREE_ERR_INVALID_ARG;
+    if (D > DDTREE_MAX_ROPE_D) return DDTREE_ERR_UNSUPPORTED;
+    if (T == 0) return DDTREE_OK;
+    if (!seq || !pos || !aligned4({seq, pos})) return DDTREE_ERR_INVALID_ARG;
+    if (!rows_ok(k, dt, D, false) || !rows_ok(v, dt, D, false) || k->heads != cache->Hkv ||
+        v->heads != cache->Hkv || (q || q_out ? !pair_ok(q, q_out, dt, D) : false) ||
+        (rot && !rotary_ok(rot, D)))
+        return DDTREE_ERR_INVALID_ARG;
+    if (2 * (int64_t)cache->Hkv + (q ? q->heads : 0) > 65535) return DDTREE_ERR_UNSUPPORTED;
+    ddt::AppendArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(v), T, B, seq, pos,
+                      cache_arg(cache), rot ? rot->turns : nullptr, rot ? rot->rot_dim : 0,
+                      rot && rot->interleaved, rot ? rot->scale : 1.f, error_word()};
+    return launched(ddt::launch_append_paged(a, (cudaStream_t)stream));
+}
+
+ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_cache* cache,
+                                     const ddtree_rows* k_tree, const ddtree_rows* v_tree,
+                                     const int32_t* prefix_len, const int32_t* n_nodes,
+                                     const uint32_t* anc_mask, int B, int N, float scale,
+                                     void* out, float* lse, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+    if (ddtree_status st = cache_status(cache)) return st;
+    const int dt = cache->dtype, D = cache->D, Hkv = cache->Hkv, ps = cache->page_size;
+    if (!prefix_len || !n_nodes || !anc_mask || !out || B <= 0 || N < 0 || !(scale > 0.f) ||
+        !std::isfinite(scale))
+        return DDTREE_ERR_INVALID_ARG;
+    if (!rows_ok(q, dt, D, true) || !rows_ok(k_tree, dt, D, true) ||
+        !rows_ok(v_tree, dt, D, true) || k_tree->heads != Hkv || v_tree->heads != Hkv ||
+        q->heads % Hkv)
+        return DDTREE_ERR_INVALID_ARG;
+    if (N > DDTREE_MAX_N || (D != 64 && D != 128) || q->heads / Hkv > 128 || ps < 8 ||
+        (ps & (ps - 1)) || (int64_t)B * (N + 1) > INT32_MAX)
+        return DDTREE_ERR_UNSUPPORTED;
+    if (!rows16(q) || !rows16(k_tree) || !rows16(v_tree) || !cache16(cache) || !aligned(out, 16) ||
+        !aligned4({prefix_len, n_nodes, anc_mask, lse}))
+        return DDTREE_ERR_INVALID_ARG;
+    const size_t need = ddt::paged_attn_workspace_bytes(B, N, q->heads, Hkv, D,
+                                                        (int64_t)cache->max_pages * ps);
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+        return DDTREE_ERR_INVALID_ARG;
+    ddt::PagedAttnArgs a{rows_arg(q), rows_arg(k_tree), rows_arg(v_tree), cache_arg(cache),
+                         prefix_len, n_nodes, anc_mask, B, N, scale, out, lse, workspace,
+                         error_word()};
+    return launched(ddt::launch_tree_attn_paged(a, (cudaStream_t)stream));
+}
+
+ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_rows* k_tree,
+                                  const ddtree_rows* v_tree, const int32_t* accept_len,
+                                  const int32_t* accepted_nodes, const int32_t* prefix_len,
+                                  int32_t* new_len, int B, int L, int N, void* stream) {
+    if (ddtree_status st = cache_status(cache)) return st;
+    const int dt = cache->dtype, D = cache->D;
+    if (!accept_len || !accepted_nodes || !prefix_len || new_len == prefix_len || B <= 0 ||
+        B > 65535 || L <= 0 || N < 0)
+        return DDTREE_ERR_INVALID_ARG;
+    if (!rows_ok(k_tree, dt, D, false) || !rows_ok(v_tree, dt, D, false) ||
+        k_tree->heads != cache->Hkv || v_tree->heads != cache->Hkv ||
+        !aligned4({accept_len, accepted_nodes, prefix_len, new_len}))
+        return DDTREE_ERR_INVALID_ARG;
+    if (L > DDTREE_MAX_L || N > DDTREE_MAX_N || D % 8 != 0) return DDTREE_ERR_UNSUPPORTED;
+    if (!rows16(k_tree) || !rows16(v_tree) || !cache16(cache)) return DDTREE_ERR_INVALID_ARG;
+    ddt::CommitPagedArgs a{cache_arg(cache), rows_arg(k_tree), rows_arg(v_tree), accept_len,
+                           accepted_nodes, prefix_len, new_len, B, L, N, error_word()};
+    return launched(ddt::launch_commit_paged(a, (cudaStream_t)stream));
 }
 
 namespace {

@@ -72,7 +72,67 @@ commit_kernel(uint4* __restrict__ k_cache, uint4* __restrict__ v_cache, int64_t 
     if (tid == 0) prefix_len[b] = (int32_t)(P + a + 1);
 }
 
+// The same commit into a paged cache.  One CTA per (path row, sequence): each
+// checks the whole path and its pages with one warp -- lane i row i, L + 1 <= 17
+// rows -- so that all of a sequence's CTAs reach the same verdict without
+// talking to each other, then copies its row's Hkv heads of K and V, 16 bytes a
+// thread.  A row of a few KB is latency, not bandwidth: with a CTA a row every
+// copy is in flight at once, where one CTA a sequence would take up to 17 turns.
+__global__ void __launch_bounds__(kThreads)
+commit_paged_kernel(const __grid_constant__ PagedArgs c, const RowsArg kt, const RowsArg vt,
+                    const int32_t* __restrict__ accept_len,
+                    const int32_t* __restrict__ accepted_nodes,
+                    const int32_t* __restrict__ prefix_len, int32_t* __restrict__ new_len, int L,
+                    int N, uint32_t* err) {
+    __shared__ int s_ok, s_node, s_page;
+    const int b = blockIdx.y, row = blockIdx.x, tid = threadIdx.x;
+    pdl_wait();
+    const int P = prefix_len[b], a = accept_len[b];
+    if (tid < 32) {
+        // what is wrong with path row `tid`, the first kind found over the warp
+        uint32_t bad = 0;
+        int node = 0, page = 0;
+        if (a < 0 || a > L || P < 0 || (int64_t)P + a + 1 > (int64_t)c.max_pages * c.page_size) {
+            bad = ERR_BAD_PREFIX_LEN;
+        } else if (tid <= a) {
+            if (tid > 0) node = accepted_nodes[(size_t)b * L + tid - 1];
+            page = c.table[b * c.table_stride + (P + tid) / c.page_size];
+            if (tid > 0 && (node < 1 || node > N)) bad = ERR_BAD_TREE;
+            else if (page < 0 || page >= c.num_pages) bad = ERR_BAD_PAGE;
+        }
+        const uint32_t worst = __reduce_max_sync(0xffffffffu, bad);
+        if (tid == 0) {
+            s_ok = worst == 0;
+            if (worst && row == 0) record_error(err, ERR_COMMIT | worst);
+        }
+        if (tid == row) {
+            s_node = node;
+            s_page = page;
+        }
+    }
+    __syncthreads();
+    pdl_trigger();
+    if (row == 0 && tid == 0 && new_len) new_len[b] = s_ok ? P + a + 1 : P;
+    if (!s_ok || row > a) return;
+    const int vd = c.D / 8;
+    const int64_t tok = (int64_t)b * (N + 1) + s_node;
+    const int64_t dst = s_page * c.page_stride + (P + row) % c.page_size * c.slot_stride;
+    for (int i = tid; i < 2 * c.Hkv * vd; i += kThreads) {
+        const int which = i / (c.Hkv * vd), j = i - which * c.Hkv * vd;
+        const int g = j / vd, e = (j - g * vd) * 8;
+        const RowsArg& src = which ? vt : kt;
+        uint16_t* to = (uint16_t*)(which ? c.v : c.k) + dst + g * c.head_stride + e;
+        *(uint4*)to = __ldg((const uint4*)((const uint16_t*)src.data + tok * src.ts + g * src.hs + e));
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_commit_paged(const CommitPagedArgs& a, cudaStream_t s) {
+    return launch_pdl(commit_paged_kernel, dim3(a.L + 1, a.B), dim3(kThreads), 0, s, a.cache,
+                      a.k_tree, a.v_tree, a.accept_len, a.accepted_nodes, a.prefix_len, a.new_len,
+                      a.L, a.N, a.err);
+}
 
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s) {
     return launch_pdl(commit_kernel, dim3(a.B), dim3(kThreads), 0, s, (uint4*)a.k_cache,

@@ -21,6 +21,7 @@ enum : uint32_t {
     ERR_ATTN = 0x03000000u,
     ERR_ACCEPT = 0x04000000u,
     ERR_COMMIT = 0x05000000u,
+    ERR_APPEND = 0x06000000u,
     ERR_SELFTEST = 0x0F000000u,  // ddtree_selftest_wait
     ERR_BAD_PREFIX_LEN = 0x1,
     ERR_BAD_N_NODES = 0x2,
@@ -28,6 +29,7 @@ enum : uint32_t {
     ERR_WAIT_TIMEOUT = 0x4,
     ERR_BAD_INPUT = 0x5,
     ERR_PLAN = 0x6,  // a launch plan the kernel cannot carry out (a library bug)
+    ERR_BAD_PAGE = 0x7,  // a page number outside the pool
 };
 
 DDT_DEV void record_error(uint32_t* err, uint32_t code) {

@@ -92,6 +92,77 @@ struct CommitArgs {
 };
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 
+// ---- paged cache ---------------------------------------------------------------
+// Tokens' heads seen through strides (elements); the rows of a token's head are
+// D contiguous elements.  heads == 0: absent.
+struct RowsArg {
+    void* data;
+    int heads;
+    int64_t ts, hs;
+};
+// Pages of a KV pool: row (page, head, slot) at page * page_stride + head *
+// head_stride + slot * slot_stride (elements), in k and in v.
+struct PagedArgs {
+    void *k, *v;
+    int dtype;
+    int num_pages, page_size, Hkv, D;
+    int64_t page_stride, head_stride, slot_stride;
+    const int32_t* table;
+    int max_pages;
+    int64_t table_stride;
+};
+
+struct RopeArgs {
+    RowsArg q, q_out, k, k_out;
+    int dtype, T, D;
+    const int32_t* pos;
+    const uint64_t* turns;
+    int rot;
+    bool interleaved;
+    float scale;
+    int inverse;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+    RowsArg q, q_out, k, v;
+    int T, B;
+    const int32_t *seq, *pos;
+    PagedArgs cache;
+    const uint64_t* turns;
+    int rot;  // 0: no rotation
+    bool interleaved;
+    float scale;
+    uint32_t* err;
+};
+cudaError_t launch_append_paged(const AppendArgs& a, cudaStream_t s);
+
+struct CommitPagedArgs {
+    PagedArgs cache;
+    RowsArg k_tree, v_tree;
+    const int32_t *accept_len, *accepted_nodes, *prefix_len;
+    int32_t* new_len;
+    int B, L, N;
+    uint32_t* err;
+};
+cudaError_t launch_commit_paged(const CommitPagedArgs& a, cudaStream_t s);
+
+struct PagedAttnArgs {
+    RowsArg q, k_tree, v_tree;
+    PagedArgs cache;
+    const int32_t* prefix_len;
+    const int32_t* n_nodes;
+    const uint32_t* anc_mask;
+    int B, N;
+    float scale;
+    void* out;
+    float* lse;
+    void* ws;
+    uint32_t* err;
+};
+size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t cache_cap);
+cudaError_t launch_tree_attn_paged(const PagedAttnArgs& a, cudaStream_t s);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ---- shared by the entry points (api.cu) --------------------------------------

@@ -22,12 +22,34 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libddtree.so")
 
-BF16, FP32 = 0, 1
-OP_TOPK, OP_TREE_ATTN, OP_ACCEPT = 0, 2, 3
+BF16, FP32, FP16 = 0, 1, 2
+OP_TOPK, OP_TREE_ATTN, OP_ACCEPT, OP_TREE_ATTN_PAGED = 0, 2, 3, 4
 MAX_K, MAX_L, MAX_N = 32, 16, 1024
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error",
           4: "kernel recorded bad device data or a timeout"}
+
+
+class _Rows(ctypes.Structure):
+    """ddtree_rows."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):
+    """ddtree_paged_cache."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64)]
+
+
+class _Rotary(ctypes.Structure):
+    """ddtree_rotary."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class DDTreeError(RuntimeError):
@@ -62,6 +84,16 @@ def _load() -> ctypes.CDLL:
     lib.ddtree_accept_path.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i32, f32, u64, u64,
                                        P, P, P, P, P, P]
     lib.ddtree_topk_noalloc.argtypes = [P, i32, i32, i32, i64, i32, P, P, P, P]
+    rows, cache, rotary = (ctypes.POINTER(c) for c in (_Rows, _Cache, _Rotary))
+    f64 = ctypes.c_double
+    lib.ddtree_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
+                                            ctypes.POINTER(f64), ctypes.POINTER(f32)]
+    lib.ddtree_rope_turns.argtypes = [ctypes.POINTER(f64), i32, ctypes.POINTER(u64)]
+    lib.ddtree_rope.argtypes = [rows, rows, rows, rows, i32, i32, i32, P, rotary, i32, P]
+    lib.ddtree_append_paged.argtypes = [rows, rows, i32, P, P, i32, cache, rotary, rows, rows, P]
+    lib.ddtree_tree_attn_paged.argtypes = [rows, cache, rows, rows, P, P, P, i32, i32, f32, P, P,
+                                           P, sz, P]
+    lib.ddtree_commit_paged.argtypes = [cache, rows, rows, P, P, P, P, i32, i32, i32, P]
     lib.ddtree_device_check.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.ddtree_selftest_wait.argtypes = [ctypes.c_uint32, P]
     lib.ddtree_last_cuda_error.argtypes = []
@@ -70,7 +102,9 @@ def _load() -> ctypes.CDLL:
     lib.ddtree_status_str.restype = ctypes.c_char_p
     for f in ("ddtree_topk", "ddtree_build", "ddtree_build_heap", "ddtree_tree_attn",
               "ddtree_accept", "ddtree_accept_path", "ddtree_commit", "ddtree_topk_noalloc",
-              "ddtree_device_check", "ddtree_selftest_wait"):
+              "ddtree_device_check", "ddtree_selftest_wait", "ddtree_rope_frequencies",
+              "ddtree_rope_turns", "ddtree_rope", "ddtree_append_paged",
+              "ddtree_tree_attn_paged", "ddtree_commit_paged"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -79,7 +113,8 @@ lib = _load()
 
 EXPORTED = ("ddtree_workspace_size", "ddtree_topk", "ddtree_build", "ddtree_build_heap",
             "ddtree_tree_attn", "ddtree_accept", "ddtree_device_check", "ddtree_last_cuda_error",
-            "ddtree_status_str")
+            "ddtree_status_str", "ddtree_rope", "ddtree_append_paged", "ddtree_tree_attn_paged",
+            "ddtree_commit_paged")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -286,3 +321,288 @@ def accept(target_logits, tree: dict, L: int, temperature=0.0, seed=0, step=0, w
     ddtree_accept(target_logits, tree["parent"], tree["token"], tree["n_nodes"], L, out,
                   temperature, seed, step, workspace, stream)
     return out
+
+
+# --------------------------------------------------------------------------
+# the round over a paged cache
+# --------------------------------------------------------------------------
+# These calls take strided views: slices of a fused projection, either page
+# layout, a pool that interleaves keys and values.  Only the last dimension of a
+# tensor has to be contiguous.  Everything a call is given has to be on one
+# device, which need not be the current one; without `stream` it is enqueued on
+# that device's current stream.
+
+_CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
+
+
+def _rows(t: torch.Tensor, name: str, D: int, dtype, index: int):
+    """ddtree_rows of a [tokens][heads][D] or [B][nodes][heads][D] tensor, and its
+    number of tokens."""
+    shape, st = t.shape, t.stride()
+    if len(shape) == 4:
+        if shape[1] == 1:
+            ts = st[0]
+        elif shape[0] == 1 or st[0] == shape[1] * st[1]:
+            ts = st[1]
+        else:
+            raise ValueError(f"{name}: the strides of its first two dimensions do not merge")
+        tokens, heads, hs = shape[0] * shape[1], shape[2], st[2]
+    elif len(shape) == 3:
+        tokens, heads, ts, hs = shape[0], shape[1], st[0], st[1]
+    else:
+        raise ValueError(f"{name} must be [tokens][heads][D] or [B][nodes][heads][D]")
+    if t.get_device() != index or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}, got {t.dtype} on "
+                         f"{t.device}")
+    if shape[-1] != D or (st[-1] != 1 and D > 1):
+        raise ValueError(f"{name} must end in {D} contiguous elements")
+    # (the stride of a dimension of one entry says nothing)
+    return _Rows(t.data_ptr(), heads, ts if tokens > 1 else max(ts, heads * hs, D),
+                 hs if heads > 1 else D), tokens
+
+
+def _ints(t: torch.Tensor, name: str, shape: tuple, index: int):
+    """Device pointer of a contiguous int32 tensor of the given shape."""
+    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != index or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _enqueue(name: str, index: int, stream, *args):
+    """Calls the library with `index` as the current device and its stream last."""
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to "
+                         f"cuda:{index}")
+    fn = getattr(lib, name)
+    if torch.cuda.current_device() == index:
+        _check(name, fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(index):
+            _check(name, fn(*args, stream.cuda_stream))
+
+
+def _index(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("ddtree kernels take CUDA tensors")
+    return t.get_device()
+
+
+class Rotary:
+    """A rotation: which elements are paired, by how much a position turns each
+    pair (include/ddtree.h, ddtree_rotary).  Made once, used by every call.
+
+    rot_dim elements of a head are rotated; `interleaved` pairs (2j, 2j+1),
+    otherwise (j, j + rot_dim/2).  scaling is "none", "linear", "ntk", "banded" or
+    "yarn", with factor, orig_len, low and high as ddtree_rope_frequencies has
+    them.  Frequencies of another kind can be given as inv_freq (radians per
+    position, rot_dim/2 of them), with their scale on cosine and sine."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0,
+                 low: float = 1.0, high: float = 4.0, inv_freq=None,
+                 scale: Optional[float] = None, device="cuda"):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+        n = max(rot_dim // 2, 1)
+        freq, own_scale = (ctypes.c_double * n)(), ctypes.c_float(1.0)
+        if inv_freq is None:
+            _check("ddtree_rope_frequencies", lib.ddtree_rope_frequencies(
+                rot_dim, base, ROPE_SCALINGS[scaling], factor, orig_len, low, high, freq,
+                ctypes.byref(own_scale)))
+        else:
+            values = [float(x) for x in inv_freq]
+            if rot_dim < 2 or rot_dim % 2 or len(values) != n:
+                raise ValueError(f"inv_freq must hold rot_dim / 2 values, rot_dim even; got "
+                                 f"{len(values)} for {rot_dim}")
+            freq = (ctypes.c_double * n)(*values)
+        turns = (ctypes.c_uint64 * n)()
+        _check("ddtree_rope_turns", lib.ddtree_rope_turns(freq, n, turns))
+        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
+        self.inv_freq = list(freq)
+        self.scale = own_scale.value if scale is None else float(scale)
+        signed = [x - (1 << 64) if x >> 63 else x for x in turns]
+        self.turns = torch.tensor(signed, dtype=torch.int64).to(device)
+        self._index = _index(self.turns)
+        self._c = _Rotary(self.turns.data_ptr(), rot_dim, int(self.interleaved), self.scale)
+
+
+class PagedCache:
+    """A paged KV cache: k_pages and v_pages [num_pages][Hkv][page_size][D] (bf16 or
+    fp16; views with equal strides, e.g. of a [num_pages][page_size][Hkv][D] pool
+    transposed) and page_table int32 [B][max_pages].  Holds the tensors, copies
+    nothing: pages and table may be changed in place between calls."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor):
+        index = _index(k_pages)
+        if k_pages.dim() != 4 or k_pages.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("k_pages must be a bf16 or fp16 [num_pages][Hkv][page_size][D] tensor")
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or \
+                v_pages.stride() != k_pages.stride() or v_pages.get_device() != index:
+            raise ValueError("v_pages must match k_pages in shape, type, strides and device")
+        if k_pages.stride(3) != 1 and k_pages.shape[3] > 1:
+            raise ValueError("a page's rows must be contiguous")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                page_table.get_device() != index or \
+                (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+            raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows, on the "
+                             "pages' device")
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.num_pages, self.Hkv, self.page_size, self.D = k_pages.shape
+        self.B, self.max_pages = page_table.shape
+        self.dtype, self.device, self._index = k_pages.dtype, k_pages.device, index
+        if 0 in k_pages.shape or 0 in page_table.shape:
+            raise ValueError("a paged cache needs at least one page, head, slot and table entry")
+        st = [s if n > 1 else k_pages.shape[3] for n, s in zip(k_pages.shape, k_pages.stride())]
+        self._c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), _CODES[self.dtype],
+                         self.num_pages, self.page_size, self.Hkv, self.D, st[0], st[1], st[2],
+                         page_table.data_ptr(), self.max_pages,
+                         page_table.stride(0) if self.B > 1 else self.max_pages)
+
+
+def ddtree_rope(q, k, pos, rotary: Rotary, q_out=None, k_out=None, inverse=False, stream=None):
+    """Rotates q and, unless it is None, k ([tokens][heads][D] or
+    [B][nodes][heads][D], bf16 / fp16 / fp32) for pos int32 [tokens] or
+    [B][nodes]; in place where no output is given."""
+    index, D, dtype = _index(q), q.shape[-1], q.dtype
+    if dtype not in _CODES:
+        raise ValueError(f"q must be bfloat16, float16 or float32, got {dtype}")
+    if rotary._index != index:
+        raise ValueError("rotary is on another device than q")
+    q_rows, T = _rows(q, "q", D, dtype, index)
+    q_to, k_rows, k_to = q_rows, None, None
+    if q_out is not None:
+        q_to, _ = _rows(q_out, "q_out", D, dtype, index)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    if k is not None:
+        k_rows, Tk = _rows(k, "k", D, dtype, index)
+        k_to = k_rows
+        if Tk != T:
+            raise ValueError(f"k has {Tk} tokens, q {T}")
+        if k_out is not None:
+            k_to, _ = _rows(k_out, "k_out", D, dtype, index)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    at = _ints(pos, "pos", (T,) if pos.dim() == 1 else q.shape[:2], index)
+    _enqueue("ddtree_rope", index, stream, q_rows, q_to, k_rows, k_to, _CODES[dtype], T, D, at,
+             rotary._c, int(bool(inverse)))
+
+
+def rope(q, k, pos, rotary: Rotary, inverse=False, stream=None):
+    """ddtree_rope into new tensors: (q, k) rotated; k may be None."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    ddtree_rope(q, k, pos, rotary, q_out, k_out, inverse, stream)
+    return q_out, k_out
+
+
+def ddtree_append_paged(k, v, seq, pos, cache: PagedCache, rotary: Optional[Rotary] = None,
+                        q=None, q_out=None, stream=None):
+    """Writes tokens' k (rotated for pos if a rotary is given) and v to positions
+    pos of sequences seq of the cache (int32 [tokens]; a negative pos: not
+    written), and rotates their queries q, in place unless q_out is given."""
+    index, D, dtype = cache._index, cache.D, cache.dtype
+    k_rows, T = _rows(k, "k", D, dtype, index)
+    v_rows, Tv = _rows(v, "v", D, dtype, index)
+    if Tv != T:
+        raise ValueError(f"v has {Tv} tokens, k {T}")
+    if rotary is not None and rotary._index != index:
+        raise ValueError("rotary is on another device than the cache")
+    q_rows = q_to = None
+    if q is not None:
+        q_rows, Tq = _rows(q, "q", D, dtype, index)
+        q_to = q_rows
+        if Tq != T:
+            raise ValueError(f"q has {Tq} tokens, k {T}")
+        if q_out is not None:
+            q_to, _ = _rows(q_out, "q_out", D, dtype, index)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    lead = (T,) if pos.dim() == 1 else k.shape[:2]
+    _enqueue("ddtree_append_paged", index, stream, k_rows, v_rows, T,
+             _ints(seq, "seq", lead, index), _ints(pos, "pos", lead, index), cache.B, cache._c,
+             None if rotary is None else rotary._c, q_rows, q_to)
+
+
+def paged_attn_workspace(q, cache: PagedCache) -> torch.Tensor:
+    """A workspace for ddtree_tree_attn_paged of q's sizes over the cache."""
+    B, R, Hq, D = q.shape
+    with torch.cuda.device(cache._index):
+        n = workspace_size(OP_TREE_ATTN_PAGED, B=B, N=R - 1, Hq=Hq, Hkv=cache.Hkv, D=D,
+                           cache_cap=cache.max_pages * cache.page_size)
+    return alloc_workspace(n, cache.device)
+
+
+def ddtree_tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask,
+                           out, lse=None, scale=None, workspace=None, stream=None):
+    """q [B][N+1][Hq][D], k_tree / v_tree [B][N+1][Hkv][D], prefix_len and n_nodes
+    [B], anc_mask int32 [B][N+1][W] -> out like q (contiguous), lse fp32
+    [B][N+1][Hq]."""
+    index, D, dtype = cache._index, cache.D, cache.dtype
+    if q.dim() != 4 or k_tree.dim() != 4 or v_tree.dim() != 4:
+        raise ValueError("q, k_tree and v_tree must be [B][nodes][heads][D]")
+    B, R, Hq, _ = q.shape
+    if k_tree.shape[:2] != (B, R) or v_tree.shape[:2] != (B, R) or cache.B != B:
+        raise ValueError("q, k_tree, v_tree and the page table must agree in B and nodes")
+    q_rows, _ = _rows(q, "q", D, dtype, index)
+    k_rows, _ = _rows(k_tree, "k_tree", D, dtype, index)
+    v_rows, _ = _rows(v_tree, "v_tree", D, dtype, index)
+    if out.shape != q.shape or out.dtype != dtype or out.get_device() != index or \
+            not out.is_contiguous():
+        raise ValueError("out must be contiguous, with q's shape, type and device")
+    if lse is not None and (lse.shape != (B, R, Hq) or lse.dtype != torch.float32 or
+                            lse.get_device() != index or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [B][nodes][Hq] on q's device")
+    if workspace is not None and (workspace.get_device() != index or
+                                  workspace.dtype != torch.uint8 or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _enqueue("ddtree_tree_attn_paged", index, stream, q_rows, cache._c, k_rows, v_rows,
+             _ints(prefix_len, "prefix_len", (B,), index), _ints(n_nodes, "n_nodes", (B,), index),
+             _ints(anc_mask, "anc_mask", (B, R, (R + 31) // 32), index), B, R - 1,
+             D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+             None if lse is None else lse.data_ptr(),
+             None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.numel())
+
+
+def tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask,
+                    scale=None, want_lse=True, workspace=None, stream=None):
+    B, R, Hq, _ = q.shape
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, R, Hq), dtype=torch.float32, device=q.device) if want_lse else None
+    if workspace is None:
+        workspace = paged_attn_workspace(q, cache)
+    ddtree_tree_attn_paged(q, cache, k_tree, v_tree, prefix_len, n_nodes, anc_mask, out, lse,
+                           scale, workspace, stream)
+    return out, lse
+
+
+def ddtree_commit_paged(cache: PagedCache, k_tree, v_tree, accept_len, accepted_nodes, prefix_len,
+                        new_len=None, stream=None):
+    """Writes the accepted path (root + accepted nodes, as ddtree_accept gives them)
+    of k_tree / v_tree [B][N+1][Hkv][D] to positions prefix_len.. of the cache;
+    prefix_len stays, new_len [B] receives prefix_len + accept_len + 1."""
+    index, D, dtype, B = cache._index, cache.D, cache.dtype, cache.B
+    if k_tree.dim() != 4 or k_tree.shape[0] != B or v_tree.shape != k_tree.shape:
+        raise ValueError("k_tree and v_tree must be [B][nodes][Hkv][D], B as the page table's")
+    if accepted_nodes.dim() != 2:
+        raise ValueError("accepted_nodes must be [B][L]")
+    k_rows, _ = _rows(k_tree, "k_tree", D, dtype, index)
+    v_rows, _ = _rows(v_tree, "v_tree", D, dtype, index)
+    L = accepted_nodes.shape[1]
+    _enqueue("ddtree_commit_paged", index, stream, cache._c, k_rows, v_rows,
+             _ints(accept_len, "accept_len", (B,), index),
+             _ints(accepted_nodes, "accepted_nodes", (B, L), index),
+             _ints(prefix_len, "prefix_len", (B,), index),
+             None if new_len is None else _ints(new_len, "new_len", (B,), index), B, L,
+             k_tree.shape[1] - 1)

@@ -60,21 +60,29 @@ typedef enum {
     DDTREE_ERR_DEVICE = 4       /* a kernel recorded bad device-side data or a timeout */
 } ddtree_status;
 
-typedef enum { DDTREE_BF16 = 0, DDTREE_FP32 = 1 } ddtree_dtype;
+/* DDTREE_FP16 is taken by the paged-cache calls and ddtree_rope only. */
+typedef enum { DDTREE_BF16 = 0, DDTREE_FP32 = 1, DDTREE_FP16 = 2 } ddtree_dtype;
 
 /* Operation ids for ddtree_workspace_size. */
-typedef enum { DDTREE_OP_TOPK = 0, DDTREE_OP_TREE_ATTN = 2, DDTREE_OP_ACCEPT = 3 } ddtree_op;
+typedef enum {
+    DDTREE_OP_TOPK = 0,
+    DDTREE_OP_TREE_ATTN = 2,
+    DDTREE_OP_ACCEPT = 3,
+    DDTREE_OP_TREE_ATTN_PAGED = 4
+} ddtree_op;
 
 /* Upper limits of this implementation. */
 #define DDTREE_MAX_K 32
 #define DDTREE_MAX_L 16
 #define DDTREE_MAX_N 1024
+#define DDTREE_MAX_ROPE_D 512 /* head dimension of ddtree_rope / ddtree_append_paged */
 
 /* Bytes of workspace that `op` needs for the given sizes (0 if it needs none,
  * or on an invalid combination).  Arguments an op does not use are ignored:
  *   TOPK:      rows = B*L, V, K, dtype
  *   TREE_ATTN: B, N, Hq, Hkv, D, cache_cap
- *   ACCEPT:    B, N, V, dtype */
+ *   ACCEPT:    B, N, V, dtype
+ *   TREE_ATTN_PAGED: B, N, Hq, Hkv, D, cache_cap = max_pages * page_size */
 size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, int dtype, int Hq,
                              int Hkv, int D, int64_t cache_cap);
 
@@ -257,13 +265,178 @@ ddtree_status ddtree_commit(void* k_cache, void* v_cache, int64_t cache_cap, con
                             const int32_t* accepted_nodes, int32_t* prefix_len, int B, int L,
                             int N, int Hkv, int D, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The round over a PAGED cache.  A server does not keep one dense
+ * [Hkv][cache_cap][D] block per sequence: its keys and values sit in pages of
+ * page_size positions, anywhere in a pool, listed per sequence in a table.  The
+ * calls below are the round's steps over such a cache, per layer:
+ *
+ *   ddtree_append_paged     prompts, or one token a sequence, into the pages,
+ *                           keys (and queries) rotated on the way
+ *   ddtree_rope             rotary positions of the tree's queries and keys
+ *   ddtree_tree_attn_paged  step 3 over the pages
+ *   ddtree_commit_paged     the accepted path into the pages
+ *
+ * (Rotary positions and the cache's layout are the target model's, not the
+ * paper's: "Accelerating Speculative Decoding with Block Diffusion Draft Trees"
+ * §4.1 only needs every node at position P + depth and the accepted path in
+ * the cache.)  The structs are host memory, read during the call. */
+
+/* Rows of D contiguous elements for tokens and their heads, through strides in
+ * elements: head h of token t starts at data + t * token_stride + h *
+ * head_stride.  Slices of a fused projection, or heads-first layouts, need no
+ * copy.  Strides are not negative; a row that is written has strides of at least
+ * D (rows that overlap are the caller's error). */
+typedef struct {
+    void* data; /* DEVICE; only read where the call says "in" */
+    int32_t heads;
+    int64_t token_stride, head_stride;
+} ddtree_rows;
+
+/* A paged cache.  Row (page, head, slot) of the keys is at k_pages + page *
+ * page_stride + head * head_stride + slot * slot_stride (elements), the
+ * values' the same in v_pages: [page][Hkv][page_size][D] and [page][page_size]
+ * [Hkv][D] are both such layouts, and so is one pool that interleaves keys and
+ * values.  Position p of sequence b is slot p % page_size of page
+ * page_table[b * table_stride + p / page_size].  Entries past a sequence's
+ * last position are not read and may hold anything; an entry that is read and
+ * lies outside [0, num_pages) is never dereferenced, only recorded (reason 7).  Pages may be shared between sequences by calls that only read them.
+ * max_pages * page_size is at most 2^31 - 1. */
+typedef struct {
+    void *k_pages, *v_pages; /* DEVICE */
+    int32_t dtype;           /* DDTREE_BF16 or DDTREE_FP16 */
+    int32_t num_pages, page_size, Hkv, D;
+    int64_t page_stride, head_stride, slot_stride;
+    const int32_t* page_table; /* DEVICE [B][table_stride] */
+    int32_t max_pages;         /* entries of a sequence, <= table_stride */
+    int64_t table_stride;
+} ddtree_paged_cache;
+
+/* A rotation: the first rot_dim (even) elements of a head, in pairs, pair j
+ * turned by position * turns[j] / 2^64 of a full turn; cosine and sine are
+ * multiplied by `scale`.  Pairs are elements (2j, 2j+1) if interleaved, else
+ * (j, j + rot_dim/2).  `turns` comes from ddtree_rope_turns(); the product with
+ * a position is exact modulo one turn, so far positions lose nothing. */
+typedef struct {
+    const uint64_t* turns; /* DEVICE [rot_dim / 2], 8-byte aligned */
+    int32_t rot_dim, interleaved;
+    float scale;
+} ddtree_rotary;
+
+/* How the frequencies f_j = base^(-2j / rot_dim) are changed for contexts
+ * longer than the model was trained on (orig_len positions), by `factor`:
+ *   NONE    f_j
+ *   LINEAR  f_j / factor
+ *   NTK     f_j of the base base * factor^(rot_dim / (rot_dim - 2))
+ *   BANDED  pairs that make t = orig_len f_j / 2pi turns: f_j above `high`
+ *           turns, f_j / factor below `low`, in between the mixture
+ *           (1 - s) f_j / factor + s f_j with s = (t - low) / (high - low)
+ *   YARN    f_j for j below lo, f_j / factor above hi, linear in j between,
+ *           lo = max(0, floor(d(high))), hi = min(rot_dim - 1, ceil(d(low))),
+ *           d(t) = rot_dim ln(orig_len / (2pi t)) / (2 ln base); and a scale of
+ *           0.1 ln(factor) + 1 (1 for factor <= 1) */
+typedef enum {
+    DDTREE_ROPE_NONE = 0,
+    DDTREE_ROPE_LINEAR = 1,
+    DDTREE_ROPE_NTK = 2,
+    DDTREE_ROPE_BANDED = 3,
+    DDTREE_ROPE_YARN = 4
+} ddtree_rope_scaling;
+
+/* Host only: the rot_dim / 2 angles per position (radians) of a scaling, and
+ * its scale.  rot_dim even, 2..DDTREE_MAX_ROPE_D (NTK: at least 4); base > 1
+ * (NONE, LINEAR, NTK, BANDED: base > 0); factor > 0; orig_len > 0 and
+ * 0 < low < high where they are used.  Both outputs are HOST memory. */
+ddtree_status ddtree_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                      double orig_len, double low, double high,
+                                      double* inv_freq, float* scale);
+
+/* Host only: n angles per position (radians, finite) -> turns per position as
+ * 64-bit fractions (whole turns drop out).  Both arrays are HOST memory. */
+ddtree_status ddtree_rope_turns(const double* inv_freq, int n, uint64_t* turns);
+
+/* Rotary positions of queries and, if given, keys of T tokens.
+ *   q, k       in (k nullable); q_out, k_out out: the same tensor (in place) or
+ *              one that does not overlap any input.  Elements past rot_dim are
+ *              copied.  D 1..DDTREE_MAX_ROPE_D.
+ *   dtype      DDTREE_BF16, DDTREE_FP16 or DDTREE_FP32; the product is formed
+ *              in 32 bits and rounded once.
+ *   pos        int32 [T].  A token at a negative position -- the padding rows of
+ *              ddtree_build's pos_id -- is copied as it is.
+ *   inverse    0, or 1 for the transpose (turns by minus the angle, same
+ *              scale): the gradient with respect to the input.
+ * T = 0 does nothing.  Any alignment of the element type is taken; 16-byte
+ * aligned rows are faster.  No workspace. */
+ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const ddtree_rows* k,
+                          const ddtree_rows* k_out, int dtype, int T, int D, const int32_t* pos,
+                          const ddtree_rotary* rot, int inverse, void* stream);
+
+/* Appends T tokens' keys and values to a paged cache, the keys rotated on the
+ * way, and rotates their queries in the same launch if they are given.
+ *   k, v       in, cache->Hkv heads each, of the cache's dtype and D
+ *              (1..DDTREE_MAX_ROPE_D).
+ *   seq, pos   int32 [T]: token t becomes position pos[t] of sequence seq[t]
+ *              (0..B-1, the rows of the page table) and is rotated for pos[t].
+ *              A negative pos marks a padding token: it is not written.  No two
+ *              tokens may name the same (seq, pos): that row would hold some
+ *              mixture of theirs.
+ *   rot        the rotation, or NULL for keys (and queries) as they are.
+ *   q, q_out   as in ddtree_rope; both NULL to leave queries out.
+ * A token whose sequence or position lies outside the table, or whose page
+ * outside the pool, is not written and recorded (its query is still rotated).
+ * The caller's sequence lengths are not changed.  T = 0 does nothing.  No
+ * workspace. */
+ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, int T,
+                                  const int32_t* seq, const int32_t* pos, int B,
+                                  const ddtree_paged_cache* cache, const ddtree_rotary* rot,
+                                  const ddtree_rows* q, const ddtree_rows* q_out, void* stream);
+
+/* ddtree_tree_attn with the prefix in a paged cache: the same formula, tree
+ * inputs and padding rules.
+ *   q, k_tree, v_tree  in; token b * (N + 1) + u is node u of sequence b.
+ *   dtype (the cache's) DDTREE_BF16 or DDTREE_FP16, D in {64, 128}, any
+ *   G = Hq / Hkv up to 128, page_size a power of two of at least 8; every
+ *   pointer 16-byte aligned, every stride a multiple of 8 elements and at least D.
+ *   N = 0 is plain decoding: one token a sequence.
+ * Outputs: out [B][N+1][Hq][D] in the cache's dtype and lse fp32 [B][N+1][Hq]
+ * (nullable), dense.  A node whose mask row leaves it no key (an empty prefix
+ * and no bit set) gets zeros and -inf, like the rows past n_nodes.
+ * A page whose number is outside the pool counts as keys and values of zero and
+ * is recorded; a prefix_len or n_nodes out of range leaves the
+ * sequence's outputs unwritten and is recorded.
+ * Softmax statistics, partial outputs and their merge are held in 32 bits; the
+ * softmax weights are rounded to the cache's dtype for the product with v.
+ * Workspace: ddtree_workspace_size(DDTREE_OP_TREE_ATTN_PAGED, ...). */
+ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_cache* cache,
+                                     const ddtree_rows* k_tree, const ddtree_rows* v_tree,
+                                     const int32_t* prefix_len, const int32_t* n_nodes,
+                                     const uint32_t* anc_mask, int B, int N, float scale,
+                                     void* out, float* lse, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* ddtree_commit into a paged cache.
+ *   k_tree, v_tree  in; token b * (N + 1) + u is node u of sequence b; D a
+ *                   multiple of 8, pointers 16-byte aligned, strides multiples
+ *                   of 8.
+ *   prefix_len [B]  read only: the model's other layers commit at the same
+ *                   prefix.  new_len [B] (nullable; not prefix_len itself)
+ *                   receives P_b + accept_len[b] + 1.
+ * A sequence whose path does not fit its max_pages * page_size positions, names
+ * a node outside [1, N] or needs a page outside the pool is left unchanged --
+ * new_len = P_b -- and recorded.  The pages that receive the path must belong to
+ * that sequence alone.  No workspace. */
+ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_rows* k_tree,
+                                  const ddtree_rows* v_tree, const int32_t* accept_len,
+                                  const int32_t* accepted_nodes, const int32_t* prefix_len,
+                                  int32_t* new_len, int B, int L, int N, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns DDTREE_OK, DDTREE_ERR_DEVICE (and the recorded code in
  * *detail when non-null: which kernel and what was wrong), or DDTREE_ERR_CUDA.
  * Code: high byte = kernel (1 top-K, 2 build, 3 tree attention, 4 accept,
- * 5 commit, 15 ddtree_selftest_wait), low byte = reason (1 bad prefix length,
- * 2 bad node count, 3 bad tree or path, 4 a bounded wait timed out, 5 bad
- * input, 6 internal plan). */
+ * 5 commit, 6 append, 15 ddtree_selftest_wait), low byte = reason (1 bad prefix
+ * length, 2 bad node count, 3 bad tree or path, 4 a bounded wait timed out, 5
+ * bad input, 6 internal plan, 7 a page number outside the pool). */
 ddtree_status ddtree_device_check(void* stream, uint32_t* detail);
 
 /* Failure-reporting self-test (diagnostics; the paper has no counterpart).
