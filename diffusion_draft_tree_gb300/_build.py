@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libddtree.so")
 SOURCES = ["api.cu", "topk.cu", "build.cu", "build_level.cu", "tree_attn.cu", "accept.cu",
-           "accept_path.cu", "commit.cu", "rotary.cu", "tree_attn_paged.cu"]
+           "accept_path.cu", "commit.cu", "rotary.cu", "tree_attn_paged.cu",
+           "tree_attn_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

@@ -45,10 +45,7 @@
 #include <queue>
 #include <map>
 
-#include <cudaTypedefs.h>
-
-#include "internal.h"
-#include "sm100.cuh"
+#include "tree_attn_common.cuh"
 
 #include "../../include/ddtree.h"
 
@@ -140,18 +137,6 @@ DDT_DEV bool softmax_bar_and(bool v) {
         : "r"((uint32_t)v)
         : "memory");
     return r != 0;
-}
-
-// A pair of weights or outputs rounded to the kernel's 16-bit type.
-template <bool F16>
-DDT_DEV uint32_t pack16(float lo, float hi) {
-    if constexpr (F16) {
-        uint32_t r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    } else {
-        return pack_bf16x2(lo, hi);
-    }
 }
 
 // On-chip merge of the paged forms: of the D / 4 four-column chunks, rank o of
@@ -1159,59 +1144,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
 // ------------------------------- host side ---------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
-    });
-    return fn;
-}
-
-struct MapDim {
-    uint64_t size, stride_bytes;  // (the innermost stride is the element's)
-    uint32_t box;
-};
-// A 128-byte-swizzled map of 16-bit elements, rank 3 or 4.
-template <int RANK>
-bool make_map(CUtensorMap* m, const void* ptr, const MapDim (&d)[RANK], bool f16 = false) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[RANK], strides[RANK - 1];
-    cuuint32_t box[RANK], estr[RANK];
-    for (int i = 0; i < RANK; ++i) {
-        dims[i] = d[i].size ? d[i].size : 1;
-        if (i) strides[i - 1] = d[i].stride_bytes;
-        box[i] = d[i].box;
-        estr[i] = 1;
-    }
-    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK,
-              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct Plan {
     int mtiles, mpairs, tps, smax, merge;
 };
-
-// Streaming multiprocessors of the current device (148 if the query fails).
-int num_sms() {
-    static int cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!cached[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
 
 // Per-unit tile counts bounding a plan: the longest prefix and the largest tree.
 struct Tiles {

@@ -6,11 +6,6 @@ namespace ddt {
 
 namespace {
 
-// The stride of a dimension of one entry is never used; its map needs a legal one.
-uint64_t stride_bytes(int64_t elements, int64_t size, uint64_t rowb) {
-    return size > 1 ? (uint64_t)elements * 2 : rowb;
-}
-
 template <int D, int MODE>
 cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     int dev = 0;
@@ -28,25 +23,12 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
                                    });
     const WsLayout wl = attn_layout(pl, a.B, Hkv, D, 4);
     const int G = Hq / Hkv, R = a.N + 1;
-    const uint64_t rowb = (uint64_t)D * 2, tokens = (uint64_t)a.B * R;
+    const uint64_t tokens = (uint64_t)a.B * R;
     constexpr bool f16 = MODE == kPagedFp16;
-    auto tree_map = [&](CUtensorMap* m, const RowsArg& r, uint32_t heads, uint32_t nodes) {
-        const MapDim d[3] = {{(uint64_t)D, 0, 64},
-                             {(uint64_t)r.heads, stride_bytes(r.hs, r.heads, rowb), heads},
-                             {tokens, stride_bytes(r.ts, tokens, rowb), nodes}};
-        return make_map(m, r.data, d, f16);
-    };
-    auto page_map = [&](CUtensorMap* m, const void* pages) {
-        const PagedArgs& c = a.cache;
-        const MapDim d[4] = {{(uint64_t)D, 0, 64},
-                             {(uint64_t)ps, stride_bytes(c.slot_stride, ps, rowb), (uint32_t)std::min(ps, BN)},
-                             {(uint64_t)Hkv, stride_bytes(c.head_stride, Hkv, rowb), 1},
-                             {(uint64_t)c.num_pages, stride_bytes(c.page_stride, c.num_pages, rowb), 1}};
-        return make_map(m, pages, d, f16);
-    };
     CUtensorMap mq, mkc, mvc, mkt, mvt;
-    if (!tree_map(&mq, a.q, G, BM / G) || !tree_map(&mkt, a.k_tree, 1, BN) ||
-        !tree_map(&mvt, a.v_tree, 1, BN) || !page_map(&mkc, a.cache.k) || !page_map(&mvc, a.cache.v))
+    if (!tree_map<D>(&mq, a.q, tokens, G, BM / G, f16) || !tree_map<D>(&mkt, a.k_tree, tokens, 1, BN, f16) ||
+        !tree_map<D>(&mvt, a.v_tree, tokens, 1, BN, f16) ||
+        !page_map<D>(&mkc, a.cache, a.cache.k, BN, f16) || !page_map<D>(&mvc, a.cache, a.cache.v, BN, f16))
         return cudaErrorInvalidValue;
     PagedParams p{};
     p.prefix_len = a.prefix_len;
@@ -82,6 +64,7 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t cache_cap) {
+    if (few_rows(B, N, Hq, Hkv, cache_cap)) return few_rows_workspace_bytes(B, N, Hq, Hkv, D);
     const Plan base = plan_base(N, Hq, Hkv);
     const long units = plan_units(base, B, Hkv);
     if (units < num_sms()) return 0;
@@ -89,6 +72,8 @@ size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t 
 }
 
 cudaError_t launch_tree_attn_paged(const PagedAttnArgs& a, cudaStream_t s) {
+    if (few_rows(a.B, a.N, a.q.heads, a.cache.Hkv, (int64_t)a.cache.max_pages * a.cache.page_size))
+        return launch_tree_attn_rows(a, s);
     const bool f16 = a.cache.dtype == 2;
     if (a.cache.D == 128)
         return f16 ? launch_mode<128, kPagedFp16>(a, s) : launch_mode<128, kPagedBf16>(a, s);

@@ -338,6 +338,16 @@ CASES = [
     ([1000], 200, 32, 2, 64, 64, BF16, False, None, False),         # G = 16
     ([40], 130, 100, 1, 128, 16, FP16, False, None, False),         # G = 100: a node a tile
     ([129], 1024, 4, 2, 128, 32, BF16, False, None, False),         # the largest tree
+    # few rows: 16, 32 and 64 of them, one over; two mask words; one long sequence
+    ([64, 0, 63, 65, 200], 3, 8, 2, 128, 16, BF16, False, None, False),
+    ([700, 5], 7, 8, 2, 64, 8, FP16, True, None, True),
+    ([333, 64], 15, 16, 4, 128, 64, BF16, False, None, False),
+    ([128, 1], 16, 16, 4, 128, 64, BF16, False, None, False),
+    ([90, 700], 63, 3, 3, 128, 32, FP16, False, None, False),
+    ([90, 700], 32, 1, 1, 64, 128, BF16, False, None, True),
+    ([20011], 0, 4, 1, 128, 16, BF16, False, None, False),
+    ([20011], 0, 40, 2, 64, 64, FP16, False, None, False),
+    ([0, 0, 0, 9000, 0], 4, 8, 1, 128, 32, BF16, False, None, False),
 ]
 
 
@@ -445,7 +455,8 @@ def test_attention_bad_lengths_leave_the_sequence(cuda_device, what, value, deta
     ref = _ref(c)
     c[what][0] = value
     out, lse = torch.full_like(c["q"], 5.0), torch.full(c["q"].shape[:3], 5.0, device="cuda")
-    ops.ddtree_tree_attn_paged(**c, out=out, lse=lse)
+    ops.ddtree_tree_attn_paged(**c, out=out, lse=lse,
+                               workspace=ops.paged_attn_workspace(c["q"], c["cache"]))
     with pytest.raises(ops.DDTreeError) as e:
         ops.ddtree_device_check()
     assert e.value.detail == detail
@@ -498,11 +509,13 @@ def test_attention_is_repeatable(cuda_device):
 def test_attention_python_refusals(cuda_device):
     c = _attn_case(15, [20, 9], 3, 8, 2, 128, 16, BF16)
     out, lse = torch.empty_like(c["q"]), torch.empty(c["q"].shape[:3], device="cuda")
-    ok = dict(c, out=out, lse=lse)
+    ok = dict(c, out=out, lse=lse, workspace=ops.paged_attn_workspace(c["q"], c["cache"]))
+    ops.ddtree_tree_attn_paged(**ok)
     for bad in (dict(q=c["q"].half()), dict(q=c["q"][:1]), dict(k_tree=c["k_tree"][:, :3]),
                 dict(prefix_len=c["prefix_len"].long()), dict(n_nodes=c["n_nodes"][:1]),
                 dict(anc_mask=c["anc_mask"][:, :3]), dict(out=out[:, :3]), dict(lse=lse.half()),
                 dict(out=out.cpu()), dict(workspace=torch.zeros(64, device="cuda")),
+                dict(workspace=None), dict(workspace=ok["workspace"][:256]),
                 dict(q=c["q"].transpose(0, 1)), dict(scale=-1.0)):
         with pytest.raises((ValueError, ops.DDTreeError)):
             ops.ddtree_tree_attn_paged(**(ok | bad))
