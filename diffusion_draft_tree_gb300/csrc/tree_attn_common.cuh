@@ -109,7 +109,7 @@ bool page_map(CUtensorMap* m, const PagedArgs& c, const void* pages, int rows, b
 // The kernel for few query rows (tree_attn_rows.cu): whether it takes a shape,
 // its workspace, its launch.
 bool few_rows(int B, int N, int Hq, int Hkv, int64_t cache_cap);
-size_t few_rows_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+size_t few_rows_workspace_bytes(int N, int Hq, int Hkv, int D);
 cudaError_t launch_tree_attn_rows(const PagedAttnArgs& a, cudaStream_t s);
 
 }  // namespace ddt

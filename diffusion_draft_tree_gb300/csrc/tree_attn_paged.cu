@@ -64,7 +64,7 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t cache_cap) {
-    if (few_rows(B, N, Hq, Hkv, cache_cap)) return few_rows_workspace_bytes(B, N, Hq, Hkv, D);
+    if (few_rows(B, N, Hq, Hkv, cache_cap)) return few_rows_workspace_bytes(N, Hq, Hkv, D);
     const Plan base = plan_base(N, Hq, Hkv);
     const long units = plan_units(base, B, Hkv);
     if (units < num_sms()) return 0;

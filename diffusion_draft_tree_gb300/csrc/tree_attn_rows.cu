@@ -9,8 +9,8 @@
 // the same number of bytes.  All key tiles (64 keys) of all units are one list;
 // each CTA takes an equal run of it, whatever the sequences' lengths, reading
 // the lengths itself.  A unit cut by a run's end leaves (m, l, O) in 32 bits in
-// the workspace, at most two a CTA, and the last of its CTAs to finish -- an
-// atomic ticket, nobody waits -- joins them in the list's order.
+// the workspace, at most two pieces a CTA, and a second kernel, whose launch
+// overlaps the first's end, joins each cut unit's pieces in the list's order.
 //
 // A CTA is one copy warp and four computing warps; two CTAs share an SM.  The
 // copy warp runs through the list ahead of them with TMA, pages and unit
@@ -32,7 +32,9 @@ constexpr int kWarps = 4;       // computing warps
 constexpr int kThreadsR = 32 * (kWarps + 1);
 constexpr int kMaxSeqs = 1024;  // sequences whose tile counts a CTA adds up
 constexpr int kFewRows = 32;    // rows of a unit, at most
-constexpr int kMinTiles = 2;    // tiles per CTA, at least
+// A batch of at most kSmallRuns tiles a CTA is cut at unit borders instead, where
+// runs of kMaxRun tiles suffice for that.
+constexpr int kSmallRuns = 16, kMinRun = 3, kMaxRun = 24;
 
 template <int D, int MB>
 struct CfgR {
@@ -51,8 +53,8 @@ struct ParamsR {
     const uint32_t* anc_mask;
     uint16_t* out;
     float* lse;
-    float* part;            // [CTA][2][rows][D + 2]: O, m, l
-    unsigned int* tickets;  // [B * Hkv]
+    float* part;  // [CTA][2][rows][D + 4]: O, m, l, padding to 16 bytes
+    int4* cut;    // [CTA]: the unit that is cut by the end of the CTA's run
     int64_t table_stride, cap;
     int B, N, Hq, Hkv, G, rows, num_pages, ps_log2;
     float scale_log2;
@@ -92,6 +94,22 @@ DDT_DEV uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) 
 // Named barrier over the computing warps.
 DDT_DEV void warps_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
+// One output value group: columns [4 c, 4 c + 4) of row r (of `row`, counted over
+// the whole output), from the sums over all keys.
+template <int D, bool F16>
+DDT_DEV void finish(const ParamsR& p, size_t row, int c, bool live, float4 v, float M, float L) {
+    live = live && L > 0.f;
+    const float inv = live ? 1.f / L : 0.f;
+    uint2 w = make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv));
+    if (!live) w = make_uint2(0, 0);
+    reinterpret_cast<uint2*>(p.out + row * D)[c] = w;
+    if (c == 0 && p.lse) p.lse[row] = live ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+// Row of the output that is row r of unit (b, g).
+DDT_DEV size_t out_row(const ParamsR& p, int b, int g, int r) {
+    return ((size_t)b * (p.N + 1) + r / p.G) * p.Hq + g * p.G + r % p.G;
+}
+
 // MB: 16-row blocks of query rows (1 or 2).  Warp w computes row block w % MB
 // against the 16-key groups w / MB, w / MB + 4 / MB, ... of every tile.
 template <int D, bool F16, int MB>
@@ -107,9 +125,10 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __shared__ int s_cum[kMaxSeqs + 1];  // key tiles of a KV head, summed over sequences
     __shared__ uint8_t s_rem[kMaxSeqs];  // keys of a sequence's last prefix tile (64: also none)
     __shared__ uint8_t s_nodes[kMaxSeqs];
+    __shared__ uint8_t s_pad[kMaxSeqs];  // tiles added to a unit to make its runs equal
+    __shared__ int s_chunk;
     __shared__ float2 s_ml[kWarps][16];
     __shared__ volatile int s_abort;
-    __shared__ bool s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u32 - smem_u32(smem_raw));
@@ -146,25 +165,55 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         s_nodes[b] = (uint8_t)n;
     }
     __syncthreads();
+    // Each CTA's run is `chunk` tiles.  A large batch is cut anywhere; in a small
+    // one, where crossing into another unit costs more than an uneven last run,
+    // units are padded to whole runs of the least length, at least kMinRun, for which
+    // the grid suffices.
     if (warp == 0) {
+        int sum = 0;
+        for (int b = lane; b < p.B; b += 32) sum += s_cum[b + 1];
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        const int64_t all = (int64_t)sum * p.Hkv;
+        int c = (int)((all + gridDim.x - 1) / gridDim.x);
+        bool small = false;
+        if (c <= kSmallRuns) {
+            int k = max(c, kMinRun);
+            for (; !small && k <= kMaxRun; ++k) {
+                int runs = 0;
+                for (int b = lane; b < p.B; b += 32) runs += (s_cum[b + 1] + k - 1) / k;
+                small = (int64_t)__reduce_add_sync(0xffffffffu, runs) * p.Hkv <= gridDim.x;
+            }
+            if (small) c = k - 1;
+        }
         int carry = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int v = b0 + lane < p.B ? s_cum[b0 + lane + 1] : 0;
+            const int t = b0 + lane < p.B ? s_cum[b0 + lane + 1] : 0;
+            const int pad = small ? (c - t % c) % c : 0;
+            int v = t + pad;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += up;
             }
-            if (b0 + lane < p.B) s_cum[b0 + lane + 1] = v + carry;
+            if (b0 + lane < p.B) {
+                s_cum[b0 + lane + 1] = v + carry;
+                s_pad[b0 + lane] = (uint8_t)pad;
+            }
             carry += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) s_cum[0] = 0;
+        if (lane == 0) {
+            s_cum[0] = 0;
+            s_chunk = c;
+        }
     }
     __syncthreads();
-    const int64_t total = (int64_t)s_cum[p.B] * p.Hkv;
-    const int64_t chunk = max((int64_t)kMinTiles, (total + gridDim.x - 1) / gridDim.x);
-    const int64_t t_begin = blockIdx.x * chunk, t_end = min(total, t_begin + chunk);
-    if (t_begin >= t_end) return;
+    const int64_t total = (int64_t)s_cum[p.B] * p.Hkv, chunk = s_chunk;
+    const int64_t t_begin = blockIdx.x * chunk;
+    int64_t t_end = min(total, t_begin + chunk);
+    if (t_begin >= t_end) {
+        if (tid == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
 
     // A place in the list: sequence, KV head, tile of the unit.
     struct Place {
@@ -181,10 +230,11 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         Place x;
         x.b = lo;
-        x.tiles = s_cum[lo + 1] - s_cum[lo];
+        const int span = s_cum[lo + 1] - s_cum[lo];
         const int64_t off = t - (int64_t)s_cum[lo] * p.Hkv;
-        x.g = (int)(off / x.tiles);
-        x.tile = (int)(off - (int64_t)x.g * x.tiles);
+        x.g = (int)(off / span);
+        x.tile = (int)(off - (int64_t)x.g * span);
+        x.tiles = span - s_pad[lo];
         return x;
     };
     auto next_unit = [&](Place& x) {
@@ -200,35 +250,55 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         s_abort = 1;
     };
     Place at = place_of(t_begin);
+    if (s_pad[at.b]) t_end = min(t_end, t_begin + at.tiles - at.tile);  // (the padding)
 
     if (warp == kWarps) {
         // ============================= copy warp =============================
         const int ps = 1 << p.ps_log2, box = min(ps, kTile), nb = kTile / box;
         const int i = lane & (nb - 1);  // this lane's box of a tile
-        int P = prefix_of(at);
-        // Page of this lane's box of a tile, -1 past the prefix; a number outside
-        // the pool becomes the pool's end, from where a copy reads zeros.
-        auto page_of = [&](const Place& x, int Px) {
-            const int key = x.tile * kTile + i * box;
-            if (key >= Px) return -1;
-            const int page = __ldg(&p.table[x.b * p.table_stride + (key >> p.ps_log2)]);
+        // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of its
+        // unit; the batch after that -- of this unit or the next -- is in flight.
+        // -1 past the prefix; a number outside the pool becomes the pool's end, from
+        // where a copy reads zeros.
+        struct Batch {
+            Place x;
+            int k;
+            int64_t left;  // tiles of the run from the unit's first (or the run's) tile on
+        };
+        auto ids_of = [&](const Batch& y) {
+            const int64_t key = ((int64_t)y.k * 32 + lane) * box;
+            if (key >= prefix_of(y.x)) return -1;
+            const int page = __ldg(&p.table[y.x.b * p.table_stride + (key >> p.ps_log2)]);
             if (page >= 0 && page < p.num_pages) return page;
             record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
             return p.num_pages;
         };
-        int page = page_of(at, P);
+        auto advance = [&](Batch& y) {
+            if (((int64_t)y.k + 1) * 32 * box < prefix_of(y.x)) {
+                ++y.k;
+            } else {
+                y.k = 0;
+                y.left -= y.x.tiles - y.x.tile;
+                if (y.left > 0) next_unit(y.x);
+            }
+        };
+        Batch ahead{at, (int)((int64_t)at.tile * nb / 32), t_end - t_begin};
+        int ids = ids_of(ahead), next_ids = -1;
+        advance(ahead);
+        if (ahead.left > 0) next_ids = ids_of(ahead);
         int units = 0, issued = 0;
         for (int64_t t = t_begin; t < t_end; ++t) {
             const int it = (int)(t - t_begin), s = it % NS;
-            Place nx = at;
-            int Pn = P, next = -1;
-            if (t + 1 < t_end) {  // the next tile's pages, in flight meanwhile
-                if (++nx.tile == nx.tiles) {
-                    next_unit(nx);
-                    Pn = prefix_of(nx);
+            if (t > t_begin) {
+                const bool same = ++at.tile < at.tiles;
+                if (!same) next_unit(at);
+                if (!same || (at.tile * nb % 32 == 0 && at.tile < at.tiles - 1)) {
+                    ids = next_ids;
+                    advance(ahead);
+                    if (ahead.left > 0) next_ids = ids_of(ahead);
                 }
-                next = page_of(nx, Pn);
             }
+            const int page = __shfl_sync(0xffffffffu, ids, (at.tile * nb + i) & 31);
             const bool first = t == t_begin || at.tile == 0, tree = at.tile == at.tiles - 1;
             const unsigned boxes = __ballot_sync(0xffffffffu, page >= 0 && lane < nb);
             bool ok = true;
@@ -264,16 +334,12 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                                 &bar_full[s], 64 * h, row, at.g, page);
                 }
             }
-            at = nx;
-            P = Pn;
-            page = next;
             issued = it + 1;
         }
         // (after a wait that gave up: no copy may land in memory given back)
         if (s_abort)
             for (int it = max(0, issued - NS); it < issued; ++it)
                 mbar_wait(&bar_full[it % NS], (it / NS) & 1, nullptr, 100000000ull);
-        pdl_trigger();
         return;
     }
 
@@ -297,7 +363,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         uint32_t qf[D / 16][4];
         // A wait that gives up ends the unit's products, not its barriers: the warps
-        // stay together, and tickets return to zero.
+        // stay together.
         bool ok = mbar_wait(&bar_qfull, units & 1, &s_abort);
         if (!ok) fail();
 #pragma unroll
@@ -425,24 +491,17 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // value (r, 8 j + e) of a warp's 16 rows, its groups of 8 permuted by the row
         // so that the 8 rows a warp stores at once do not share their banks
         auto so_at = [&](int w, int r, int j, int e) { return &so[(w * 16 + r) * D + ((j ^ (r & 7)) << 3) + e]; };
-        // rows of the unit as units of work: which CTAs hold its tiles
-        const int64_t u_begin = t - at.tile, u_end = u_begin + at.tiles;
-        const int64_t c_first = u_begin / chunk, c_last = (u_end - 1) / chunk;
-        const bool alone = c_first == c_last;
-        const int slot = u_begin > t_begin ? 1 : 0;
-        float* mine = p.part + ((size_t)blockIdx.x * 2 + slot) * p.rows * (D + 2);
-        auto row_at = [&](int r) {  // output row of the unit's row r
-            return ((size_t)at.b * R + r / p.G) * p.Hq + at.g * p.G + r % p.G;
-        };
-        auto finish = [&](int r, int c, float4 v, float M, float L) {
-            const bool live = r / p.G <= n && L > 0.f;
-            const float inv = live ? 1.f / L : 0.f;
-            uint2 w = make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv));
-            if (!live) w = make_uint2(0, 0);
-            reinterpret_cast<uint2*>(p.out + row_at(r) * D)[c] = w;
-            if (c == 0 && p.lse)
-                p.lse[row_at(r)] = live ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
-        };
+        // The CTAs that hold its tiles: alone, or this run's piece of several -- slot 1
+        // if it is the first, which leaves word of the unit for the second kernel.
+        const bool whole_unit = at.tile == 0 && left == at.tiles;
+        const bool first = at.tile == 0;
+        float* mine = p.part + ((size_t)blockIdx.x * 2 + (first ? 1 : 0)) * p.rows * (D + 4);
+        if (tid == 0 && t + left == t_end) {
+            const int64_t last_run = (t - at.tile + at.tiles - 1) / chunk;
+            p.cut[blockIdx.x] = first && !whole_unit
+                                    ? make_int4(at.b, at.g, (int)(last_run - blockIdx.x + 1), n)
+                                    : make_int4(0, 0, 0, 0);
+        }
         warps_bar();  // every warp has read its keys of the stage
 #pragma unroll 1
         for (int blk = 0; blk < MB; ++blk) {
@@ -475,87 +534,88 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     v.z = fmaf(f, a.z, v.z), v.w = fmaf(f, a.w, v.w);
                 }
                 const int row = blk * 16 + r;
-                if (alone) {
-                    finish(row, c, v, M, L);
+                if (whole_unit) {
+                    finish<D, F16>(p, out_row(p, at.b, at.g, row), c, row / p.G <= n, v, M, L);
                 } else {
-                    float* to = mine + row * (D + 2);
-                    *(float2*)&to[4 * c] = make_float2(v.x, v.y);  // (rows are 8-byte aligned)
-                    *(float2*)&to[4 * c + 2] = make_float2(v.z, v.w);
+                    float* to = mine + row * (D + 4);
+                    *(float4*)&to[4 * c] = v;
                     if (c == 0) *(float2*)&to[D] = make_float2(M, L);
                 }
             }
             if (blk + 1 < MB) warps_bar();
         }
-        if (!alone) __threadfence();
         fence_proxy_async_smem();
-        warps_bar();
+        __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[it % NS]);
-        if (!alone) {
-            if (tid == 0) {
-                s_last = ticket_is_last(&p.tickets[at.b * p.Hkv + at.g], (unsigned)(c_last - c_first + 1));
-            }
-            warps_bar();
-            if (s_last) {
-                // in the list's order, kBatch pieces in flight for kItems values a thread
-                constexpr int kItems = 4, kBatch = 4;
-                const int items = p.rows * (D / 4), np = (int)(c_last - c_first + 1);
-                const size_t piece = (size_t)p.rows * (D + 2);
-                for (int i0 = tid; i0 < items; i0 += kItems * 32 * kWarps) {
-                    float M[kItems], L[kItems];
-                    float4 v[kItems];
-#pragma unroll
-                    for (int q = 0; q < kItems; ++q) {
-                        M[q] = -INFINITY, L[q] = 0.f;
-                        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll 1
-                    for (int k0 = 0; k0 < np; k0 += kBatch) {
-                        float2 ml[kBatch][kItems], x[kBatch][kItems], y[kBatch][kItems];
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int64_t cta = c_first + k0 + k;
-                            const float* from = p.part + ((size_t)cta * 2 + (u_begin > cta * chunk ? 1 : 0)) * piece;
-#pragma unroll
-                            for (int q = 0; q < kItems; ++q) {
-                                const int i = i0 + q * 32 * kWarps, r = i / (D / 4), c = i % (D / 4);
-                                const bool there = k0 + k < np && i < items;
-                                const float* f = from + r * (D + 2);
-                                ml[k][q] = there ? __ldcg((const float2*)&f[D]) : make_float2(-INFINITY, 0.f);
-                                x[k][q] = there ? __ldcg((const float2*)&f[4 * c]) : make_float2(0.f, 0.f);
-                                y[k][q] = there ? __ldcg((const float2*)&f[4 * c + 2]) : make_float2(0.f, 0.f);
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < kItems; ++q) {
-                            float Mn = M[q];
-#pragma unroll
-                            for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k][q].x);
-                            const float ref = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M[q] - ref);
-                            v[q].x *= f, v[q].y *= f, v[q].z *= f, v[q].w *= f;
-                            L[q] *= f;
-                            M[q] = Mn;
-#pragma unroll
-                            for (int k = 0; k < kBatch; ++k) {
-                                const float h = fast_exp2(ml[k][q].x - ref);
-                                v[q].x = fmaf(h, x[k][q].x, v[q].x), v[q].y = fmaf(h, x[k][q].y, v[q].y);
-                                v[q].z = fmaf(h, y[k][q].x, v[q].z), v[q].w = fmaf(h, y[k][q].y, v[q].w);
-                                L[q] = fmaf(h, ml[k][q].y, L[q]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < kItems; ++q) {
-                        const int i = i0 + q * 32 * kWarps;
-                        if (i < items) finish(i / (D / 4), i % (D / 4), v[q], M[q], L[q]);
-                    }
-                }
-            }
-            warps_bar();  // (s_last is read before the next unit's)
-        }
         t += left;
         if (t < t_end) next_unit(at);
     }
     pdl_trigger();
+}
+
+// Joins the pieces of the units that run ends cut: block (c, y) takes rows 4 y ..
+// 4 y + 3 of the unit cut by the end of CTA c's run, whose pieces are slot 1 of c
+// and slot 0 of the CTAs after it.  A thread owns 4 columns of a row in every
+// fourth piece, kBatch pieces in flight; the four shares meet in shared memory:
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+template <int D, bool F16>
+__global__ void __launch_bounds__(4 * D) tree_attn_join_kernel(const __grid_constant__ ParamsR p) {
+    constexpr int kBatch = 4, kShares = 4;
+    __shared__ float4 s_v[kShares][D];
+    __shared__ float2 s_ml[kShares][4];
+    pdl_wait();
+    const int4 unit = p.cut[blockIdx.x];
+    if (unit.z == 0) return;
+    const int share = threadIdx.x / D, i = threadIdx.x % D;
+    const int r = blockIdx.y * 4 + i / (D / 4), c = i % (D / 4);
+    const size_t piece = (size_t)p.rows * (D + 4);
+    const float* from = p.part + (size_t)blockIdx.x * 2 * piece + (size_t)min(r, p.rows - 1) * (D + 4);
+    float M = -INFINITY, L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = share; k0 < unit.z; k0 += kBatch * kShares) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int s = k0 + k * kShares;
+            const float* f = from + (size_t)(2 * s + (s == 0 ? 1 : 0)) * piece;
+            ml[k] = s < unit.z ? __ldcg((const float2*)&f[D]) : make_float2(-INFINITY, 0.f);
+            x[k] = s < unit.z ? __ldcg((const float4*)&f[4 * c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
+        const float ref = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M - ref);
+        v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+        L *= f;
+        M = Mn;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float h = fast_exp2(ml[k].x - ref);
+            v.x = fmaf(h, x[k].x, v.x), v.y = fmaf(h, x[k].y, v.y);
+            v.z = fmaf(h, x[k].z, v.z), v.w = fmaf(h, x[k].w, v.w);
+            L = fmaf(h, ml[k].y, L);
+        }
+    }
+    s_v[share][i] = v;
+    if (c == 0) s_ml[share][i / (D / 4)] = make_float2(M, L);
+    __syncthreads();
+    if (share > 0 || r >= p.rows) return;
+#pragma unroll
+    for (int q = 0; q < kShares; ++q) M = fmaxf(M, s_ml[q][i / (D / 4)].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+    L = 0.f;
+#pragma unroll
+    for (int q = 0; q < kShares; ++q) {
+        const float2 ml = s_ml[q][i / (D / 4)];
+        const float4 x = s_v[q][i];
+        const float h = fast_exp2(ml.x - ref);
+        v.x = fmaf(h, x.x, v.x), v.y = fmaf(h, x.y, v.y);
+        v.z = fmaf(h, x.z, v.z), v.w = fmaf(h, x.w, v.w);
+        L = fmaf(h, ml.y, L);
+    }
+    finish<D, F16>(p, out_row(p, unit.x, unit.y, r), c, r / p.G <= unit.w, v, M, L);
 }
 
 template <int D, bool F16, int MB>
@@ -585,8 +645,9 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
     p.anc_mask = a.anc_mask;
     p.out = (uint16_t*)a.out;
     p.lse = a.lse;
-    p.tickets = (unsigned int*)a.ws;
-    p.part = (float*)((char*)a.ws + align_up((size_t)a.B * Hkv * 4, 256));
+    const int ctas = 2 * num_sms();
+    p.cut = (int4*)a.ws;
+    p.part = (float*)((char*)a.ws + align_up((size_t)ctas * sizeof(int4), 256));
     p.table_stride = c.table_stride;
     p.cap = (int64_t)c.max_pages * c.page_size;
     p.B = a.B, p.N = a.N, p.Hq = Hq, p.Hkv = Hkv, p.G = G, p.rows = R * G;
@@ -594,8 +655,10 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
     for (p.ps_log2 = 0; (1 << p.ps_log2) < c.page_size;) ++p.ps_log2;
     p.scale_log2 = a.scale * kLog2e;
     p.err = a.err;
-    return launch_pdl(tree_attn_rows_kernel<D, F16, MB>, dim3(2 * num_sms()), dim3(kThreadsR),
-                      (size_t)C::SMEM, s, mq, mkc, mvc, mkt, mvt, p);
+    if (const cudaError_t e = launch_pdl(tree_attn_rows_kernel<D, F16, MB>, dim3(ctas), dim3(kThreadsR),
+                                         (size_t)C::SMEM, s, mq, mkc, mvc, mkt, mvt, p))
+        return e;
+    return launch_pdl(tree_attn_join_kernel<D, F16>, dim3(ctas, (p.rows + 3) / 4), dim3(4 * D), 0, s, p);
 }
 
 template <int D, bool F16>
@@ -613,9 +676,10 @@ bool few_rows(int B, int N, int Hq, int Hkv, int64_t cache_cap) {
            B * (cache_cap / kTile + 2) <= INT32_MAX;
 }
 
-size_t few_rows_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+size_t few_rows_workspace_bytes(int N, int Hq, int Hkv, int D) {
     const size_t rows = (size_t)(N + 1) * (Hq / Hkv);
-    return align_up((size_t)B * Hkv * 4, 256) + (size_t)num_sms() * 4 * rows * (D + 2) * 4;
+    const size_t ctas = 2 * (size_t)num_sms();
+    return align_up(ctas * sizeof(int4), 256) + ctas * 2 * rows * (D + 4) * 4;
 }
 
 cudaError_t launch_tree_attn_rows(const PagedAttnArgs& a, cudaStream_t s) {
