@@ -183,7 +183,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ float2 s_ml[PAGED ? 2 * BM : 1];  // paged cluster merge: (m, l) of the rows
     __shared__ float2 s_ml1[BM];  // lone tile: (m, l) of the second group's key halves
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // (paged: known to be one number a warp, see the MMA issuer)
+    const int warp = PAGED ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid >> 5;
 
     // ---- set-up that reads no global memory (overlaps the previous kernel) -------
     if (tid == 0) {
@@ -357,21 +359,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 0) {
         // =========================== TMA producer ===========================
         if constexpr (PAGED) {
-            // A prefix tile is nb boxes of `box` rows, one page (or part of one)
-            // each; box i is lane i's, and lanes i + nb, i + 2 nb, ... issue its
-            // other copies: both 64-column slabs of K, then of V.
+            // A prefix tile is nb boxes of `box` rows, one page (or part of one) each.
+            // The warp keeps together and one lane issues (measured with pages of 16:
+            // a lane for each copy made the copies the slowest part of the kernel).
             const int ps = 1 << p.ps_log2, box = min(ps, BN), nb = BN / box;
-            const int i = lane & (nb - 1);
+            const uint32_t lead = elect_one();
             const int32_t* table = p.table + b * p.table_stride;
-            // Page of this lane's box of tile j; the pool's end, from where a copy
-            // reads zeros, for a box past the prefix or a number outside the pool.
-            auto page_of = [&](int j) {
-                const int key = (t_begin + j) * BN + i * box;
-                if (j >= nprefix || key >= P) return p.num_pages;
-                const int page = __ldg(&table[key >> p.ps_log2]);
-                if (page >= 0 && page < p.num_pages) return page;
-                record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-                return p.num_pages;
+            // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of the
+            // split, the batch after that in flight; nothing looks at them before a
+            // tile of theirs is due.
+            auto ids_of = [&](int k) {
+                const int x = k * 32 + lane, key = t_begin * BN + x * box;
+                return x < nprefix * nb && key < P ? __ldg(&table[key >> p.ps_log2]) : p.num_pages;
             };
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
@@ -382,26 +381,40 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                     b * R + u01);
                 }
             }
-            int page = page_of(0);
+            int ids = ids_of(0), next_ids = ids_of(1);
             for (int j = 0; j < nt; ++j) {
                 const int s = j % NS;
-                const int next = page_of(j + 1);  // in flight while the stage empties
-                bool ok = true;
-                if (lane == 0) {
-                    ok = mbar_wait(&bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort);
-                    if (ok) mbar_arrive_expect_tx(&bar_full[s], 2 * C::KV_BYTES);
-                    else fail();
+                if (j > 0 && (j * nb & 31) == 0) {
+                    ids = next_ids;
+                    next_ids = ids_of(j * nb / 32 + 1);
                 }
-                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                // (all lanes wait: one that polled for the others would leave the warp
+                // divided, which slowed every warp of its scheduler -- 3.2 to 4.1 ms on
+                // long_context_70b)
+                if (!mbar_wait(&bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort)) { fail(); break; }
+                if (lane == 0) mbar_arrive_expect_tx(&bar_full[s], 2 * C::KV_BYTES);
+                __syncwarp();
                 uint8_t* dk = sk + s * C::KV_BYTES;
                 uint8_t* dv = sv + s * C::KV_BYTES;
                 if (j < nprefix) {
-                    const int row = ((t_begin + j) * BN + i * box) & (ps - 1);
-                    for (int x = lane; x < nb * C::NH * 2; x += 32) {
-                        const int y = x / nb, h = y % C::NH;
-                        const bool v = y >= C::NH;
-                        tma_load_4d((v ? dv : dk) + h * kHalfBytes + i * box * 128,
-                                    v ? &tm_vc : &tm_kc, &bar_full[s], 64 * h, row, g, page);
+                    const int key0 = (t_begin + j) * BN;
+#pragma unroll 1
+                    for (int i = 0; i < nb; ++i) {
+                        // (from the pool's end a copy reads zeros: boxes past the prefix,
+                        // and pages outside the pool)
+                        int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
+                        const int key = key0 + i * box;
+                        if ((unsigned)page >= (unsigned)p.num_pages) {
+                            if (lane == 0 && key < P) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+                            page = p.num_pages;
+                        }
+                        const int row = key & (ps - 1);
+#pragma unroll
+                        for (int h = 0; h < C::NH; ++h) {
+                            const uint32_t to = h * kHalfBytes + i * box * 128;
+                            tma_load_4d_warp(lead, smem_u32(dk) + to, &tm_kc, &bar_full[s], 64 * h, row, g, page);
+                            tma_load_4d_warp(lead, smem_u32(dv) + to, &tm_vc, &bar_full[s], 64 * h, row, g, page);
+                        }
                     }
                 } else if (lane == 0) {
                     const int a0 = (tree_first + j - nprefix) * BN;
@@ -410,7 +423,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         tma_load_3d(dv + h * kHalfBytes, &tm_vt, &bar_full[s], 64 * h, g, b * R + a0);
                     }
                 }
-                page = next;
             }
         } else if (lane == 0) {
             mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::QT_BYTES);
@@ -443,7 +455,56 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        if (lane == 0) {
+        if constexpr (PAGED) {
+            // The whole warp runs the loop and one lane issues: per tile and query
+            // tile k, O_k += P_k V_j and then S_k = Q_k K_{j+1}^T (the same order as
+            // below), each product's descriptors a base plus constants.
+            constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
+            const uint32_t lead = elect_one();
+            const uint32_t idesc_qk = idesc_f32<F16>(BM, dual ? BN / 2 : BN, 0, 0);
+            constexpr uint32_t idesc_pv = idesc_f32<F16>(BM, D, 0, 1);
+            const uint64_t qd = smem_desc_sw128(smem_u32(sq), 16, 1024);
+            const uint64_t kd = smem_desc_sw128(smem_u32(sk), 16, 1024);
+            const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
+            const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
+            bool ok = mbar_wait(&bar_q, 0, &s_abort);
+            int sj = 0;  // stage of tile j
+#pragma unroll 1
+            for (int j = -1; ok && j < nt; ++j) {
+                const int sn = j < 0 || sj + 1 == NS ? 0 : sj + 1;  // ... of tile j + 1
+#pragma unroll 1
+                for (int k = 0; ok && k < (two ? 2 : 1); ++k) {
+                    if (j >= 0) {
+                        ok = mbar_wait(&bar_pfull[k], j & 1, &s_abort);
+                        tc_fence_after();
+                        const uint64_t b0 = vd + (uint32_t)(sj * (C::KV_BYTES >> 4)) + k * k_half;
+                        const uint32_t d0 = tmem + 256 + k * D, a0 = tmem + k * BN;
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk) {
+                            if (dual && kk >= BN / 32) break;  // 64 keys: P columns [0, 32)
+                            mma_bf16_ts_warp(lead, d0, a0 + p_col(kk), b0 + kk * (2048 >> 4), idesc_pv,
+                                             kk > 0 ? 1u : (uint32_t)(j > 0));
+                        }
+                        mma_commit_warp(lead, &bar_odone[k]);
+                        if (k == 1 || !two) mma_commit_warp(lead, &bar_empty[sj]);
+                    }
+                    if (ok && j + 1 < nt) {
+                        if (k == 0) ok = mbar_wait(&bar_full[sn], ((j + 1) / NS) & 1, &s_abort);
+                        tc_fence_after();
+                        const uint64_t a0 = qd + k * q_tile;
+                        const uint64_t b0 = kd + (uint32_t)(sn * (C::KV_BYTES >> 4)) + k * k_half;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                            mma_bf16_ss_warp(lead, tmem + k * BN, a0 + off, b0 + off, idesc_qk, kk > 0);
+                        }
+                        mma_commit_warp(lead, &bar_sfull[k]);
+                    }
+                }
+                sj = sn;
+            }
+            if (!ok) fail();
+        } else if (lane == 0) {
             constexpr uint32_t idesc_qk = idesc_f32<F16>(BM, BN, 0, 0);
             constexpr uint32_t idesc_qk_half = idesc_f32<F16>(BM, BN / 2, 0, 0);
             constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
@@ -556,21 +617,44 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // valid keys among the group's columns (a lone tile's group owns 64: its
             // other columns hold whatever the tensor memory held before)
             const int lim = min(lim_t - key0, ncol);
-            const bool full = !is_tree && lim >= ncol;
+            bool full = !is_tree && lim >= ncol;
+            if constexpr (PAGED) {
+                if (!full) {
+                    // scores of keys that the row does not see become -inf in place, and
+                    // the tile then goes the way of a whole one: one copy of that code
+#pragma unroll 1
+                    for (int c = 0; c < ncol / 32; ++c) {
+                        uint32_t t[32];
+                        tmem_ld32(tm_s + 32 * c, t);
+                        const int rem = lim - 32 * c, w = c + key0 / 32;
+                        uint32_t see = rem >= 32 ? ~0u : (rem <= 0 ? 0u : ((1u << rem) - 1u));
+                        if (is_tree) see &= w < 2 ? (w == 0 ? am[0] : am[1]) : (w == 2 ? am[2] : am[3]);
+                        tmem_ld_wait();
+                        tmem_ld_fence(t);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1u)) t[i] = 0xff800000u;
+                        tmem_st32(tm_s + 32 * c, t);
+                    }
+                    tmem_st_wait();
+                    if (is_tree && j + 1 < nt) fetch_mask(tree_first + j + 1 - nprefix);
+                    full = true;
+                }
+            }
             uint32_t vm[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int rem = lim - 32 * c;
                 vm[c] = rem >= 32 ? ~0u : (rem <= 0 ? 0u : ((1u << rem) - 1u));
             }
-            if (is_tree) {
+            if (!PAGED && is_tree) {
                 const bool hi = dual && k == 1;  // keys 64-127: ancestor words 2, 3
 #pragma unroll
                 for (int c = 0; c < 4; ++c) vm[c] &= (c < 2 && hi) ? am[c + 2] : am[c];
                 if (j + 1 < nt) fetch_mask(tree_first + j + 1 - nprefix);
             }
             float sum = 0.f;
-            if (full) {
+            if (PAGED || full) {
                 // ---- a whole prefix tile: both passes read S_k in 32-column
                 // quarters, the next quarter's TMEM load in flight while the
                 // current one is used ----
@@ -693,12 +777,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const float bq = ((m0 >> (2 * i + 1)) & 1u) ? fast_exp2(fmaf(__uint_as_float(t0[2 * i + 1]), sl2, neg)) : 0.f;
                     const float c = ((m1 >> (2 * i)) & 1u) ? fast_exp2(fmaf(__uint_as_float(t1[2 * i]), sl2, neg)) : 0.f;
                     const float d = ((m1 >> (2 * i + 1)) & 1u) ? fast_exp2(fmaf(__uint_as_float(t1[2 * i + 1]), sl2, neg)) : 0.f;
-                    pk[i] = pack16<F16>(a, bq);
-                    pk[16 + i] = pack16<F16>(c, d);
-                    // (paged: the 32-bit weights, as on whole tiles, so that the
-                    // logsumexp keeps 32 bits however few the keys)
-                    if constexpr (PAGED) sum += (a + bq) + (c + d);
-                    else sum += (__uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xffff0000u)) +
+                    pk[i] = pack_bf16x2(a, bq);
+                    pk[16 + i] = pack_bf16x2(c, d);
+                    sum += (__uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xffff0000u)) +
                            (__uint_as_float(pk[16 + i] << 16) + __uint_as_float(pk[16 + i] & 0xffff0000u));
                 }
                 if (half == 0) {

@@ -129,7 +129,8 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __shared__ int s_chunk;
     __shared__ float2 s_ml[kWarps][16];
     __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one number a warp
     const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u32 - smem_u32(smem_raw));
     uint8_t* sq = base + NS * C::STAGE;
@@ -255,11 +256,10 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (warp == kWarps) {
         // ============================= copy warp =============================
         const int ps = 1 << p.ps_log2, box = min(ps, kTile), nb = kTile / box;
-        const int i = lane & (nb - 1);  // this lane's box of a tile
+        const uint32_t lead = elect_one();
         // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of its
-        // unit; the batch after that -- of this unit or the next -- is in flight.
-        // -1 past the prefix; a number outside the pool becomes the pool's end, from
-        // where a copy reads zeros.
+        // unit; the batch after that -- of this unit or the next -- is in flight, and
+        // nothing looks at it before a tile of it is due.
         struct Batch {
             Place x;
             int k;
@@ -267,11 +267,8 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         };
         auto ids_of = [&](const Batch& y) {
             const int64_t key = ((int64_t)y.k * 32 + lane) * box;
-            if (key >= prefix_of(y.x)) return -1;
-            const int page = __ldg(&p.table[y.x.b * p.table_stride + (key >> p.ps_log2)]);
-            if (page >= 0 && page < p.num_pages) return page;
-            record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-            return p.num_pages;
+            return key < prefix_of(y.x) ? __ldg(&p.table[y.x.b * p.table_stride + (key >> p.ps_log2)])
+                                        : p.num_pages;
         };
         auto advance = [&](Batch& y) {
             if (((int64_t)y.k + 1) * 32 * box < prefix_of(y.x)) {
@@ -298,25 +295,24 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     if (ahead.left > 0) next_ids = ids_of(ahead);
                 }
             }
-            const int page = __shfl_sync(0xffffffffu, ids, (at.tile * nb + i) & 31);
             const bool first = t == t_begin || at.tile == 0, tree = at.tile == at.tiles - 1;
-            const unsigned boxes = __ballot_sync(0xffffffffu, page >= 0 && lane < nb);
-            bool ok = true;
-            if (lane == 0) {
-                if (first) {
-                    ok = mbar_wait(&bar_qempty, (units & 1) ^ 1, &s_abort);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&bar_qfull, NH * p.rows * 128);
-                        for (int h = 0; h < NH; ++h)
-                            tma_load_3d(sq + h * C::QSLAB, &tm_q, &bar_qfull, 64 * h, at.g * p.G, at.b * R);
-                    }
+            const int key0 = at.tile * kTile;
+            const int boxes = tree ? 0 : min(nb, (prefix_of(at) - key0 + box - 1) / box);
+            bool ok = true;  // (all lanes wait, so that the warp stays in one piece)
+            if (first) {
+                ok = mbar_wait(&bar_qempty, (units & 1) ^ 1, &s_abort);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&bar_qfull, NH * p.rows * 128);
+                    for (int h = 0; h < NH; ++h)
+                        tma_load_3d(sq + h * C::QSLAB, &tm_q, &bar_qfull, 64 * h, at.g * p.G, at.b * R);
                 }
-                ok = ok && mbar_wait(&bar_empty[s], ((it / NS) & 1) ^ 1, &s_abort);
-                if (ok) mbar_arrive_expect_tx(&bar_full[s], 2 * NH * 128 * (tree ? R : __popc(boxes) * box));
-                else fail();
+                ++units;
             }
-            units += first;
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            ok = ok && mbar_wait(&bar_empty[s], ((it / NS) & 1) ^ 1, &s_abort);
+            if (__any_sync(0xffffffffu, !ok)) { fail(); break; }
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bar_full[s], 2 * NH * 128 * (tree ? R : boxes * box));
+            __syncwarp();
             uint8_t* dk = base + s * C::STAGE;
             if (tree) {
                 if (lane < 2 * NH) {
@@ -325,13 +321,21 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     tma_load_3d(dk + (v ? C::KV : 0) + h * C::SLAB, v ? &tm_vt : &tm_kt, &bar_full[s],
                                 64 * h, at.g, at.b * R);
                 }
-            } else if (page >= 0) {
-                const int row = (at.tile * kTile + i * box) & (ps - 1);
-                for (int x = lane; x < nb * NH * 2; x += 32) {
-                    const int y = x / nb, h = y % NH;
-                    const bool v = y >= NH;
-                    tma_load_4d(dk + (v ? C::KV : 0) + h * C::SLAB + i * box * 128, v ? &tm_vc : &tm_kc,
-                                &bar_full[s], 64 * h, row, at.g, page);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < boxes; ++i) {
+                    int page = __shfl_sync(0xffffffffu, ids, (at.tile * nb + i) & 31);
+                    if ((unsigned)page >= (unsigned)p.num_pages) {
+                        if (lane == 0) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+                        page = p.num_pages;  // from the pool's end a copy reads zeros
+                    }
+                    const int row = (key0 + i * box) & (ps - 1);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        const uint32_t to = smem_u32(dk) + h * C::SLAB + i * box * 128;
+                        tma_load_4d_warp(lead, to, &tm_kc, &bar_full[s], 64 * h, row, at.g, page);
+                        tma_load_4d_warp(lead, to + C::KV, &tm_vc, &bar_full[s], 64 * h, row, at.g, page);
+                    }
                 }
             }
             issued = it + 1;
@@ -556,11 +560,11 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 // Joins the pieces of the units that run ends cut: block (c, y) takes rows 4 y ..
 // 4 y + 3 of the unit cut by the end of CTA c's run, whose pieces are slot 1 of c
 // and slot 0 of the CTAs after it.  A thread owns 4 columns of a row in every
-// fourth piece, kBatch pieces in flight; the four shares meet in shared memory:
+// second piece, kBatch pieces in flight; the two shares meet in shared memory:
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 template <int D, bool F16>
-__global__ void __launch_bounds__(4 * D) tree_attn_join_kernel(const __grid_constant__ ParamsR p) {
-    constexpr int kBatch = 4, kShares = 4;
+__global__ void __launch_bounds__(2 * D) tree_attn_join_kernel(const __grid_constant__ ParamsR p) {
+    constexpr int kBatch = 8, kShares = 2;
     __shared__ float4 s_v[kShares][D];
     __shared__ float2 s_ml[kShares][4];
     pdl_wait();
@@ -658,7 +662,7 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
     if (const cudaError_t e = launch_pdl(tree_attn_rows_kernel<D, F16, MB>, dim3(ctas), dim3(kThreadsR),
                                          (size_t)C::SMEM, s, mq, mkc, mvc, mkt, mvt, p))
         return e;
-    return launch_pdl(tree_attn_join_kernel<D, F16>, dim3(ctas, (p.rows + 3) / 4), dim3(4 * D), 0, s, p);
+    return launch_pdl(tree_attn_join_kernel<D, F16>, dim3(ctas, (p.rows + 3) / 4), dim3(2 * D), 0, s, p);
 }
 
 template <int D, bool F16>
