@@ -82,6 +82,15 @@ DDT_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c
         : "memory");
 }
 // ... and issued by the lane of a whole warp whose `lead` is set (elect_one).
+DDT_DEV void tma_load_3d_warp(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                              int c0, int c1, int c2) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(lead)
+        : "memory");
+}
 DDT_DEV void tma_load_4d_warp(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                               int c0, int c1, int c2, int c3) {
     asm volatile(

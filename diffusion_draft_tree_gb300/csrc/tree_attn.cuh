@@ -177,6 +177,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_full[NS], bar_empty[NS], bar_sfull[2],
         bar_pfull[2], bar_odone[2], bar_recv;
+    // (paged: the two above are K's; V has its own, see the copy warp)
+    __shared__ __align__(8) uint64_t bar_vfull[NS], bar_vempty[NS];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
@@ -193,6 +195,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], 1);
+            if constexpr (PAGED) {
+                mbar_init(&bar_vfull[s], 1);
+                mbar_init(&bar_vempty[s], 1);
+            }
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&bar_sfull[k], 1);
@@ -388,41 +394,47 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ids = next_ids;
                     next_ids = ids_of(j * nb / 32 + 1);
                 }
-                // (all lanes wait: one that polled for the others would leave the warp
-                // divided, which slowed every warp of its scheduler -- 3.2 to 4.1 ms on
-                // long_context_70b)
-                if (!mbar_wait(&bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort)) { fail(); break; }
-                if (lane == 0) mbar_arrive_expect_tx(&bar_full[s], 2 * C::KV_BYTES);
-                __syncwarp();
-                uint8_t* dk = sk + s * C::KV_BYTES;
-                uint8_t* dv = sv + s * C::KV_BYTES;
-                if (j < nprefix) {
-                    const int key0 = (t_begin + j) * BN;
+                // K and V of a stage come and go separately: K's half is free again as
+                // soon as its tile's scores are formed, so K runs a tile further ahead,
+                // and the scores wait for half the bytes.  (All lanes wait: one that
+                // polled for the others would leave the warp divided.)
+                bool ok = true;
 #pragma unroll 1
-                    for (int i = 0; i < nb; ++i) {
-                        // (from the pool's end a copy reads zeros: boxes past the prefix,
-                        // and pages outside the pool)
-                        int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
-                        const int key = key0 + i * box;
-                        if ((unsigned)page >= (unsigned)p.num_pages) {
-                            if (lane == 0 && key < P) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-                            page = p.num_pages;
-                        }
-                        const int row = key & (ps - 1);
+                for (int v = 0; v < 2; ++v) {
+                    const CUtensorMap* map = v ? &tm_vc : &tm_kc;
+                    uint64_t* full = v ? &bar_vfull[s] : &bar_full[s];
+                    const uint32_t to = smem_u32(v ? sv : sk) + s * C::KV_BYTES;
+                    ok = mbar_wait(v ? &bar_vempty[s] : &bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
+                    __syncwarp();
+                    if (j < nprefix) {
+                        const int key0 = (t_begin + j) * BN;
+#pragma unroll 1
+                        for (int i = 0; i < nb; ++i) {
+                            // (from the pool's end a copy reads zeros: boxes past the
+                            // prefix, and pages outside the pool)
+                            int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
+                            const int key = key0 + i * box;
+                            if ((unsigned)page >= (unsigned)p.num_pages) {
+                                if (lane == 0 && key < P) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+                                page = p.num_pages;
+                            }
+                            const int row = key & (ps - 1);
 #pragma unroll
-                        for (int h = 0; h < C::NH; ++h) {
-                            const uint32_t to = h * kHalfBytes + i * box * 128;
-                            tma_load_4d_warp(lead, smem_u32(dk) + to, &tm_kc, &bar_full[s], 64 * h, row, g, page);
-                            tma_load_4d_warp(lead, smem_u32(dv) + to, &tm_vc, &bar_full[s], 64 * h, row, g, page);
+                            for (int h = 0; h < C::NH; ++h)
+                                tma_load_4d_warp(lead, to + h * kHalfBytes + i * box * 128, map, full, 64 * h,
+                                                 row, g, page);
                         }
-                    }
-                } else if (lane == 0) {
-                    const int a0 = (tree_first + j - nprefix) * BN;
-                    for (int h = 0; h < C::NH; ++h) {
-                        tma_load_3d(dk + h * kHalfBytes, &tm_kt, &bar_full[s], 64 * h, g, b * R + a0);
-                        tma_load_3d(dv + h * kHalfBytes, &tm_vt, &bar_full[s], 64 * h, g, b * R + a0);
+                    } else {
+                        const int a0 = (tree_first + j - nprefix) * BN;
+#pragma unroll
+                        for (int h = 0; h < C::NH; ++h)
+                            tma_load_3d_warp(lead, to + h * kHalfBytes, v ? &tm_vt : &tm_kt, full, 64 * h, g,
+                                             b * R + a0);
                     }
                 }
+                if (!ok) { fail(); break; }
             }
         } else if (lane == 0) {
             mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::QT_BYTES);
@@ -476,6 +488,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int k = 0; ok && k < (two ? 2 : 1); ++k) {
                     if (j >= 0) {
                         ok = mbar_wait(&bar_pfull[k], j & 1, &s_abort);
+                        if (k == 0) ok = ok && mbar_wait(&bar_vfull[sj], (j / NS) & 1, &s_abort);
                         tc_fence_after();
                         const uint64_t b0 = vd + (uint32_t)(sj * (C::KV_BYTES >> 4)) + k * k_half;
                         const uint32_t d0 = tmem + 256 + k * D, a0 = tmem + k * BN;
@@ -486,7 +499,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                              kk > 0 ? 1u : (uint32_t)(j > 0));
                         }
                         mma_commit_warp(lead, &bar_odone[k]);
-                        if (k == 1 || !two) mma_commit_warp(lead, &bar_empty[sj]);
+                        if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[sj]);
                     }
                     if (ok && j + 1 < nt) {
                         if (k == 0) ok = mbar_wait(&bar_full[sn], ((j + 1) / NS) & 1, &s_abort);
@@ -499,6 +512,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             mma_bf16_ss_warp(lead, tmem + k * BN, a0 + off, b0 + off, idesc_qk, kk > 0);
                         }
                         mma_commit_warp(lead, &bar_sfull[k]);
+                        if (k == 1 || !two) mma_commit_warp(lead, &bar_empty[sn]);
                     }
                 }
                 sj = sn;
@@ -801,7 +815,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (k == 0 && !key_r_valid) {
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
-                if (!mbar_wait(&bar_full[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
+                if (!mbar_wait(PAGED ? &bar_vfull[s] : &bar_full[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
                 uint8_t* vrow = sv + s * C::KV_BYTES + r * 128;
 #pragma unroll
                 for (int h = 0; h < C::NH; ++h)
