@@ -373,10 +373,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int32_t* table = p.table + b * p.table_stride;
             // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of the
             // split, the batch after that in flight; nothing looks at them before a
-            // tile of theirs is due.
+            // tile of theirs is due.  From the pool's end a copy reads zeros: boxes
+            // past the prefix, and pages outside the pool.
             auto ids_of = [&](int k) {
                 const int x = k * 32 + lane, key = t_begin * BN + x * box;
                 return x < nprefix * nb && key < P ? __ldg(&table[key >> p.ps_log2]) : p.num_pages;
+            };
+            auto checked = [&](int page, int k) {
+                if ((unsigned)page < (unsigned)p.num_pages) return page;
+                const int x = k * 32 + lane;
+                if (x < nprefix * nb && t_begin * BN + x * box < P)
+                    record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+                return p.num_pages;
             };
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
@@ -387,11 +395,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                     b * R + u01);
                 }
             }
-            int ids = ids_of(0), next_ids = ids_of(1);
+            int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
             for (int j = 0; j < nt; ++j) {
                 const int s = j % NS;
                 if (j > 0 && (j * nb & 31) == 0) {
-                    ids = next_ids;
+                    ids = checked(next_ids, j * nb / 32);
                     next_ids = ids_of(j * nb / 32 + 1);
                 }
                 // K and V of a stage come and go separately: K's half is free again as
@@ -410,17 +418,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     __syncwarp();
                     if (j < nprefix) {
                         const int key0 = (t_begin + j) * BN;
-#pragma unroll 1
+#pragma unroll 4
                         for (int i = 0; i < nb; ++i) {
-                            // (from the pool's end a copy reads zeros: boxes past the
-                            // prefix, and pages outside the pool)
-                            int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
-                            const int key = key0 + i * box;
-                            if ((unsigned)page >= (unsigned)p.num_pages) {
-                                if (lane == 0 && key < P) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-                                page = p.num_pages;
-                            }
-                            const int row = key & (ps - 1);
+                            const int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
+                            const int row = (key0 + i * box) & (ps - 1);
 #pragma unroll
                             for (int h = 0; h < C::NH; ++h)
                                 tma_load_4d_warp(lead, to + h * kHalfBytes + i * box * 128, map, full, 64 * h,

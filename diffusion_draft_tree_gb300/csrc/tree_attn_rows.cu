@@ -259,7 +259,8 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint32_t lead = elect_one();
         // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of its
         // unit; the batch after that -- of this unit or the next -- is in flight, and
-        // nothing looks at it before a tile of it is due.
+        // nothing looks at it before a tile of it is due.  From the pool's end a copy
+        // reads zeros: pages outside the pool.
         struct Batch {
             Place x;
             int k;
@@ -269,6 +270,12 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int64_t key = ((int64_t)y.k * 32 + lane) * box;
             return key < prefix_of(y.x) ? __ldg(&p.table[y.x.b * p.table_stride + (key >> p.ps_log2)])
                                         : p.num_pages;
+        };
+        auto checked = [&](int page, const Batch& y) {
+            if ((unsigned)page < (unsigned)p.num_pages) return page;
+            if (((int64_t)y.k * 32 + lane) * box < prefix_of(y.x))
+                record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+            return p.num_pages;
         };
         auto advance = [&](Batch& y) {
             if (((int64_t)y.k + 1) * 32 * box < prefix_of(y.x)) {
@@ -280,7 +287,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
         };
         Batch ahead{at, (int)((int64_t)at.tile * nb / 32), t_end - t_begin};
-        int ids = ids_of(ahead), next_ids = -1;
+        int ids = checked(ids_of(ahead), ahead), next_ids = -1;
         advance(ahead);
         if (ahead.left > 0) next_ids = ids_of(ahead);
         int units = 0, issued = 0;
@@ -290,7 +297,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const bool same = ++at.tile < at.tiles;
                 if (!same) next_unit(at);
                 if (!same || (at.tile * nb % 32 == 0 && at.tile < at.tiles - 1)) {
-                    ids = next_ids;
+                    ids = checked(next_ids, ahead);
                     advance(ahead);
                     if (ahead.left > 0) next_ids = ids_of(ahead);
                 }
@@ -322,13 +329,9 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                                 64 * h, at.g, at.b * R);
                 }
             } else {
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < boxes; ++i) {
-                    int page = __shfl_sync(0xffffffffu, ids, (at.tile * nb + i) & 31);
-                    if ((unsigned)page >= (unsigned)p.num_pages) {
-                        if (lane == 0) record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-                        page = p.num_pages;  // from the pool's end a copy reads zeros
-                    }
+                    const int page = __shfl_sync(0xffffffffu, ids, (at.tile * nb + i) & 31);
                     const int row = (key0 + i * box) & (ps - 1);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
