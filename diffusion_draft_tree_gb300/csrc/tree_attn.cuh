@@ -122,7 +122,8 @@ struct PagedParams : Params {
     const int32_t* table;  // [B][table_stride] page numbers
     int64_t table_stride;
     int num_pages, ps_log2;  // pages of the pool; log2(positions per page)
-    int npt;                 // nodes per query tile, floor(BM / G)
+    int npt;                 // nodes per query tile, at most BM / G
+    int single;              // a unit is one query tile, not a pair
 };
 
 // Named barrier over the 256 softmax threads (both query tiles).
@@ -305,9 +306,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     const int rows_used = nodes_per_tile * G;  // of a tile's 128 (all of them if dense)
     const int splits = (npt + ntt + tps - 1) / tps;
-    const int mt0 = 2 * mpair, mt1 = mt0 + 1;
+    int mt0 = 2 * mpair, mt1 = mt0 + 1;
+    bool tile1 = mt1 < p.mtiles;                // the second tile exists
+    if constexpr (PAGED) {
+        if (p.single) mt0 = mpair, mt1 = mt0 + 1, tile1 = false;  // one tile a unit
+    }
     const int u00 = mt0 * nodes_per_tile, u01 = mt1 * nodes_per_tile;
-    const bool tile1 = mt1 < p.mtiles;          // the second tile exists
     const bool has1 = tile1 && (u01 <= n);      // ... and holds a live node
     // The last query tile of an odd count (R G = 128 m + G r, e.g. N + 1 nodes with
     // N a power of two) is alone: both softmax groups then work on it, each on
@@ -1342,6 +1346,44 @@ Plan plan_few(const Plan& base, Tiles t, long units, int sms, Active active) {
     pl.smax = (T + pl.tps - 1) / pl.tps;
     pl.merge = pl.smax > 1 ? kMergeCluster : kMergeNone;
     return pl;
+}
+
+// Few units, paged: what a CTA's exchange with its cluster costs grows with its
+// rows (32-bit partials through distributed shared memory, which passes about 25
+// GB/s a CTA), so rows are spread over idle SMs too: a unit may be a single query
+// tile, and tiles may hold fewer nodes than fit.  Every number of tiles up to
+// four times the least and every cluster size that is resident at once is
+// scored, in microseconds measured on GB300 (D = 128): a key tile takes a pair
+// of query tiles 1.5, a single one 1.2; an exchange 1 and 0.035 a row.
+struct PagedPlan : Plan {
+    int npt, single;
+};
+template <typename Active>
+PagedPlan plan_paged_few(int B, int N, int G, int Hkv, Tiles t, int sms, Active active) {
+    const int R = N + 1, T = t.prefix + t.tree, most = BM / G, least = (R + most - 1) / most;
+    PagedPlan best{};
+    double best_cost = 1e30;
+    for (int tiles = least; tiles <= std::min(R, 4 * least); ++tiles) {
+        if (tiles > least && (long)B * Hkv * tiles > sms) break;  // (single from here on)
+        const int npt = (R + tiles - 1) / tiles;
+        if ((R + npt - 1) / npt != tiles) continue;
+        for (int single = tiles == least && tiles > 1 ? 0 : 1; single < 2; ++single) {
+            const int per_head = single ? tiles : (tiles + 1) / 2;
+            const long units = (long)B * Hkv * per_head;
+            for (int S = 1; S <= kMaxSplits && units * S <= sms; ++S) {
+                const int per_cta = (T + S - 1) / S;
+                if (S > 1 && (per_cta < 2 || active(S) < units)) continue;
+                const int rows = npt * G * (single ? 1 : 2);
+                const double cost = per_cta * (single ? 1.2 : 1.5) + (S > 1 ? 1.0 + 0.035 * rows : 0.0);
+                if (cost >= best_cost) continue;
+                best_cost = cost;
+                best.mtiles = tiles, best.mpairs = per_head, best.smax = S, best.tps = per_cta;
+                best.merge = S > 1 ? kMergeCluster : kMergeNone;
+                best.npt = npt, best.single = single;
+            }
+        }
+    }
+    return best;
 }
 
 struct WsLayout {

@@ -13,20 +13,25 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     if (const cudaError_t e = prepare_kernel<D, MODE>(dev)) return e;
     const int Hq = a.q.heads, Hkv = a.cache.Hkv, ps = a.cache.page_size;
     const int64_t cap = (int64_t)a.cache.max_pages * ps;
+    const int G = Hq / Hkv, R = a.N + 1;
     const Plan base = plan_base(a.N, Hq, Hkv);
     const Tiles t = max_tiles(a.N, cap);
     const long units = plan_units(base, a.B, Hkv);
     const int sms = num_sms();
-    const Plan pl = units >= sms ? plan_many(base, t, units, sms)
-                                 : plan_few(base, t, units, sms, [&](int S) {
-                                       return merge_fits<D>(S) ? active_clusters<D, MODE>(dev, S) : 0;
-                                   });
+    PagedPlan pl{};
+    if (units >= sms) {
+        (Plan&)pl = plan_many(base, t, units, sms);
+        pl.npt = BM / G;
+    } else {
+        pl = plan_paged_few(a.B, a.N, G, Hkv, t, sms, [&](int S) {
+            return merge_fits<D>(S) ? active_clusters<D, MODE>(dev, S) : 0;
+        });
+    }
     const WsLayout wl = attn_layout(pl, a.B, Hkv, D, 4);
-    const int G = Hq / Hkv, R = a.N + 1;
     const uint64_t tokens = (uint64_t)a.B * R;
     constexpr bool f16 = MODE == kPagedFp16;
     CUtensorMap mq, mkc, mvc, mkt, mvt;
-    if (!tree_map<D>(&mq, a.q, tokens, G, BM / G, f16) || !tree_map<D>(&mkt, a.k_tree, tokens, 1, BN, f16) ||
+    if (!tree_map<D>(&mq, a.q, tokens, G, pl.npt, f16) || !tree_map<D>(&mkt, a.k_tree, tokens, 1, BN, f16) ||
         !tree_map<D>(&mvt, a.v_tree, tokens, 1, BN, f16) ||
         !page_map<D>(&mkc, a.cache, a.cache.k, BN, f16) || !page_map<D>(&mvc, a.cache, a.cache.v, BN, f16))
         return cudaErrorInvalidValue;
@@ -52,8 +57,9 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     p.table_stride = a.cache.table_stride;
     p.num_pages = a.cache.num_pages;
     for (p.ps_log2 = 0; (1 << p.ps_log2) < ps;) ++p.ps_log2;
-    p.npt = BM / G;
-    const long grid = units * pl.smax;
+    p.npt = pl.npt;
+    p.single = pl.single;
+    const long grid = plan_units(pl, a.B, Hkv) * pl.smax;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     return launch_pdl_cluster(tree_attn_kernel<D, MODE>, dim3((unsigned)grid), dim3(kThreads),
                               (size_t)Cfg<D>::SMEM, s,

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -30,26 +31,10 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error
           4: "kernel recorded bad device data or a timeout"}
 
 
-class _Rows(ctypes.Structure):
-    """ddtree_rows."""
-    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int32),
-                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class _Cache(ctypes.Structure):
-    """ddtree_paged_cache."""
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
-                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
-                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("slot_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
-                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64)]
-
-
-class _Rotary(ctypes.Structure):
-    """ddtree_rotary."""
-    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+# The structs of include/ddtree.h, packed with the platform's own alignment.
+_pack_rows = struct.Struct("@Piqq").pack              # ddtree_rows
+_pack_cache = struct.Struct("@PPiiiiiqqqPiq").pack    # ddtree_paged_cache
+_pack_rotary = struct.Struct("@Piif").pack            # ddtree_rotary
 
 
 class DDTreeError(RuntimeError):
@@ -84,7 +69,7 @@ def _load() -> ctypes.CDLL:
     lib.ddtree_accept_path.argtypes = [P, i32, i64, P, P, P, i32, i32, i32, i32, f32, u64, u64,
                                        P, P, P, P, P, P]
     lib.ddtree_topk_noalloc.argtypes = [P, i32, i32, i32, i64, i32, P, P, P, P]
-    rows, cache, rotary = (ctypes.POINTER(c) for c in (_Rows, _Cache, _Rotary))
+    rows = cache = rotary = P  # packed bytes
     f64 = ctypes.c_double
     lib.ddtree_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
                                             ctypes.POINTER(f64), ctypes.POINTER(f32)]
@@ -340,26 +325,28 @@ def _rows(t: torch.Tensor, name: str, D: int, dtype, index: int):
     """ddtree_rows of a [tokens][heads][D] or [B][nodes][heads][D] tensor, and its
     number of tokens."""
     shape, st = t.shape, t.stride()
-    if len(shape) == 4:
-        if shape[1] == 1:
-            ts = st[0]
-        elif shape[0] == 1 or st[0] == shape[1] * st[1]:
-            ts = st[1]
-        else:
-            raise ValueError(f"{name}: the strides of its first two dimensions do not merge")
-        tokens, heads, hs = shape[0] * shape[1], shape[2], st[2]
-    elif len(shape) == 3:
-        tokens, heads, ts, hs = shape[0], shape[1], st[0], st[1]
-    else:
-        raise ValueError(f"{name} must be [tokens][heads][D] or [B][nodes][heads][D]")
     if t.get_device() != index or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}, got {t.dtype} on "
                          f"{t.device}")
-    if shape[-1] != D or (st[-1] != 1 and D > 1):
+    if len(shape) == 3:
+        tokens, heads, width = shape
+        ts, hs, one = st
+    elif len(shape) == 4:
+        outer, inner, heads, width = shape
+        tokens, ts, hs, one = outer * inner, st[1], st[2], st[3]
+        if inner == 1:
+            ts = st[0]
+        elif outer > 1 and st[0] != inner * ts:
+            raise ValueError(f"{name}: the strides of its first two dimensions do not merge")
+    else:
+        raise ValueError(f"{name} must be [tokens][heads][D] or [B][nodes][heads][D]")
+    if width != D or (one != 1 and D > 1):
         raise ValueError(f"{name} must end in {D} contiguous elements")
-    # (the stride of a dimension of one entry says nothing)
-    return _Rows(t.data_ptr(), heads, ts if tokens > 1 else max(ts, heads * hs, D),
-                 hs if heads > 1 else D), tokens
+    if heads == 1:  # (the stride of a dimension of one entry says nothing)
+        hs = D
+    if tokens == 1:
+        ts = max(ts, heads * hs, D)
+    return _pack_rows(t.data_ptr(), heads, ts, hs), tokens
 
 
 def _ints(t: torch.Tensor, name: str, shape: tuple, index: int):
@@ -371,19 +358,29 @@ def _ints(t: torch.Tensor, name: str, shape: tuple, index: int):
     return t.data_ptr()
 
 
-def _enqueue(name: str, index: int, stream, *args):
+# torch.cuda.current_stream() and current_device() cost more than a launch; these
+# are what they end in.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _enqueue(fn, name: str, index: int, stream, *args):
     """Calls the library with `index` as the current device and its stream last."""
     if stream is None:
-        stream = torch.cuda.current_stream(index)
+        raw = _raw_stream(index)
     elif stream.device.index != index:
         raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to "
                          f"cuda:{index}")
-    fn = getattr(lib, name)
-    if torch.cuda.current_device() == index:
-        _check(name, fn(*args, stream.cuda_stream))
+    else:
+        raw = stream.cuda_stream
+    if _current_device() == index:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(index):
-            _check(name, fn(*args, stream.cuda_stream))
+            status = fn(*args, raw)
+    if status:
+        raise DDTreeError(name, status)
 
 
 def _index(t: torch.Tensor) -> int:
@@ -428,7 +425,7 @@ class Rotary:
         signed = [x - (1 << 64) if x >> 63 else x for x in turns]
         self.turns = torch.tensor(signed, dtype=torch.int64).to(device)
         self._index = _index(self.turns)
-        self._c = _Rotary(self.turns.data_ptr(), rot_dim, int(self.interleaved), self.scale)
+        self._c = _pack_rotary(self.turns.data_ptr(), rot_dim, int(self.interleaved), self.scale)
 
 
 class PagedCache:
@@ -458,10 +455,10 @@ class PagedCache:
         if 0 in k_pages.shape or 0 in page_table.shape:
             raise ValueError("a paged cache needs at least one page, head, slot and table entry")
         st = [s if n > 1 else k_pages.shape[3] for n, s in zip(k_pages.shape, k_pages.stride())]
-        self._c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), _CODES[self.dtype],
-                         self.num_pages, self.page_size, self.Hkv, self.D, st[0], st[1], st[2],
-                         page_table.data_ptr(), self.max_pages,
-                         page_table.stride(0) if self.B > 1 else self.max_pages)
+        self._c = _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _CODES[self.dtype],
+                              self.num_pages, self.page_size, self.Hkv, self.D, *st[:3],
+                              page_table.data_ptr(), self.max_pages,
+                              page_table.stride(0) if self.B > 1 else self.max_pages)
 
 
 def ddtree_rope(q, k, pos, rotary: Rotary, q_out=None, k_out=None, inverse=False, stream=None):
@@ -491,7 +488,7 @@ def ddtree_rope(q, k, pos, rotary: Rotary, q_out=None, k_out=None, inverse=False
     elif k_out is not None:
         raise ValueError("k_out without k")
     at = _ints(pos, "pos", (T,) if pos.dim() == 1 else q.shape[:2], index)
-    _enqueue("ddtree_rope", index, stream, q_rows, q_to, k_rows, k_to, _CODES[dtype], T, D, at,
+    _enqueue(lib.ddtree_rope, "ddtree_rope", index, stream, q_rows, q_to, k_rows, k_to, _CODES[dtype], T, D, at,
              rotary._c, int(bool(inverse)))
 
 
@@ -528,7 +525,7 @@ def ddtree_append_paged(k, v, seq, pos, cache: PagedCache, rotary: Optional[Rota
     elif q_out is not None:
         raise ValueError("q_out without q")
     lead = (T,) if pos.dim() == 1 else k.shape[:2]
-    _enqueue("ddtree_append_paged", index, stream, k_rows, v_rows, T,
+    _enqueue(lib.ddtree_append_paged, "ddtree_append_paged", index, stream, k_rows, v_rows, T,
              _ints(seq, "seq", lead, index), _ints(pos, "pos", lead, index), cache.B, cache._c,
              None if rotary is None else rotary._c, q_rows, q_to)
 
@@ -566,7 +563,7 @@ def ddtree_tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_n
                                   workspace.dtype != torch.uint8 or
                                   not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    _enqueue("ddtree_tree_attn_paged", index, stream, q_rows, cache._c, k_rows, v_rows,
+    _enqueue(lib.ddtree_tree_attn_paged, "ddtree_tree_attn_paged", index, stream, q_rows, cache._c, k_rows, v_rows,
              _ints(prefix_len, "prefix_len", (B,), index), _ints(n_nodes, "n_nodes", (B,), index),
              _ints(anc_mask, "anc_mask", (B, R, (R + 31) // 32), index), B, R - 1,
              D ** -0.5 if scale is None else float(scale), out.data_ptr(),
@@ -600,7 +597,7 @@ def ddtree_commit_paged(cache: PagedCache, k_tree, v_tree, accept_len, accepted_
     k_rows, _ = _rows(k_tree, "k_tree", D, dtype, index)
     v_rows, _ = _rows(v_tree, "v_tree", D, dtype, index)
     L = accepted_nodes.shape[1]
-    _enqueue("ddtree_commit_paged", index, stream, cache._c, k_rows, v_rows,
+    _enqueue(lib.ddtree_commit_paged, "ddtree_commit_paged", index, stream, cache._c, k_rows, v_rows,
              _ints(accept_len, "accept_len", (B,), index),
              _ints(accepted_nodes, "accepted_nodes", (B, L), index),
              _ints(prefix_len, "prefix_len", (B,), index),

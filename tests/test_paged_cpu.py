@@ -85,7 +85,7 @@ def test_turns_are_fractions_of_a_turn():
 
 
 def _rows(data=0x10000, heads=2, ts=256, hs=128):
-    return ops._Rows(data, heads, ts, hs)
+    return ops._pack_rows(data, heads, ts, hs)
 
 
 def _cache(**kw):
@@ -93,11 +93,11 @@ def _cache(**kw):
              page_stride=4096, head_stride=2048, slot_stride=128, page_table=0x30000, max_pages=4,
              table_stride=4)
     d.update(kw)
-    return ops._Cache(*[d[n] for n, _ in ops._Cache._fields_])
+    return ops._pack_cache(*d.values())
 
 
 def _rot(turns=0x40000, rot_dim=128, scale=1.0):
-    return ops._Rotary(turns, rot_dim, 0, scale)
+    return ops._pack_rotary(turns, rot_dim, 0, scale)
 
 
 OK = P(0x50000)
