@@ -218,6 +218,20 @@ DDT_DEV int count_larger(const uint64_t* a, int n, uint64_t x) {
     return r;
 }
 
+// Streaming multiprocessors of the current device (148 if the query fails).
+inline int num_sms() {
+    static int cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if (!cached[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            n = 148;
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch.  Kernels are launched so that they may start
 // while the previous kernel on the stream is finishing: each one waits

@@ -9,15 +9,24 @@
 // reduction in floating point (a 32-bit product p f_j is off by 0.06 rad at a
 // million).  The top bits give the octant-centred remainder, sincospif the rest.
 //
-// HBM-bound: every row is read and written once.  A CTA takes kTok tokens: it
+// HBM-bound: every row is read and written once.  A CTA takes some tokens: it
 // fills their cosine / sine table (rot/2 entries each) in shared memory, so an
-// angle is computed once a token and serves every head, then its threads go
-// over (token, head, unit) items, a unit being two vectors -- the two halves of
-// a group of pairs, or neighbours -- of the widest type that the sizes and
-// addresses allow.  Each thread's first item is loaded before the table is
-// built, which takes the table off a small call's critical path.
+// angle is computed once a token and serves every head, then its threads go over
+// (token, head, unit) items, a unit being two vectors -- the two halves of a
+// group of pairs, or neighbours -- of the widest type that the sizes and
+// addresses allow, the next item's loads in flight while one is turned.  Each
+// thread's first item is loaded before the table is built, which takes the table
+// off a small call's critical path; few tokens are cut by heads over more CTAs.
+// CTAs are small (128 threads, 8 an SM) because each one's table and barrier
+// leave it idle for a while: 256 threads and one token a CTA took 81 us for 16384
+// tokens of 40 heads, D = 128, bf16, and 3.4 us for 65 tokens; this takes 63 us
+// (79 % of measured HBM) and 2.5.  A warp a token with its angles in registers
+// and no table took 68 us (the angles are then computed once every 4 heads), two
+// items in flight 70 (registers, so fewer CTAs).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -26,9 +35,11 @@ namespace ddt {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = 4;     // tokens per CTA, at most
-constexpr int kMaxPairs = 256;  // rot / 2, at most (D <= 512)
+constexpr int kThreads = 128;
+constexpr int kMaxTok = 16;        // tokens per CTA, at most
+constexpr int kTable = 2048;       // pairs of a CTA's tokens, at most
+constexpr int kPasses = 8;         // rounds of a CTA's threads over its items, about
+constexpr int kFill = 16;          // CTAs per SM that fill the GPU
 
 template <typename T> DDT_DEV float to_f(T x);
 template <> DDT_DEV float to_f<float>(float x) { return x; }
@@ -55,6 +66,7 @@ struct Params {
     int units;    // two-vector units per head
     int ru;       // ... of which rotated
     int heads;    // q, k and v heads of a token
+    int chunk;    // ... of which a CTA takes
     int inplace;  // bit 0: q, bit 1: k (untouched parts are skipped)
     int inverse;
     uint32_t* err;
@@ -78,20 +90,22 @@ DDT_DEV float2 cos_sin(uint64_t phase) {
 
 // V: elements per vector.  PAIRED: pairs (2j, 2j + 1), else (j, j + rot/2).
 template <typename T, int V, bool PAIRED, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const __grid_constant__ Params p) {
     using Vt = Vec<T, V>;
     // cos and sin of token t's pair V * u + e, at [t][e / 4][u][e % 4] (for V < 4:
     // [t][u][e]), so that a warp's 16-byte reads fall on different banks
-    __shared__ __align__(16) float s_cos[kMaxTok * kMaxPairs];
-    __shared__ __align__(16) float s_sin[kMaxTok * kMaxPairs];
+    extern __shared__ __align__(16) float s_cos[];
+    float* s_sin = s_cos + p.tok * (p.rot / 2);
     __shared__ int64_t s_dst[kMaxTok];  // page * page_stride + slot * slot_stride, or -1
     __shared__ int32_t s_pos[kMaxTok];
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tok;
     const int nt = min(p.tok, p.T - t0);
-    const int units = p.units, per_pass = kThreads / units;  // heads of a pass
-    const int u = tid % units;
-    const int items = nt * p.heads;  // (token, head)
+    // (a head of more units than threads is cut along blockIdx.z)
+    const int per = min(p.units, kThreads), per_pass = kThreads / per;  // heads of a pass
+    const int u = blockIdx.z * kThreads + tid % per;
+    const int h_first = blockIdx.y * p.chunk, heads = min(p.chunk, p.heads - h_first);
+    const int items = nt * heads;  // (token, head of this CTA's)
     const bool rotated = u < p.ru;
     // the unit's two vectors (the second may lie past an odd tail)
     const int e0 = rotated ? (PAIRED ? 2 * V * u : V * u) : p.rot + 2 * V * (u - p.ru);
@@ -103,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         Vt a, b;
     };
     auto source = [&](int i) -> const T* {
-        const int t = i / p.heads, h = i - t * p.heads;
+        const int t = i / heads, h = h_first + i - t * heads;
         const int64_t tok = t0 + t;
         if (h < p.q.heads) return (const T*)p.q.data + tok * p.q.ts + h * p.q.hs;
         if (h < p.q.heads + p.k.heads)
@@ -115,9 +129,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         x.a = *(const Vt*)(s + e0);
         if (two) x.b = *(const Vt*)(s + e1);
     };
-    int i = tid / units < per_pass ? tid / units : items;
-    Item cur;
-    if (i < items) load(i, cur);
+    int i = tid / per < per_pass && u < p.units ? tid / per : items;
+    Item ahead;
+    if (i < items) load(i, ahead);
 
     // ---- the tokens' tables ----------------------------------------------------
     if (tid < nt) {
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         const int pos = p.pos[t0 + t];
         const float2 cs = cos_sin((uint64_t)(uint32_t)max(pos, 0) * p.turns[f]);
         const int un = f / V, e = f - un * V;
-        const int at = t * kMaxPairs + (V < 4 ? un * V + e : ((e >> 2) * p.ru + un) * 4 + (e & 3));
+        const int at = t * pairs + (V < 4 ? un * V + e : ((e >> 2) * p.ru + un) * 4 + (e & 3));
         s_cos[at] = cs.x * p.scale;
         s_sin[at] = (p.inverse ? -cs.y : cs.y) * p.scale;
     }
@@ -156,9 +170,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
     // ---- the items -------------------------------------------------------------
     for (; i < items; i += per_pass) {
-        Item x = cur;
-        if (i + per_pass < items) load(i + per_pass, cur);
-        const int t = i / p.heads, h = i - t * p.heads;
+        Item x = ahead;
+        if (i + per_pass < items) load(i + per_pass, ahead);
+        const int t = i / heads, h = h_first + i - t * heads;
         const int64_t tok = t0 + t;
         const int hk = h - p.q.heads, hv = hk - p.k.heads;
         T* dst;
@@ -176,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         }
         if (turn) {
             float c[V], s[V];
-            const float* tc = s_cos + t * kMaxPairs;
-            const float* ts = s_sin + t * kMaxPairs;
+            const float* tc = s_cos + t * pairs;
+            const float* ts = s_sin + t * pairs;
             if constexpr (V >= 4) {
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
@@ -216,9 +230,20 @@ template <typename T, int V, bool APPEND>
 cudaError_t launch_v(Params& p, bool paired, cudaStream_t s) {
     p.ru = p.rot / (2 * V);
     p.units = p.ru + (p.D - p.rot + 2 * V - 1) / (2 * V);
-    const dim3 grid((unsigned)((p.T + p.tok - 1) / p.tok));
-    return paired ? launch_pdl(rotary_kernel<T, V, true, APPEND>, grid, dim3(kThreads), 0, s, p)
-                  : launch_pdl(rotary_kernel<T, V, false, APPEND>, grid, dim3(kThreads), 0, s, p);
+    // Tokens of a CTA: enough for kPasses rounds of its threads, as long as the CTAs
+    // still fill the GPU; few tokens are cut by heads instead.
+    const int64_t fill = (int64_t)num_sms() * kFill, units = (int64_t)p.heads * p.units;
+    p.tok = 1;
+    while (p.tok < kMaxTok && p.tok * units < kPasses * kThreads && 2 * p.tok * (p.rot / 2) <= kTable &&
+           p.T / (2 * p.tok) >= fill)
+        p.tok *= 2;
+    const int64_t cuts = std::min((units + kThreads - 1) / kThreads, std::max<int64_t>(1, fill / p.T));
+    p.chunk = (int)((p.heads + cuts - 1) / cuts);
+    const dim3 grid((unsigned)((p.T + p.tok - 1) / p.tok), (unsigned)((p.heads + p.chunk - 1) / p.chunk),
+                    (unsigned)((p.units + kThreads - 1) / kThreads));
+    const size_t smem = (size_t)p.tok * p.rot * sizeof(float);
+    return paired ? launch_pdl(rotary_kernel<T, V, true, APPEND>, grid, dim3(kThreads), smem, s, p)
+                  : launch_pdl(rotary_kernel<T, V, false, APPEND>, grid, dim3(kThreads), smem, s, p);
 }
 
 // The widest vectors that sizes, strides and addresses allow: 16 bytes, 8, or
@@ -243,8 +268,6 @@ cudaError_t launch_t(Params& p, bool paired, cudaStream_t s) {
 
 template <bool APPEND>
 cudaError_t launch(Params& p, int dtype, bool paired, cudaStream_t s) {
-    // One token a CTA: measured against 2 and 4, see below.
-    p.tok = 1;
     if (dtype == 0) return launch_t<__nv_bfloat16, APPEND>(p, paired, s);
     if constexpr (!APPEND)  // a cache has no 32-bit form
         if (dtype == 1) return launch_t<float, APPEND>(p, paired, s);

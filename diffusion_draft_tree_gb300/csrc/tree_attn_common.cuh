@@ -62,20 +62,6 @@ bool make_map(CUtensorMap* m, const void* ptr, const MapDim (&d)[RANK], bool f16
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Streaming multiprocessors of the current device (148 if the query fails).
-int num_sms() {
-    static int cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!cached[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
 // The stride of a dimension of one entry is never used; its map needs a legal one.
 inline uint64_t stride_bytes(int64_t elements, uint64_t size, uint64_t rowb) {
     return size > 1 ? (uint64_t)elements * 2 : rowb;
