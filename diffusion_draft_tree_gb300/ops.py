@@ -34,7 +34,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error
 # The structs of include/ddtree.h, packed with the platform's own alignment.
 _pack_rows = struct.Struct("@Piqq").pack              # ddtree_rows
 _pack_cache = struct.Struct("@PPiiiiiqqqPiq").pack    # ddtree_paged_cache
-_pack_rotary = struct.Struct("@Piif").pack            # ddtree_rotary
+_pack_rotary = struct.Struct("@Piif4x").pack          # ddtree_rotary
 
 
 class DDTreeError(RuntimeError):
@@ -95,6 +95,8 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+from . import _ddtree  # noqa: E402  (built beside libddtree.so, which it uses)
 
 EXPORTED = ("ddtree_workspace_size", "ddtree_topk", "ddtree_build", "ddtree_build_heap",
             "ddtree_tree_attn", "ddtree_accept", "ddtree_device_check", "ddtree_last_cuda_error",
@@ -315,72 +317,21 @@ def accept(target_logits, tree: dict, L: int, temperature=0.0, seed=0, step=0, w
 # layout, a pool that interleaves keys and values.  Only the last dimension of a
 # tensor has to be contiguous.  Everything a call is given has to be on one
 # device, which need not be the current one; without `stream` it is enqueued on
-# that device's current stream.
+# that device's current stream.  The module _ddtree (csrc/binding.cpp) checks
+# and passes on the tensors.
 
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
 
 
-def _rows(t: torch.Tensor, name: str, D: int, dtype, index: int):
-    """ddtree_rows of a [tokens][heads][D] or [B][nodes][heads][D] tensor, and its
-    number of tokens."""
-    shape, st = t.shape, t.stride()
-    if t.get_device() != index or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}, got {t.dtype} on "
-                         f"{t.device}")
-    if len(shape) == 3:
-        tokens, heads, width = shape
-        ts, hs, one = st
-    elif len(shape) == 4:
-        outer, inner, heads, width = shape
-        tokens, ts, hs, one = outer * inner, st[1], st[2], st[3]
-        if inner == 1:
-            ts = st[0]
-        elif outer > 1 and st[0] != inner * ts:
-            raise ValueError(f"{name}: the strides of its first two dimensions do not merge")
-    else:
-        raise ValueError(f"{name} must be [tokens][heads][D] or [B][nodes][heads][D]")
-    if width != D or (one != 1 and D > 1):
-        raise ValueError(f"{name} must end in {D} contiguous elements")
-    if heads == 1:  # (the stride of a dimension of one entry says nothing)
-        hs = D
-    if tokens == 1:
-        ts = max(ts, heads * hs, D)
-    return _pack_rows(t.data_ptr(), heads, ts, hs), tokens
-
-
-def _ints(t: torch.Tensor, name: str, shape: tuple, index: int):
-    """Device pointer of a contiguous int32 tensor of the given shape."""
-    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != index or \
-            not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-# torch.cuda.current_stream() and current_device() cost more than a launch; these
-# are what they end in.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _enqueue(fn, name: str, index: int, stream, *args):
-    """Calls the library with `index` as the current device and its stream last."""
+def _raw(name: str, stream: Optional[torch.cuda.Stream], index: int):
+    """The stream's handle for _ddtree: None for the device's current stream."""
     if stream is None:
-        raw = _raw_stream(index)
-    elif stream.device.index != index:
+        return None
+    if stream.device.index != index:
         raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to "
                          f"cuda:{index}")
-    else:
-        raw = stream.cuda_stream
-    if _current_device() == index:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, raw)
-    if status:
-        raise DDTreeError(name, status)
+    return stream.cuda_stream
 
 
 def _index(t: torch.Tensor) -> int:
@@ -465,31 +416,12 @@ def ddtree_rope(q, k, pos, rotary: Rotary, q_out=None, k_out=None, inverse=False
     """Rotates q and, unless it is None, k ([tokens][heads][D] or
     [B][nodes][heads][D], bf16 / fp16 / fp32) for pos int32 [tokens] or
     [B][nodes]; in place where no output is given."""
-    index, D, dtype = _index(q), q.shape[-1], q.dtype
-    if dtype not in _CODES:
-        raise ValueError(f"q must be bfloat16, float16 or float32, got {dtype}")
-    if rotary._index != index:
-        raise ValueError("rotary is on another device than q")
-    q_rows, T = _rows(q, "q", D, dtype, index)
-    q_to, k_rows, k_to = q_rows, None, None
-    if q_out is not None:
-        q_to, _ = _rows(q_out, "q_out", D, dtype, index)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    if k is not None:
-        k_rows, Tk = _rows(k, "k", D, dtype, index)
-        k_to = k_rows
-        if Tk != T:
-            raise ValueError(f"k has {Tk} tokens, q {T}")
-        if k_out is not None:
-            k_to, _ = _rows(k_out, "k_out", D, dtype, index)
-            if k_out.shape != k.shape:
-                raise ValueError("k_out must have k's shape")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    at = _ints(pos, "pos", (T,) if pos.dim() == 1 else q.shape[:2], index)
-    _enqueue(lib.ddtree_rope, "ddtree_rope", index, stream, q_rows, q_to, k_rows, k_to, _CODES[dtype], T, D, at,
-             rotary._c, int(bool(inverse)))
+    if not q.is_cuda:
+        raise ValueError("ddtree kernels take CUDA tensors")
+    st = _ddtree.rope(q, k, pos, rotary._c, rotary._index, q_out, k_out, inverse,
+                      _raw("ddtree_rope", stream, rotary._index))
+    if st:
+        raise DDTreeError("ddtree_rope", st)
 
 
 def rope(q, k, pos, rotary: Rotary, inverse=False, stream=None):
@@ -505,29 +437,11 @@ def ddtree_append_paged(k, v, seq, pos, cache: PagedCache, rotary: Optional[Rota
     """Writes tokens' k (rotated for pos if a rotary is given) and v to positions
     pos of sequences seq of the cache (int32 [tokens]; a negative pos: not
     written), and rotates their queries q, in place unless q_out is given."""
-    index, D, dtype = cache._index, cache.D, cache.dtype
-    k_rows, T = _rows(k, "k", D, dtype, index)
-    v_rows, Tv = _rows(v, "v", D, dtype, index)
-    if Tv != T:
-        raise ValueError(f"v has {Tv} tokens, k {T}")
-    if rotary is not None and rotary._index != index:
-        raise ValueError("rotary is on another device than the cache")
-    q_rows = q_to = None
-    if q is not None:
-        q_rows, Tq = _rows(q, "q", D, dtype, index)
-        q_to = q_rows
-        if Tq != T:
-            raise ValueError(f"q has {Tq} tokens, k {T}")
-        if q_out is not None:
-            q_to, _ = _rows(q_out, "q_out", D, dtype, index)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    lead = (T,) if pos.dim() == 1 else k.shape[:2]
-    _enqueue(lib.ddtree_append_paged, "ddtree_append_paged", index, stream, k_rows, v_rows, T,
-             _ints(seq, "seq", lead, index), _ints(pos, "pos", lead, index), cache.B, cache._c,
-             None if rotary is None else rotary._c, q_rows, q_to)
+    turns, where = (None, None) if rotary is None else (rotary._c, rotary._index)
+    st = _ddtree.append_paged(cache._c, cache._index, cache.B, k, v, seq, pos, turns, where, q,
+                              q_out, _raw("ddtree_append_paged", stream, cache._index))
+    if st:
+        raise DDTreeError("ddtree_append_paged", st)
 
 
 def paged_attn_workspace(q, cache: PagedCache) -> torch.Tensor:
@@ -544,32 +458,11 @@ def ddtree_tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_n
     """q [B][N+1][Hq][D], k_tree / v_tree [B][N+1][Hkv][D], prefix_len and n_nodes
     [B], anc_mask int32 [B][N+1][W] -> out like q (contiguous), lse fp32
     [B][N+1][Hq]."""
-    index, D, dtype = cache._index, cache.D, cache.dtype
-    if q.dim() != 4 or k_tree.dim() != 4 or v_tree.dim() != 4:
-        raise ValueError("q, k_tree and v_tree must be [B][nodes][heads][D]")
-    B, R, Hq, _ = q.shape
-    if k_tree.shape[:2] != (B, R) or v_tree.shape[:2] != (B, R) or cache.B != B:
-        raise ValueError("q, k_tree, v_tree and the page table must agree in B and nodes")
-    q_rows, _ = _rows(q, "q", D, dtype, index)
-    k_rows, _ = _rows(k_tree, "k_tree", D, dtype, index)
-    v_rows, _ = _rows(v_tree, "v_tree", D, dtype, index)
-    if out.shape != q.shape or out.dtype != dtype or out.get_device() != index or \
-            not out.is_contiguous():
-        raise ValueError("out must be contiguous, with q's shape, type and device")
-    if lse is not None and (lse.shape != (B, R, Hq) or lse.dtype != torch.float32 or
-                            lse.get_device() != index or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [B][nodes][Hq] on q's device")
-    if workspace is not None and (workspace.get_device() != index or
-                                  workspace.dtype != torch.uint8 or
-                                  not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    _enqueue(lib.ddtree_tree_attn_paged, "ddtree_tree_attn_paged", index, stream, q_rows, cache._c, k_rows, v_rows,
-             _ints(prefix_len, "prefix_len", (B,), index), _ints(n_nodes, "n_nodes", (B,), index),
-             _ints(anc_mask, "anc_mask", (B, R, (R + 31) // 32), index), B, R - 1,
-             D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-             None if lse is None else lse.data_ptr(),
-             None if workspace is None else workspace.data_ptr(),
-             0 if workspace is None else workspace.numel())
+    st = _ddtree.tree_attn_paged(cache._c, cache._index, cache.B, q, k_tree, v_tree, prefix_len,
+                                 n_nodes, anc_mask, out, lse, scale, workspace,
+                                 _raw("ddtree_tree_attn_paged", stream, cache._index))
+    if st:
+        raise DDTreeError("ddtree_tree_attn_paged", st)
 
 
 def tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask,
@@ -589,17 +482,8 @@ def ddtree_commit_paged(cache: PagedCache, k_tree, v_tree, accept_len, accepted_
     """Writes the accepted path (root + accepted nodes, as ddtree_accept gives them)
     of k_tree / v_tree [B][N+1][Hkv][D] to positions prefix_len.. of the cache;
     prefix_len stays, new_len [B] receives prefix_len + accept_len + 1."""
-    index, D, dtype, B = cache._index, cache.D, cache.dtype, cache.B
-    if k_tree.dim() != 4 or k_tree.shape[0] != B or v_tree.shape != k_tree.shape:
-        raise ValueError("k_tree and v_tree must be [B][nodes][Hkv][D], B as the page table's")
-    if accepted_nodes.dim() != 2:
-        raise ValueError("accepted_nodes must be [B][L]")
-    k_rows, _ = _rows(k_tree, "k_tree", D, dtype, index)
-    v_rows, _ = _rows(v_tree, "v_tree", D, dtype, index)
-    L = accepted_nodes.shape[1]
-    _enqueue(lib.ddtree_commit_paged, "ddtree_commit_paged", index, stream, cache._c, k_rows, v_rows,
-             _ints(accept_len, "accept_len", (B,), index),
-             _ints(accepted_nodes, "accepted_nodes", (B, L), index),
-             _ints(prefix_len, "prefix_len", (B,), index),
-             None if new_len is None else _ints(new_len, "new_len", (B,), index), B, L,
-             k_tree.shape[1] - 1)
+    st = _ddtree.commit_paged(cache._c, cache._index, cache.B, k_tree, v_tree, accept_len,
+                              accepted_nodes, prefix_len, new_len,
+                              _raw("ddtree_commit_paged", stream, cache._index))
+    if st:
+        raise DDTreeError("ddtree_commit_paged", st)
