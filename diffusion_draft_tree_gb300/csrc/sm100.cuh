@@ -65,23 +65,7 @@ DDT_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
 }
 
 // ---- TMA (bulk tensor copy global -> shared, completes on an mbarrier) -----------
-DDT_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                         int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-DDT_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                         int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-// ... and issued by the lane of a whole warp whose `lead` is set (elect_one).
+// Issued by the lane of a whole warp whose `lead` is set (elect_one, below).
 DDT_DEV void tma_load_3d_warp(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                               int c0, int c1, int c2) {
     asm volatile(
@@ -160,31 +144,10 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, int a_mn, int b_m
                : idesc_bf16_f32(M, N, a_mn, b_mn);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
-DDT_DEV void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T: the A operand (M rows in TMEM lanes, two
-// 16-bit elements per 32-bit column, lower half first) read from tensor memory.
-DDT_DEV void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The same products and commit for a whole warp that keeps together: issued by
-// the one lane whose `lead` is set (elect_one), without a branch, so that the
-// compiler keeps descriptors and addresses, equal in all lanes, in the uniform
-// registers that tcgen05.mma takes them from.
+// Products, commits and copies are issued by a whole warp that keeps together, in
+// the one lane whose `lead` is set (elect_one), without a branch: the compiler
+// then keeps descriptors and addresses, equal in all lanes, in the uniform
+// registers that these instructions take them from.
 DDT_DEV uint32_t elect_one() {
     uint32_t r;
     asm volatile(
@@ -192,7 +155,8 @@ DDT_DEV uint32_t elect_one() {
         : "=r"(r));
     return r;
 }
-DDT_DEV void mma_bf16_ss_warp(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+// D[tmem] (+)= A[smem] * B[smem]^T.
+DDT_DEV void mma_ss_warp(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                               uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -202,7 +166,9 @@ DDT_DEV void mma_bf16_ss_warp(uint32_t lead, uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
-DDT_DEV void mma_bf16_ts_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+// D[tmem] (+)= A[tmem] * B[smem]^T: the A operand (M rows in TMEM lanes, two
+// 16-bit elements per 32-bit column, lower half first) read from tensor memory.
+DDT_DEV void mma_ts_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                               uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -212,6 +178,8 @@ DDT_DEV void mma_bf16_ts_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, u
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
+// Arrives (once) on the mbarrier when every tcgen05.mma that the lead lane issued
+// so far has completed.
 DDT_DEV void mma_commit_warp(uint32_t lead, uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
@@ -220,15 +188,6 @@ DDT_DEV void mma_commit_warp(uint32_t lead, uint64_t* bar) {
         "r"(lead)
         : "memory");
 }
-// Arrives (once) on the mbarrier when every tcgen05.mma this thread issued so
-// far has completed.
-DDT_DEV void mma_commit(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
-
 // ---- TMEM <-> registers (warp-collective; a warp reaches lanes 32*(warp%4)..+31) --
 DDT_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(

@@ -176,10 +176,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     constexpr bool PAGED = MODE != kDense, F16 = MODE == kPagedFp16;
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_q, bar_full[NS], bar_empty[NS], bar_sfull[2],
+    __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
+        bar_vempty[NS], bar_sfull[2],
         bar_pfull[2], bar_odone[2], bar_recv;
-    // (paged: the two above are K's; V has its own, see the copy warp)
-    __shared__ __align__(8) uint64_t bar_vfull[NS], bar_vempty[NS];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
@@ -187,19 +186,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ float2 s_ml1[BM];  // lone tile: (m, l) of the second group's key halves
 
     const int tid = threadIdx.x, lane = tid & 31;
-    // (paged: known to be one number a warp, see the MMA issuer)
-    const int warp = PAGED ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid >> 5;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one number a warp
 
     // ---- set-up that reads no global memory (overlaps the previous kernel) -------
     if (tid == 0) {
         mbar_init(&bar_q, 1);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar_full[s], 1);
-            mbar_init(&bar_empty[s], 1);
-            if constexpr (PAGED) {
-                mbar_init(&bar_vfull[s], 1);
-                mbar_init(&bar_vempty[s], 1);
-            }
+            mbar_init(&bar_kfull[s], 1);
+            mbar_init(&bar_kempty[s], 1);
+            mbar_init(&bar_vfull[s], 1);
+            mbar_init(&bar_vempty[s], 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&bar_sfull[k], 1);
@@ -368,216 +364,141 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (idle) {
     } else if (warp == 0) {
         // =========================== TMA producer ===========================
+        // The warp keeps together and one lane issues: a lane that polled a barrier for
+        // the others, or a lane for each copy, divides the warp, which slowed every
+        // warp of its scheduler (long_context_70b over pages 3.2 -> 4.1 ms) and made
+        // the copies of 16-row pages the slowest part of the kernel.
+        const uint32_t lead = elect_one();
+        if (lane == 0) mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
+        __syncwarp();
+        for (int h = 0; h < C::NH; ++h) {
+            tma_load_3d_warp(lead, smem_u32(sq) + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G, b * R + u00);
+            if (has1)
+                tma_load_3d_warp(lead, smem_u32(sq) + C::QT_BYTES + h * kHalfBytes, &tm_q, &bar_q, 64 * h,
+                                 g * G, b * R + u01);
+        }
+        // A paged prefix tile is nb boxes of `box` rows, one page (or part of one)
+        // each.  Page numbers come 32 boxes at a time, lane l holding box 32 k + l of
+        // the split, the batch after that in flight; nothing looks at them before a
+        // tile of theirs is due.  From the pool's end a copy reads zeros: boxes past
+        // the prefix, and pages outside the pool.
+        int ps = BN, ps_log2 = 0, num_pages = 0;
+        const int32_t* table = nullptr;
         if constexpr (PAGED) {
-            // A prefix tile is nb boxes of `box` rows, one page (or part of one) each.
-            // The warp keeps together and one lane issues (measured with pages of 16:
-            // a lane for each copy made the copies the slowest part of the kernel).
-            const int ps = 1 << p.ps_log2, box = min(ps, BN), nb = BN / box;
-            const uint32_t lead = elect_one();
-            const int32_t* table = p.table + b * p.table_stride;
-            // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of the
-            // split, the batch after that in flight; nothing looks at them before a
-            // tile of theirs is due.  From the pool's end a copy reads zeros: boxes
-            // past the prefix, and pages outside the pool.
-            auto ids_of = [&](int k) {
-                const int x = k * 32 + lane, key = t_begin * BN + x * box;
-                return x < nprefix * nb && key < P ? __ldg(&table[key >> p.ps_log2]) : p.num_pages;
-            };
-            auto checked = [&](int page, int k) {
-                if ((unsigned)page < (unsigned)p.num_pages) return page;
-                const int x = k * 32 + lane;
-                if (x < nprefix * nb && t_begin * BN + x * box < P)
-                    record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
-                return p.num_pages;
-            };
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
-                for (int h = 0; h < C::NH; ++h) {
-                    tma_load_3d(sq + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G, b * R + u00);
-                    if (has1)
-                        tma_load_3d(sq + C::QT_BYTES + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G,
-                                    b * R + u01);
-                }
+            ps_log2 = p.ps_log2;
+            ps = 1 << ps_log2;
+            num_pages = p.num_pages;
+            table = p.table + b * p.table_stride;
+        }
+        const int box = min(ps, BN), nb = BN / box;
+        auto ids_of = [&](int k) {
+            const int x = k * 32 + lane, key = t_begin * BN + x * box;
+            return PAGED && x < nprefix * nb && key < P ? __ldg(&table[key >> ps_log2]) : num_pages;
+        };
+        auto checked = [&](int page, int k) {
+            if (!PAGED || (unsigned)page < (unsigned)num_pages) return page;
+            const int x = k * 32 + lane;
+            if (x < nprefix * nb && t_begin * BN + x * box < P)
+                record_error(p.err, ERR_ATTN | ERR_BAD_PAGE);
+            return num_pages;
+        };
+        int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
+        for (int j = 0; j < nt; ++j) {
+            const int s = j % NS;
+            if (PAGED && j > 0 && (j * nb & 31) == 0) {
+                ids = checked(next_ids, j * nb / 32);
+                next_ids = ids_of(j * nb / 32 + 1);
             }
-            int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
-            for (int j = 0; j < nt; ++j) {
-                const int s = j % NS;
-                if (j > 0 && (j * nb & 31) == 0) {
-                    ids = checked(next_ids, j * nb / 32);
-                    next_ids = ids_of(j * nb / 32 + 1);
-                }
-                // K and V of a stage come and go separately: K's half is free again as
-                // soon as its tile's scores are formed, so K runs a tile further ahead,
-                // and the scores wait for half the bytes.  (All lanes wait: one that
-                // polled for the others would leave the warp divided.)
-                bool ok = true;
+            // K and V of a stage come and go separately: K's half is free again as soon
+            // as its tile's scores are formed, so K runs a tile further ahead, and the
+            // scores wait for half the bytes.
+            bool ok = true;
 #pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
-                    const CUtensorMap* map = v ? &tm_vc : &tm_kc;
-                    uint64_t* full = v ? &bar_vfull[s] : &bar_full[s];
-                    const uint32_t to = smem_u32(v ? sv : sk) + s * C::KV_BYTES;
-                    ok = mbar_wait(v ? &bar_vempty[s] : &bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
-                    __syncwarp();
-                    if (j < nprefix) {
-                        const int key0 = (t_begin + j) * BN;
-#pragma unroll 4
-                        for (int i = 0; i < nb; ++i) {
-                            const int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
-                            const int row = (key0 + i * box) & (ps - 1);
+            for (int v = 0; v < 2; ++v) {
+                const CUtensorMap* map = v ? &tm_vc : &tm_kc;
+                uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
+                const uint32_t to = smem_u32(v ? sv : sk) + s * C::KV_BYTES;
+                ok = mbar_wait(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
+                __syncwarp();
+                const int key0 = (t_begin + j) * BN;
+                if (j >= nprefix) {
+                    const int a0 = (tree_first + j - nprefix) * BN;
 #pragma unroll
-                            for (int h = 0; h < C::NH; ++h)
-                                tma_load_4d_warp(lead, to + h * kHalfBytes + i * box * 128, map, full, 64 * h,
-                                                 row, g, page);
-                        }
-                    } else {
-                        const int a0 = (tree_first + j - nprefix) * BN;
+                    for (int h = 0; h < C::NH; ++h)
+                        tma_load_3d_warp(lead, to + h * kHalfBytes, v ? &tm_vt : &tm_kt, full, 64 * h, g,
+                                         b * R + a0);
+                } else if constexpr (PAGED) {
+#pragma unroll 4
+                    for (int i = 0; i < nb; ++i) {
+                        const int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
+                        const int row = (key0 + i * box) & (ps - 1);
 #pragma unroll
                         for (int h = 0; h < C::NH; ++h)
-                            tma_load_3d_warp(lead, to + h * kHalfBytes, v ? &tm_vt : &tm_kt, full, 64 * h, g,
-                                             b * R + a0);
-                    }
-                }
-                if (!ok) { fail(); break; }
-            }
-        } else if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::QT_BYTES);
-            for (int h = 0; h < C::NH; ++h) {
-                tma_load_3d(sq + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G, b * R + u00);
-                if (has1)
-                    tma_load_3d(sq + C::QT_BYTES + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G,
-                                b * R + u01);
-            }
-            for (int j = 0; j < nt; ++j) {
-                const int s = j % NS;
-                if (!mbar_wait(&bar_empty[s], ((j / NS) & 1) ^ 1, &s_abort)) { fail(); break; }
-                mbar_arrive_expect_tx(&bar_full[s], 2 * C::KV_BYTES);
-                uint8_t* dk = sk + s * C::KV_BYTES;
-                uint8_t* dv = sv + s * C::KV_BYTES;
-                if (j < nprefix) {
-                    const int p0 = (t_begin + j) * BN;
-                    for (int h = 0; h < C::NH; ++h) {
-                        tma_load_3d(dk + h * kHalfBytes, &tm_kc, &bar_full[s], 64 * h, p0, b * p.Hkv + g);
-                        tma_load_3d(dv + h * kHalfBytes, &tm_vc, &bar_full[s], 64 * h, p0, b * p.Hkv + g);
+                            tma_load_4d_warp(lead, to + h * kHalfBytes + i * box * 128, map, full, 64 * h, row,
+                                             g, page);
                     }
                 } else {
-                    const int a0 = (tree_first + j - nprefix) * BN;
-                    for (int h = 0; h < C::NH; ++h) {
-                        tma_load_3d(dk + h * kHalfBytes, &tm_kt, &bar_full[s], 64 * h, g, b * R + a0);
-                        tma_load_3d(dv + h * kHalfBytes, &tm_vt, &bar_full[s], 64 * h, g, b * R + a0);
-                    }
+#pragma unroll
+                    for (int h = 0; h < C::NH; ++h)
+                        tma_load_3d_warp(lead, to + h * kHalfBytes, map, full, 64 * h, key0, b * p.Hkv + g);
                 }
             }
+            if (!ok) { fail(); break; }
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        if constexpr (PAGED) {
-            // The whole warp runs the loop and one lane issues: per tile and query
-            // tile k, O_k += P_k V_j and then S_k = Q_k K_{j+1}^T (the same order as
-            // below), each product's descriptors a base plus constants.
-            constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
-            const uint32_t lead = elect_one();
-            const uint32_t idesc_qk = idesc_f32<F16>(BM, dual ? BN / 2 : BN, 0, 0);
-            constexpr uint32_t idesc_pv = idesc_f32<F16>(BM, D, 0, 1);
-            const uint64_t qd = smem_desc_sw128(smem_u32(sq), 16, 1024);
-            const uint64_t kd = smem_desc_sw128(smem_u32(sk), 16, 1024);
-            const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
-            const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
-            bool ok = mbar_wait(&bar_q, 0, &s_abort);
-            int sj = 0;  // stage of tile j
+        // The whole warp runs the loop and one lane issues: per key tile j and query
+        // tile k, O_k += P_k V_j and then S_k = Q_k K_{j+1}^T (which reuses S_k / P_k in
+        // that order), each product's descriptors a base plus constants.
+        constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
+        const uint32_t lead = elect_one();
+        const uint32_t idesc_qk = idesc_f32<F16>(BM, dual ? BN / 2 : BN, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_f32<F16>(BM, D, 0, 1);
+        const uint64_t qd = smem_desc_sw128(smem_u32(sq), 16, 1024);
+        const uint64_t kd = smem_desc_sw128(smem_u32(sk), 16, 1024);
+        const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
+        const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
+        bool ok = mbar_wait(&bar_q, 0, &s_abort);
+        int sj = 0;  // stage of tile j
 #pragma unroll 1
-            for (int j = -1; ok && j < nt; ++j) {
-                const int sn = j < 0 || sj + 1 == NS ? 0 : sj + 1;  // ... of tile j + 1
+        for (int j = -1; ok && j < nt; ++j) {
+            const int sn = j < 0 || sj + 1 == NS ? 0 : sj + 1;  // ... of tile j + 1
 #pragma unroll 1
-                for (int k = 0; ok && k < (two ? 2 : 1); ++k) {
-                    if (j >= 0) {
-                        ok = mbar_wait(&bar_pfull[k], j & 1, &s_abort);
-                        if (k == 0) ok = ok && mbar_wait(&bar_vfull[sj], (j / NS) & 1, &s_abort);
-                        tc_fence_after();
-                        const uint64_t b0 = vd + (uint32_t)(sj * (C::KV_BYTES >> 4)) + k * k_half;
-                        const uint32_t d0 = tmem + 256 + k * D, a0 = tmem + k * BN;
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk) {
-                            if (dual && kk >= BN / 32) break;  // 64 keys: P columns [0, 32)
-                            mma_bf16_ts_warp(lead, d0, a0 + p_col(kk), b0 + kk * (2048 >> 4), idesc_pv,
-                                             kk > 0 ? 1u : (uint32_t)(j > 0));
-                        }
-                        mma_commit_warp(lead, &bar_odone[k]);
-                        if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[sj]);
-                    }
-                    if (ok && j + 1 < nt) {
-                        if (k == 0) ok = mbar_wait(&bar_full[sn], ((j + 1) / NS) & 1, &s_abort);
-                        tc_fence_after();
-                        const uint64_t a0 = qd + k * q_tile;
-                        const uint64_t b0 = kd + (uint32_t)(sn * (C::KV_BYTES >> 4)) + k * k_half;
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                            mma_bf16_ss_warp(lead, tmem + k * BN, a0 + off, b0 + off, idesc_qk, kk > 0);
-                        }
-                        mma_commit_warp(lead, &bar_sfull[k]);
-                        if (k == 1 || !two) mma_commit_warp(lead, &bar_empty[sn]);
-                    }
-                }
-                sj = sn;
-            }
-            if (!ok) fail();
-        } else if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_f32<F16>(BM, BN, 0, 0);
-            constexpr uint32_t idesc_qk_half = idesc_f32<F16>(BM, BN / 2, 0, 0);
-            constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
-            constexpr uint32_t idesc_pv = idesc_f32<F16>(BM, D, 0, 1);
-            const uint32_t q_addr = smem_u32(sq);
-            auto qk = [&](int j, int k) {
-                // dual: query tile 0 against keys [64k, 64k + 64) of the tile
-                const uint32_t k_addr = smem_u32(sk + (j % NS) * C::KV_BYTES) + (dual ? k * kHalfRows : 0u);
-                const uint32_t qa = q_addr + (dual ? 0u : k * C::QT_BYTES);
-                const uint32_t idesc = dual ? idesc_qk_half : idesc_qk;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-                    mma_bf16_ss(tmem + k * BN, smem_desc_sw128(qa + off, 16, 1024),
-                                smem_desc_sw128(k_addr + off, 16, 1024), idesc, kk > 0);
-                }
-                mma_commit(&bar_sfull[k]);
-            };
-            auto pv = [&](int j, int k) {
-                const uint32_t v_addr = smem_u32(sv + (j % NS) * C::KV_BYTES) + (dual ? k * kHalfRows : 0u);
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk) {
-                    if (dual && kk >= BN / 32) break;  // 64 keys: P columns [0, 32)
-                    mma_bf16_ts(tmem + 256 + k * D, tmem + k * BN + p_col(kk),
-                                smem_desc_sw128(v_addr + kk * 2048, kHalfBytes, 1024), idesc_pv,
-                                (j > 0 || kk > 0) ? 1u : 0u);
-                }
-                mma_commit(&bar_odone[k]);
-            };
-            bool ok = mbar_wait(&bar_q, 0, &s_abort) && mbar_wait(&bar_full[0], 0, &s_abort);
-            if (!ok) fail();
-            if (ok) {
-                tc_fence_after();
-                qk(0, 0);
-                if (two) qk(0, 1);
-            }
-            for (int j = 0; ok && j < nt; ++j) {
-                if (!mbar_wait(&bar_pfull[0], j & 1, &s_abort)) { fail(); break; }
-                tc_fence_after();
-                pv(j, 0);
-                if (j + 1 < nt) {
-                    if (!mbar_wait(&bar_full[(j + 1) % NS], ((j + 1) / NS) & 1, &s_abort)) { fail(); break; }
+            for (int k = 0; ok && k < (two ? 2 : 1); ++k) {
+                if (j >= 0) {
+                    ok = mbar_wait(&bar_pfull[k], j & 1, &s_abort);
+                    if (k == 0) ok = ok && mbar_wait(&bar_vfull[sj], (j / NS) & 1, &s_abort);
                     tc_fence_after();
-                    qk(j + 1, 0);  // issued after pv(j, 0): reuses S_0/P_0 in order
+                    const uint64_t b0 = vd + (uint32_t)(sj * (C::KV_BYTES >> 4)) + k * k_half;
+                    const uint32_t d0 = tmem + 256 + k * D, a0 = tmem + k * BN;
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk) {
+                        if (dual && kk >= BN / 32) break;  // 64 keys: P columns [0, 32)
+                        mma_ts_warp(lead, d0, a0 + p_col(kk), b0 + kk * (2048 >> 4), idesc_pv,
+                                         kk > 0 ? 1u : (uint32_t)(j > 0));
+                    }
+                    mma_commit_warp(lead, &bar_odone[k]);
+                    if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[sj]);
                 }
-                if (two) {
-                    if (!mbar_wait(&bar_pfull[1], j & 1, &s_abort)) { fail(); break; }
+                if (ok && j + 1 < nt) {
+                    if (k == 0) ok = mbar_wait(&bar_kfull[sn], ((j + 1) / NS) & 1, &s_abort);
                     tc_fence_after();
-                    pv(j, 1);
+                    const uint64_t a0 = qd + k * q_tile;
+                    const uint64_t b0 = kd + (uint32_t)(sn * (C::KV_BYTES >> 4)) + k * k_half;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                        mma_ss_warp(lead, tmem + k * BN, a0 + off, b0 + off, idesc_qk, kk > 0);
+                    }
+                    mma_commit_warp(lead, &bar_sfull[k]);
+                    if (k == 1 || !two) mma_commit_warp(lead, &bar_kempty[sn]);
                 }
-                mma_commit(&bar_empty[j % NS]);
-                if (two && j + 1 < nt) qk(j + 1, 1);
             }
+            sj = sn;
         }
+        if (!ok) fail();
     } else {
         // ==================== softmax / epilogue, one thread per query row ====================
         const int k = (warp - 2) >> 2;            // query tile of this group
@@ -820,7 +741,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (k == 0 && !key_r_valid) {
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
-                if (!mbar_wait(PAGED ? &bar_vfull[s] : &bar_full[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
+                if (!mbar_wait(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
                 uint8_t* vrow = sv + s * C::KV_BYTES + r * 128;
 #pragma unroll
                 for (int h = 0; h < C::NH; ++h)

@@ -308,10 +308,12 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             bool ok = true;  // (all lanes wait, so that the warp stays in one piece)
             if (first) {
                 ok = mbar_wait(&bar_qempty, (units & 1) ^ 1, &s_abort);
-                if (ok && lane == 0) {
-                    mbar_arrive_expect_tx(&bar_qfull, NH * p.rows * 128);
+                if (ok) {
+                    if (lane == 0) mbar_arrive_expect_tx(&bar_qfull, NH * p.rows * 128);
+                    __syncwarp();
                     for (int h = 0; h < NH; ++h)
-                        tma_load_3d(sq + h * C::QSLAB, &tm_q, &bar_qfull, 64 * h, at.g * p.G, at.b * R);
+                        tma_load_3d_warp(lead, smem_u32(sq) + h * C::QSLAB, &tm_q, &bar_qfull, 64 * h,
+                                         at.g * p.G, at.b * R);
                 }
                 ++units;
             }
@@ -322,11 +324,11 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             __syncwarp();
             uint8_t* dk = base + s * C::STAGE;
             if (tree) {
-                if (lane < 2 * NH) {
-                    const int h = lane % NH;
-                    const bool v = lane >= NH;
-                    tma_load_3d(dk + (v ? C::KV : 0) + h * C::SLAB, v ? &tm_vt : &tm_kt, &bar_full[s],
-                                64 * h, at.g, at.b * R);
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const uint32_t to = smem_u32(dk) + h * C::SLAB;
+                    tma_load_3d_warp(lead, to, &tm_kt, &bar_full[s], 64 * h, at.g, at.b * R);
+                    tma_load_3d_warp(lead, to + C::KV, &tm_vt, &bar_full[s], 64 * h, at.g, at.b * R);
                 }
             } else {
 #pragma unroll 4
