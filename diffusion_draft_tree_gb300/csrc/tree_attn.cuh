@@ -756,11 +756,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
         // ---- epilogue (every softmax thread runs the same barrier sequence) ----
         if (work && ok && !mbar_wait(&bar_odone[k], (nt - 1) & 1, &s_abort)) { fail(); ok = false; }
-        if (dual && k == 1) s_ml1[r] = make_float2(m_run, l);
+        // (paged splits in a cluster: everything up to the exchange stays where it is)
+        const bool exchange = PAGED && p.merge == kMergeCluster && splits > 1;
+        if (exchange) s_ml[k * BM + r] = make_float2(m_run, l);
+        else if (dual && k == 1) s_ml1[r] = make_float2(m_run, l);
         const bool all_ok = softmax_bar_and(ok);
         const bool have = all_ok && mine;          // warp-uniform
         tc_fence_after();
-        if (dual && have) {
+        if (dual && have && !exchange) {
             // fold the second group's keys into O_0: O = w0 O_0 + w1 O_1,
             // l = w0 l_0 + w1 l_1, w_k = 2^(m_k - M), 0 for a group without keys
             // (both 0 for a row without keys).  No per-row branch: the TMEM loads
@@ -827,9 +830,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             } else if (all_ok && row_out) {  // a tile of padding rows
                 store_zero();
             }
-        } else if (PAGED && p.merge == kMergeCluster) {
+        } else if (exchange) {
             // (the partial stays in TMEM until the peers' shared memory is idle)
-            s_ml[k * BM + r] = make_float2(m_run, l);
             if (tid == 64) s_ok = all_ok;
         } else if (p.merge == kMergeCluster) {
             if (have) {
@@ -971,25 +973,49 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // all rows, idle ranks too: each split's threads store their rows'
             // unnormalised O, 32 bits a value straight from TMEM, and (m, l) into
             // the owners' shared memory, which no product or copy uses any more;
-            // then out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - M).
+            // then out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - M).  On a lone
+            // tile the two groups fold their halves of the keys on the way out, each
+            // for half of the columns, and share the merge.
             const int S = p.smax;
             const uint32_t slot = chunk_slots<D>(S) * kChunk4;
             const uint32_t recv = smem_u32(base), recv_ml = recv + (uint32_t)S * slot;
-            const int k = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, row2 = k * BM + r;
-            const int u = (k == 0 ? u00 : u01) + r / G, hh = g * G + r % G;
-            const bool mine = k == 0 || has1;
+            const int k = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, tile = dual ? 0 : k;
+            const int row2 = tile * BM + r;
+            const int u = (tile == 0 ? u00 : u01) + r / G, hh = g * G + r % G;
+            const bool mine = tile == 0 || has1;
             const bool row_valid = mine && u <= n && r < rows_used;
             fence_proxy_async_smem();
             cluster_sync();
             if (warp >= 2 && mine && !idle && s_ok) {
                 tc_fence_after();
-                const uint32_t tm_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + k * D;
+                const uint32_t tm_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + tile * D;
+                float2 ml = s_ml[row2];
+                float w0 = 1.f, w1 = 0.f;
+                if (dual) {
+                    const float2 ml1 = s_ml[BM + r];
+                    const float M = fmaxf(ml.x, ml1.x);
+                    w0 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+                    w1 = ml1.x == -INFINITY ? 0.f : fast_exp2(ml1.x - M);
+                    ml = make_float2(M, w0 * ml.y + w1 * ml1.y);
+                }
+                const int c_first = dual ? k * (D / 64) : 0, c_last = dual ? c_first + D / 64 : D / 32;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = c_first; c < c_last; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tm_o + c * 32, t);
-                    tmem_ld_wait();
-                    tmem_ld_fence(t);
+                    if (dual) {
+                        uint32_t t1[32];
+                        tmem_ld32(tm_o + D + c * 32, t1);
+                        tmem_ld_wait();
+                        tmem_ld_fence(t);
+                        tmem_ld_fence(t1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            t[i] = __float_as_uint(w0 * __uint_as_float(t[i]) + w1 * __uint_as_float(t1[i]));
+                    } else {
+                        tmem_ld_wait();
+                        tmem_ld_fence(t);
+                    }
                     if (row_valid) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -1002,51 +1028,58 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         }
                     }
                 }
-                if (row_valid)
+                if (row_valid && (!dual || k == 0))
                     for (int o = 0; o < S; ++o)
-                        st_dsmem_f32x2(mapa_shared(recv_ml + split * C::ML_BYTES + row2 * 8, o),
-                                       s_ml[row2]);
+                        st_dsmem_f32x2(mapa_shared(recv_ml + split * C::ML_BYTES + row2 * 8, o), ml);
                 tc_fence_before();
             }
             cluster_sync();
-            if (warp >= 2 && (k == 0 || tile1) && u < R && r < rows_used) {
+            if (warp >= 2 && (tile == 0 || tile1) && u < R && r < rows_used) {
+                // (four splits at a time, those past the last with weight 0)
                 const float2* ml = reinterpret_cast<const float2*>(base + S * slot) + row2;
-                float M = -INFINITY, Ls = 0.f, w[kMaxSplits];
+                float M = -INFINITY, Ls = 0.f, w[kMaxSplits], ls[kMaxSplits];
 #pragma unroll
                 for (int s2 = 0; s2 < kMaxSplits; ++s2) {
-                    w[s2] = row_valid && s2 < splits ? ml[s2 * 2 * BM].x : -INFINITY;
-                    M = fmaxf(M, w[s2]);
+                    const bool there = row_valid && s2 < splits;
+                    const float2 x = there ? ml[s2 * 2 * BM] : make_float2(-INFINITY, 0.f);
+                    w[s2] = x.x, ls[s2] = x.y;
+                    M = fmaxf(M, x.x);
                 }
                 const float mref = M == -INFINITY ? 0.f : M;
 #pragma unroll
                 for (int s2 = 0; s2 < kMaxSplits; ++s2) {
                     w[s2] = fast_exp2(w[s2] - mref);
-                    if (row_valid && s2 < splits) Ls = fmaf(w[s2], ml[s2 * 2 * BM].y, Ls);
+                    Ls = fmaf(w[s2], ls[s2], Ls);
                 }
                 const bool live = row_valid && Ls > 0.f;
                 const float inv = live ? 1.f / Ls : 0.f;
                 uint2* dst = (uint2*)(p.out + (((size_t)b * R + u) * p.Hq + hh) * D);
                 const int lo = chunk_lo<D>(split, S), hi = chunk_lo<D>(split + 1, S);
 #pragma unroll 1
-                for (int c = lo; c < hi; ++c) {
+                for (int c = lo + (dual ? k : 0); c < hi; c += dual ? 2 : 1) {
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     const float4* x = reinterpret_cast<const float4*>(base + (c - lo) * kChunk4) + row2;
                     if (live) {
 #pragma unroll
-                        for (int s2 = 0; s2 < kMaxSplits; ++s2) {
-                            if (s2 < splits) {
-                                const float4 v = x[s2 * (slot / 16)];
-                                acc.x = fmaf(w[s2], v.x, acc.x);
-                                acc.y = fmaf(w[s2], v.y, acc.y);
-                                acc.z = fmaf(w[s2], v.z, acc.z);
-                                acc.w = fmaf(w[s2], v.w, acc.w);
+                        for (int s0 = 0; s0 < kMaxSplits; s0 += 4) {
+                            if (s0 < splits) {
+                                float4 v[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[i] = x[min(s0 + i, splits - 1) * (slot / 16)];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    acc.x = fmaf(w[s0 + i], v[i].x, acc.x);
+                                    acc.y = fmaf(w[s0 + i], v[i].y, acc.y);
+                                    acc.z = fmaf(w[s0 + i], v[i].z, acc.z);
+                                    acc.w = fmaf(w[s0 + i], v[i].w, acc.w);
+                                }
                             }
                         }
                     }
                     dst[c] = make_uint2(pack16<F16>(acc.x * inv, acc.y * inv),
                                         pack16<F16>(acc.z * inv, acc.w * inv));
                 }
-                if (split == 0 && p.lse)
+                if (split == 0 && p.lse && (!dual || k == 0))
                     p.lse[((size_t)b * R + u) * p.Hq + hh] =
                         live ? (M + __log2f(Ls)) * 0.6931471805599453f : -INFINITY;
             }
