@@ -177,8 +177,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
-        bar_vempty[NS], bar_sfull[2],
-        bar_pfull[2], bar_odone[2], bar_recv;
+        bar_vempty[NS], bar_sfull[2][2],
+        bar_pfull[2][2], bar_odone[2], bar_recv;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
@@ -198,8 +198,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bar_vempty[s], 1);
         }
         for (int k = 0; k < 2; ++k) {
-            mbar_init(&bar_sfull[k], 1);
-            mbar_init(&bar_pfull[k], 128);
+            mbar_init(&bar_sfull[k][0], 1);
+            mbar_init(&bar_sfull[k][1], 1);
+            mbar_init(&bar_pfull[k][0], 128);
+            mbar_init(&bar_pfull[k][1], 128);
             mbar_init(&bar_odone[k], 1);
         }
         mbar_init(&bar_recv, 1);
@@ -314,6 +316,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // one 64-key half of every key tile, and merge their (m, l, O) at the end.
     const bool dual = !tile1;
     const bool two = has1 || dual;              // two S / P / O groups in flight
+    // A lone tile's scores take 64 of each group's 128 columns.  The paged forms use
+    // the others for the next key tile, whose product then runs while this one is
+    // exponentiated.
+    const int ahead = PAGED && dual ? 2 : 1;
+    auto buffer = [&](int j) { return ahead == 2 ? (uint32_t)(j & 1) * 64u : 0u; };
+    // ... and a barrier for each, as either side may then be a tile ahead of the other
+    auto bar_of = [&](int j) { return ahead == 2 ? j & 1 : 0; };
+    auto phase_of = [&](int j) { return (uint32_t)(ahead == 2 ? j >> 1 : j) & 1u; };
     if (u00 > n) {  // every query row of both tiles is padding: zeros, once
         if (split == 0) {
             for (int r = tid; r < 2 * BM; r += kThreads) {
@@ -403,18 +413,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return num_pages;
         };
         int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
-        for (int j = 0; j < nt; ++j) {
-            const int s = j % NS;
-            if (PAGED && j > 0 && (j * nb & 31) == 0) {
-                ids = checked(next_ids, j * nb / 32);
-                next_ids = ids_of(j * nb / 32 + 1);
+        for (int i = 0; i <= nt; ++i) {
+            const int ids_v = ids;  // the batch of tile i - 1
+            if (PAGED && i > 0 && (i * nb & 31) == 0) {
+                ids = checked(next_ids, i * nb / 32);
+                next_ids = ids_of(i * nb / 32 + 1);
             }
-            // K and V of a stage come and go separately: K's half is free again as soon
-            // as its tile's scores are formed, so K runs a tile further ahead, and the
-            // scores wait for half the bytes.
+            // K of tile i, then V of tile i - 1: K and V of a stage come and go
+            // separately.  K's half is free again as soon as its tile's scores are
+            // formed, so K runs ahead, and the scores wait for half the bytes.
             bool ok = true;
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
+                const int j = i - v, s = j % NS;
+                if (j < 0 || j >= nt) continue;
                 const CUtensorMap* map = v ? &tm_vc : &tm_kc;
                 uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
                 const uint32_t to = smem_u32(v ? sv : sk) + s * C::KV_BYTES;
@@ -430,13 +442,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         tma_load_3d_warp(lead, to + h * kHalfBytes, v ? &tm_vt : &tm_kt, full, 64 * h, g,
                                          b * R + a0);
                 } else if constexpr (PAGED) {
+                    const int mine = v ? ids_v : ids;
 #pragma unroll 4
-                    for (int i = 0; i < nb; ++i) {
-                        const int page = __shfl_sync(0xffffffffu, ids, (j * nb + i) & 31);
-                        const int row = (key0 + i * box) & (ps - 1);
+                    for (int x = 0; x < nb; ++x) {
+                        const int page = __shfl_sync(0xffffffffu, mine, (j * nb + x) & 31);
+                        const int row = (key0 + x * box) & (ps - 1);
 #pragma unroll
                         for (int h = 0; h < C::NH; ++h)
-                            tma_load_4d_warp(lead, to + h * kHalfBytes + i * box * 128, map, full, 64 * h, row,
+                            tma_load_4d_warp(lead, to + h * kHalfBytes + x * box * 128, map, full, 64 * h, row,
                                              g, page);
                     }
                 } else {
@@ -450,8 +463,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
         // The whole warp runs the loop and one lane issues: per key tile j and query
-        // tile k, O_k += P_k V_j and then S_k = Q_k K_{j+1}^T (which reuses S_k / P_k in
-        // that order), each product's descriptors a base plus constants.
+        // tile k, O_k += P_k V_j and then S_k = Q_k K_{j + ahead}^T (which reuses S_k /
+        // P_k in that order), each product's descriptors a base plus constants.
         constexpr uint32_t kHalfRows = (BN / 2) * 128;  // bytes of 64 key rows in a slab
         const uint32_t lead = elect_one();
         const uint32_t idesc_qk = idesc_f32<F16>(BM, dual ? BN / 2 : BN, 0, 0);
@@ -461,42 +474,44 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
         const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
         bool ok = mbar_wait(&bar_q, 0, &s_abort);
-        int sj = 0;  // stage of tile j
 #pragma unroll 1
-        for (int j = -1; ok && j < nt; ++j) {
-            const int sn = j < 0 || sj + 1 == NS ? 0 : sj + 1;  // ... of tile j + 1
+        for (int j = -ahead; ok && j < nt; ++j) {
+            const int jq = j + ahead;  // the tile whose scores follow
 #pragma unroll 1
             for (int k = 0; ok && k < (two ? 2 : 1); ++k) {
+                const uint32_t s_k = tmem + k * BN;
                 if (j >= 0) {
-                    ok = mbar_wait(&bar_pfull[k], j & 1, &s_abort);
-                    if (k == 0) ok = ok && mbar_wait(&bar_vfull[sj], (j / NS) & 1, &s_abort);
+                    const int s = j % NS;
+                    ok = mbar_wait(&bar_pfull[k][bar_of(j)], phase_of(j), &s_abort);
+                    if (k == 0) ok = ok && mbar_wait(&bar_vfull[s], (j / NS) & 1, &s_abort);
                     tc_fence_after();
-                    const uint64_t b0 = vd + (uint32_t)(sj * (C::KV_BYTES >> 4)) + k * k_half;
-                    const uint32_t d0 = tmem + 256 + k * D, a0 = tmem + k * BN;
+                    const uint64_t b0 = vd + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half;
+                    const uint32_t d0 = tmem + 256 + k * D, a0 = s_k + buffer(j);
 #pragma unroll
                     for (int kk = 0; kk < BN / 16; ++kk) {
                         if (dual && kk >= BN / 32) break;  // 64 keys: P columns [0, 32)
                         mma_ts_warp(lead, d0, a0 + p_col(kk), b0 + kk * (2048 >> 4), idesc_pv,
-                                         kk > 0 ? 1u : (uint32_t)(j > 0));
+                                    kk > 0 ? 1u : (uint32_t)(j > 0));
                     }
                     mma_commit_warp(lead, &bar_odone[k]);
-                    if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[sj]);
+                    if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[s]);
                 }
-                if (ok && j + 1 < nt) {
-                    if (k == 0) ok = mbar_wait(&bar_kfull[sn], ((j + 1) / NS) & 1, &s_abort);
+                if (ok && jq < nt) {
+                    const int s = jq % NS;
+                    if (k == 0) ok = mbar_wait(&bar_kfull[s], (jq / NS) & 1, &s_abort);
                     tc_fence_after();
                     const uint64_t a0 = qd + k * q_tile;
-                    const uint64_t b0 = kd + (uint32_t)(sn * (C::KV_BYTES >> 4)) + k * k_half;
+                    const uint64_t b0 = kd + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half;
+                    const uint32_t d0 = s_k + buffer(jq);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                        mma_ss_warp(lead, tmem + k * BN, a0 + off, b0 + off, idesc_qk, kk > 0);
+                        mma_ss_warp(lead, d0, a0 + off, b0 + off, idesc_qk, kk > 0);
                     }
-                    mma_commit_warp(lead, &bar_sfull[k]);
-                    if (k == 1 || !two) mma_commit_warp(lead, &bar_kempty[sn]);
+                    mma_commit_warp(lead, &bar_sfull[k][bar_of(jq)]);
+                    if (k == 1 || !two) mma_commit_warp(lead, &bar_kempty[s]);
                 }
             }
-            sj = sn;
         }
         if (!ok) fail();
     } else {
@@ -505,7 +520,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;         // query row == TMEM lane
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tm_s = tmem + lane_off + k * BN;
+        const uint32_t tm_s0 = tmem + lane_off + k * BN;
         const uint32_t tm_o = tmem + lane_off + 256 + k * D;
         const bool mine = (k == 0) || has1;        // this group owns a query tile
         const bool work = mine || dual;            // ... or half of tile 0's keys
@@ -545,7 +560,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = true;
         for (int j = 0; work && j < nt; ++j) {
             const int s = j % NS;
-            if (!mbar_wait(&bar_sfull[k], j & 1, &s_abort)) { fail(); ok = false; break; }
+            if (!mbar_wait(&bar_sfull[k][bar_of(j)], phase_of(j), &s_abort)) { fail(); ok = false; break; }
+            const uint32_t tm_s = tm_s0 + buffer(j);
             tc_fence_after();
             // ---- validity of the tile's keys: one 32-bit mask per 32 columns ----
             // (a whole prefix tile needs none; the last, partial prefix tile keys
@@ -628,8 +644,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float m_use = resc ? m_new : m_run;
                 const float factor = resc ? fast_exp2(m_run - m_new) : 1.f;
                 // O_k is stable here: the commit that signalled S_k covers the
-                // previous tile's P_k V product.
-                if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) rescale_o(factor);
+                // previous tile's P_k V product -- unless scores run two tiles ahead.
+                if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) {
+                    if (ahead == 2 && !mbar_wait(&bar_odone[k], (j - 1) & 1, &s_abort)) { fail(); ok = false; break; }
+                    tc_fence_after();
+                    rescale_o(factor);
+                }
                 l *= factor;
                 m_run = m_use;
                 // P = 2^(s*scale*log2e - m) as bf16 pairs: quarter c's 32 weights
@@ -751,7 +771,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 fence_proxy_async_smem();
             }
             tc_fence_before();
-            mbar_arrive(&bar_pfull[k]);
+            mbar_arrive(&bar_pfull[k][bar_of(j)]);
         }
 
         // ---- epilogue (every softmax thread runs the same barrier sequence) ----
