@@ -97,7 +97,7 @@ size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, in
             return ddt::accept_workspace_bytes(B, N, V, dtype);
         case DDTREE_OP_TREE_ATTN_PAGED:
             if (B <= 0 || N < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128 || D <= 0 ||
-                cache_cap < 0 || cache_cap > INT32_MAX)
+                cache_cap < 0 || cache_cap > (1 << 30))
                 return 0;
             return ddt::paged_attn_workspace_bytes(B, N, Hq, Hkv, D, cache_cap);
     }
@@ -292,7 +292,7 @@ ddtree_status cache_status(const ddtree_paged_cache* c) {
     if (!c || !c->k_pages || !c->v_pages || !c->page_table) return DDTREE_ERR_INVALID_ARG;
     if (!dtype16(c->dtype) || c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0 || c->D <= 0 ||
         c->max_pages <= 0 || c->table_stride < c->max_pages ||
-        (int64_t)c->max_pages * c->page_size > INT32_MAX)
+        (int64_t)c->max_pages * c->page_size > (1 << 30))
         return DDTREE_ERR_INVALID_ARG;
     if ((c->num_pages > 1 && c->page_stride < c->D) || (c->Hkv > 1 && c->head_stride < c->D) ||
         (c->page_size > 1 && c->slot_stride < c->D))
@@ -381,7 +381,7 @@ ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const 
     if (!pos || !aligned(pos, 4) || !pair_ok(q, q_out, dtype, D) || (k || k_out ? !pair_ok(k, k_out, dtype, D) : false) ||
         !rotary_ok(rot, D))
         return DDTREE_ERR_INVALID_ARG;
-    if (k && ((int64_t)q->heads + k->heads > 65535)) return DDTREE_ERR_UNSUPPORTED;
+    if ((int64_t)q->heads + (k ? k->heads : 0) > 65535) return DDTREE_ERR_UNSUPPORTED;
     ddt::RopeArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(k_out), dtype, T, D, pos,
                     rot->turns, rot->rot_dim, rot->interleaved != 0, rot->scale, inverse};
     return launched(ddt::launch_rope(a, (cudaStream_t)stream));
@@ -421,7 +421,7 @@ ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_ca
         return DDTREE_ERR_INVALID_ARG;
     if (!rows_ok(q, dt, D, true) || !rows_ok(k_tree, dt, D, true) ||
         !rows_ok(v_tree, dt, D, true) || k_tree->heads != Hkv || v_tree->heads != Hkv ||
-        q->heads % Hkv)
+        q->heads % Hkv || out == q->data || out == k_tree->data || out == v_tree->data)
         return DDTREE_ERR_INVALID_ARG;
     if (N > DDTREE_MAX_N || (D != 64 && D != 128) || q->heads / Hkv > 128 || ps < 8 ||
         (ps & (ps - 1)) || (int64_t)B * (N + 1) > INT32_MAX)
@@ -445,12 +445,12 @@ ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_
                                   int32_t* new_len, int B, int L, int N, void* stream) {
     if (ddtree_status st = cache_status(cache)) return st;
     const int dt = cache->dtype, D = cache->D;
-    if (!accept_len || !accepted_nodes || !prefix_len || new_len == prefix_len || B <= 0 ||
-        B > 65535 || L <= 0 || N < 0)
+    if (!accept_len || !accepted_nodes || !prefix_len || B <= 0 || B > 65535 || L <= 0 || N < 0)
         return DDTREE_ERR_INVALID_ARG;
     if (!rows_ok(k_tree, dt, D, false) || !rows_ok(v_tree, dt, D, false) ||
         k_tree->heads != cache->Hkv || v_tree->heads != cache->Hkv ||
-        !aligned4({accept_len, accepted_nodes, prefix_len, new_len}))
+        !aligned4({accept_len, accepted_nodes, prefix_len, new_len}) ||
+        (new_len && (new_len == prefix_len || new_len == accept_len || new_len == accepted_nodes)))
         return DDTREE_ERR_INVALID_ARG;
     if (L > DDTREE_MAX_L || N > DDTREE_MAX_N || D % 8 != 0) return DDTREE_ERR_UNSUPPORTED;
     if (!rows16(k_tree) || !rows16(v_tree) || !cache16(cache)) return DDTREE_ERR_INVALID_ARG;

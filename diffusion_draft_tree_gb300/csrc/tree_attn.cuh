@@ -15,25 +15,28 @@
 // into a 2-3 stage K/V ring; warp 1 owns TMEM and issues tcgen05.mma; two
 // groups of four warps (one thread per query row) run the online softmax of
 // the two query tiles in the log2 domain, with lazy rescaling (O is rescaled
-// only when the row max grows by more than 2^8).  P goes back into TMEM as
-// bf16 over the S columns it came from and feeds the P V product directly, so
-// shared memory holds only Q, K and V.  The two groups alternate on the tensor
+// only when the row max grows by more than 2^8).  P goes back into TMEM in the
+// 16-bit type over the S columns it came from and feeds the P V product directly,
+// so shared memory holds only Q, K and V.  The two groups alternate on the tensor
 // core: while one exponentiates, the other's products run.  When a unit's
-// prefix is split, the splits run as one thread-block cluster: each keeps its
-// unnormalised O and (m, l) in its own shared memory, and after a cluster
-// barrier every CTA merges a slice of the head dimension for all rows, reading
-// its peers' partials through distributed shared memory.  Every mbarrier wait
+// prefix is split, the splits of few units run as one thread-block cluster and
+// merge on chip, those of many units through a workspace.  Every mbarrier wait
 // is bounded in wall time; a timeout records an error and the CTA unwinds.
 //
-// The kernel comes in two forms.  kDense reads the prefix from one block per
+// Warps 0 and 1 run their loops whole and issue in one lane, under a predicate:
+// addresses and descriptors then stay in uniform registers.  Issued from inside a
+// one-lane branch a tile's four products took 3.1 to 3.8 thousand cycles where
+// the tensor core needs 2.5; this way they take 2.8 (128-key tiles, D = 128).
+//
+// The kernel comes in three forms.  kDense reads the prefix from one block per
 // sequence.  kPagedBf16 / kPagedFp16 read it from pages: a 128-key tile is
-// 128 / page_size copies, one page each, issued side by side by the lanes of
-// warp 0, whose page numbers were fetched while the previous tile was waited
-// for; the copies land in the same swizzled tile, so nothing behind them
-// changes.  These forms also keep a split's partial output in 32 bits when
-// splits are merged, sum the unrounded weights, take any G <= 128 (a query tile
-// holds floor(128 / G) nodes) and cut a sequence's tiles over the whole cluster
-// by its own length rather than by the table's capacity.
+// 128 / page_size copies, one page each, into the same swizzled tile, so nothing
+// behind them changes.  These forms also keep a split's partial output in 32 bits
+// when splits are merged, sum the unrounded weights (the logsumexp then keeps 32
+// bits however few the keys), write -inf over the scores that a row does not see
+// instead of masking in the softmax (one code path), take any G <= 128 (a query
+// tile holds up to floor(128 / G) nodes) and cut a sequence's tiles over its whole
+// cluster by its own length rather than by the table's capacity.
 #pragma once
 
 #include <mutex>
@@ -413,6 +416,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return num_pages;
         };
         int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
+        int issued[2] = {0, 0};  // tiles of K, of V
         for (int i = 0; i <= nt; ++i) {
             const int ids_v = ids;  // the batch of tile i - 1
             if (PAGED && i > 0 && (i * nb & 31) == 0) {
@@ -457,9 +461,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int h = 0; h < C::NH; ++h)
                         tma_load_3d_warp(lead, to + h * kHalfBytes, map, full, 64 * h, key0, b * p.Hkv + g);
                 }
+                if (v) issued[1] = j + 1;
+                else issued[0] = j + 1;
             }
             if (!ok) { fail(); break; }
         }
+        // (where a wait gave up, no copy may land in memory given back)
+        mbar_wait(&bar_q, 0, nullptr, 100000000ull);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            for (int j = max(0, issued[v] - NS); j < issued[v]; ++j)
+                mbar_wait(v ? &bar_vfull[j % NS] : &bar_kfull[j % NS], (j / NS) & 1, nullptr, 100000000ull);
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
         // The whole warp runs the loop and one lane issues: per key tile j and query

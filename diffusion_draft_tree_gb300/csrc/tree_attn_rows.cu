@@ -345,10 +345,9 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
             issued = it + 1;
         }
-        // (after a wait that gave up: no copy may land in memory given back)
-        if (s_abort)
-            for (int it = max(0, issued - NS); it < issued; ++it)
-                mbar_wait(&bar_full[it % NS], (it / NS) & 1, nullptr, 100000000ull);
+        // (where a wait gave up, here or below, no copy may land in memory given back)
+        for (int it = max(0, issued - NS); it < issued; ++it)
+            mbar_wait(&bar_full[it % NS], (it / NS) & 1, nullptr, 100000000ull);
         return;
     }
 

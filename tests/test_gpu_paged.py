@@ -378,6 +378,42 @@ def test_attention_of_large_batches(cuda_device, B, hi, N, Hq, Hkv, D, page, dty
         pu.check_attention(out, lse, ref, dtype, D)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_random_shapes(cuda_device, seed):
+    """Seeded shapes over the whole range, rows kernel and general kernel, one CTA
+    and many, with whatever lengths fall out."""
+    rng = np.random.default_rng(1000 + seed)
+    Hkv, G, D = int(rng.choice([1, 2, 4, 8])), int(rng.choice([1, 2, 3, 4, 6, 8, 12, 16, 32])), int(rng.choice([64, 128]))
+    B = int(min(rng.integers(1, 40), max(1, 300 // (Hkv * G))))
+    N = int(rng.choice([0, 0, 1, 3, 7, 15, 16, 31, 63, 64, 127, 200]))
+    hi = int(np.exp(rng.uniform(0, np.log(6000))))
+    lens = [int(x) for x in rng.integers(0, hi + 1, size=B)]
+    live = [int(x) for x in rng.integers(0, N + 1, size=B)]
+    c = _attn_case(seed, lens, N, Hkv * G, Hkv, D, int(rng.choice([8, 16, 32, 64, 128, 256])),
+                   BF16 if seed % 2 else FP16, bool(seed % 3 == 0), None, live, bool(seed % 4 == 0))
+    out, lse = ops.tree_attn_paged(**c)
+    ops.ddtree_device_check()
+    pu.check_attention(out, lse, _ref(c), c["q"].dtype, D)
+
+
+@pytest.mark.parametrize("B,Hkv,N", [(1024, 1, 0), (1025, 1, 0), (700, 2, 1)])
+def test_attention_of_very_many_sequences(cuda_device, B, Hkv, N):
+    """As many sequences as the rows kernel adds up, and one more (the general one)."""
+    lens = [(37 * b) % 91 if b % 5 else 0 for b in range(B)]
+    c = _attn_case(B, lens, N, 2 * Hkv, Hkv, 64, 16, BF16, live=[N * (b % 2) for b in range(B)])
+    bad = B // 2
+    ref = _ref(c)
+    c["prefix_len"][bad] = -5                 # one sequence in the middle is skipped
+    out, lse = torch.full_like(c["q"], 3.0), torch.full(c["q"].shape[:3], 3.0, device="cuda")
+    ops.ddtree_tree_attn_paged(**c, out=out, lse=lse,
+                               workspace=ops.paged_attn_workspace(c["q"], c["cache"]))
+    with pytest.raises(ops.DDTreeError):
+        ops.ddtree_device_check()
+    assert bool((out[bad] == 3.0).all())
+    keep = torch.arange(B, device="cuda") != bad
+    pu.check_attention(out[keep], lse[keep], [x[keep] for x in ref], BF16, 64)
+
+
 def test_attention_chain_mask_is_causal(cuda_device):
     """A chain of drafted tokens is a causal chunk: a plain lower triangle."""
     c = _attn_case(77, [100], 50, 8, 2, 128, 16, BF16, live=[50], chain=True)

@@ -129,6 +129,7 @@ def test_rope_refusals():
     assert _rope(qo=_rows(heads=3, data=0x90000)) == 1
     assert _rope(qo=_rows(data=0x90000, hs=64)) == 1    # written rows overlap
     assert _rope(qo=_rows(ts=512)) == 1                 # in place, other strides
+    assert _rope(q=_rows(heads=70000), qo=_rows(heads=70000)) == 2
     assert _rope(k=_rows()) == 1                        # k without k_out
     assert _rope(ko=_rows()) == 1
     assert _rope(dtype=1, q=_rows(data=0x10002)) == 1   # off the 4-byte grid
@@ -184,6 +185,7 @@ def test_attention_refusals():
     for name in ("pl", "nn", "mask", "lse"):
         assert _attn(**{name: ODD}) == 1
     assert _attn(out=P(0x60008)) == 1
+    assert _attn(out=P(0x10000)) == 1                      # an input
     assert _attn(q=_rows(heads=7, ts=1024)) == 1           # not a multiple of Hkv
     assert _attn(q=_rows(heads=258, ts=1 << 16)) == 2      # G = 129
     assert _attn(q=_rows(heads=8, ts=1024, data=0x10008)) == 1
@@ -223,7 +225,9 @@ def test_commit_refusals():
         assert _commit(**{name: None}) == 1
         assert _commit(**{name: ODD}) == 1
     assert _commit(nl=ODD) == 1
-    assert _commit(nl=OK, pl=OK) == 1                      # new_len is prefix_len
+    for name in ("al", "an", "pl"):                        # new_len is an input
+        other = {n: P(0x50000 + 0x100 * i) for i, n in enumerate(("al", "an", "pl"))}
+        assert _commit(**other, nl=other[name]) == 1
     assert _commit(B=0) == 1
     assert _commit(Lp=0) == 1
     assert _commit(Lp=17) == 2
