@@ -95,7 +95,8 @@ LAUNCHES_PER_ROUND = 5
 # the headline metric, the same string on both arms
 METRIC = "draft-tree rounds/sec (topK+build+tree-attn+accept); tree-attn % roofline"
 # Sources a kernel's DRAM traffic depends on (its own file and shared headers).
-KERNEL_SOURCES = {"tree_attn": ["tree_attn.cu", "sm100.cuh", "common.cuh"]}
+KERNEL_SOURCES = {"tree_attn": ["tree_attn.cu", "tree_attn.cuh", "tree_attn_common.cuh", "sm100.cuh",
+                                "common.cuh"]}
 
 
 def kernel_source_hash(kernel: str) -> str:

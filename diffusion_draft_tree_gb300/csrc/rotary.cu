@@ -19,10 +19,12 @@
 // off a small call's critical path; few tokens are cut by heads over more CTAs.
 // CTAs are small (128 threads, 8 an SM) because each one's table and barrier
 // leave it idle for a while: 256 threads and one token a CTA took 81 us for 16384
-// tokens of 40 heads, D = 128, bf16, and 3.4 us for 65 tokens; this takes 63 us
-// (79 % of measured HBM) and 2.5.  A warp a token with its angles in registers
-// and no table took 68 us (the angles are then computed once every 4 heads), two
-// items in flight 70 (registers, so fewer CTAs).
+// tokens of 40 heads, D = 128, bf16, and 3.4 us for 65 tokens.  Issue slots came
+// next (61 % busy): an item's token and head are stepped, not divided out, and
+// 16-bit elements are taken and rounded in pairs, 63 -> 58 us (86 % of measured
+// HBM), 2.5 us for 65 tokens.  A warp a token with its angles in registers and no
+// table took 68 us (the angles are then computed once every 4 heads), two items
+// in flight 70 (registers, so fewer CTAs).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,10 +52,57 @@ template <> DDT_DEV float from_f<float>(float x) { return x; }
 template <> DDT_DEV __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> DDT_DEV __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Two neighbours of a 16-bit type, in one word.
+template <typename T> DDT_DEV float2 unpack2(uint32_t w);
+template <> DDT_DEV float2 unpack2<__nv_bfloat16>(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+template <> DDT_DEV float2 unpack2<__half>(uint32_t w) { return __half22float2(*(const __half2*)&w); }
+template <typename T> DDT_DEV uint32_t pack2(float lo, float hi);
+template <> DDT_DEV uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
+template <> DDT_DEV uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&h;
+}
+
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
+
+// Turns the V pairs of two vectors: pairs (a.e[i], b.e[i]), or PAIRED neighbours,
+// a's before b's.  In 32 bits, one rounding each.
+DDT_DEV float2 turned(float a, float b, float c, float s) {
+    return make_float2(fmaf(a, c, -(b * s)), fmaf(a, s, b * c));
+}
+template <typename T, int V, bool PAIRED>
+DDT_DEV void turn_pairs(Vec<T, V>& a, Vec<T, V>& b, const float (&c)[V], const float (&s)[V]) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t* wa = reinterpret_cast<uint32_t*>(a.e);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(b.e);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 x = unpack2<T>(wa[i]), y = unpack2<T>(wb[i]);
+            if constexpr (PAIRED) {
+                const float2 p = turned(x.x, x.y, c[i], s[i]), q = turned(y.x, y.y, c[V / 2 + i], s[V / 2 + i]);
+                wa[i] = pack2<T>(p.x, p.y);
+                wb[i] = pack2<T>(q.x, q.y);
+            } else {
+                const float2 p = turned(x.x, y.x, c[2 * i], s[2 * i]);
+                const float2 q = turned(x.y, y.y, c[2 * i + 1], s[2 * i + 1]);
+                wa[i] = pack2<T>(p.x, q.x);
+                wb[i] = pack2<T>(p.y, q.y);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            T& ra = PAIRED ? (2 * e < V ? a.e[2 * e] : b.e[2 * e - V]) : a.e[e];
+            T& rb = PAIRED ? (2 * e + 1 < V ? a.e[2 * e + 1] : b.e[2 * e + 1 - V]) : b.e[e];
+            const float2 p = turned(to_f(ra), to_f(rb), c[e], s[e]);
+            ra = from_f<T>(p.x);
+            rb = from_f<T>(p.y);
+        }
+    }
+}
 
 struct Params {
     RowsArg q, q_out, k, k_out, v;  // unused parts have 0 heads
@@ -105,7 +154,6 @@ __global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const __grid_consta
     const int per = min(p.units, kThreads), per_pass = kThreads / per;  // heads of a pass
     const int u = blockIdx.z * kThreads + tid % per;
     const int h_first = blockIdx.y * p.chunk, heads = min(p.chunk, p.heads - h_first);
-    const int items = nt * heads;  // (token, head of this CTA's)
     const bool rotated = u < p.ru;
     // the unit's two vectors (the second may lie past an odd tail)
     const int e0 = rotated ? (PAIRED ? 2 * V * u : V * u) : p.rot + 2 * V * (u - p.ru);
@@ -116,22 +164,26 @@ __global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const __grid_consta
     struct Item {
         Vt a, b;
     };
-    auto source = [&](int i) -> const T* {
-        const int t = i / heads, h = h_first + i - t * heads;
-        const int64_t tok = t0 + t;
-        if (h < p.q.heads) return (const T*)p.q.data + tok * p.q.ts + h * p.q.hs;
-        if (h < p.q.heads + p.k.heads)
-            return (const T*)p.k.data + tok * p.k.ts + (h - p.q.heads) * p.k.hs;
-        return (const T*)p.v.data + tok * p.v.ts + (h - p.q.heads - p.k.heads) * p.v.hs;
+    // an item's token and head, kept as a pair: no division a step
+    struct At {
+        int t, h;
     };
-    auto load = [&](int i, Item& x) {
-        const T* s = source(i);
-        x.a = *(const Vt*)(s + e0);
-        if (two) x.b = *(const Vt*)(s + e1);
+    auto step = [&](At& x) {
+        for (x.h += per_pass; x.h >= h_first + heads; x.h -= heads) ++x.t;
     };
-    int i = tid / per < per_pass && u < p.units ? tid / per : items;
+    auto load = [&](const At& x, Item& v) {
+        const int64_t tok = t0 + x.t;
+        const int hk = x.h - p.q.heads, hv = hk - p.k.heads;
+        const T* s = hk < 0   ? (const T*)p.q.data + tok * p.q.ts + x.h * p.q.hs
+                     : hv < 0 ? (const T*)p.k.data + tok * p.k.ts + hk * p.k.hs
+                              : (const T*)p.v.data + tok * p.v.ts + hv * p.v.hs;
+        v.a = *(const Vt*)(s + e0);
+        if (two) v.b = *(const Vt*)(s + e1);
+    };
+    At next{tid / per < per_pass && u < p.units ? 0 : nt, h_first + tid / per};
+    while (next.h >= h_first + heads) next.h -= heads, ++next.t;
     Item ahead;
-    if (i < items) load(i, ahead);
+    if (next.t < nt) load(next, ahead);
 
     // ---- the tokens' tables ----------------------------------------------------
     if (tid < nt) {
@@ -169,14 +221,16 @@ __global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const __grid_consta
     __syncthreads();
 
     // ---- the items -------------------------------------------------------------
-    for (; i < items; i += per_pass) {
+    while (next.t < nt) {
         Item x = ahead;
-        if (i + per_pass < items) load(i + per_pass, ahead);
-        const int t = i / heads, h = h_first + i - t * heads;
+        const At at = next;
+        step(next);
+        if (next.t < nt) load(next, ahead);
+        const int t = at.t, h = at.h;
         const int64_t tok = t0 + t;
         const int hk = h - p.q.heads, hv = hk - p.k.heads;
         T* dst;
-        bool turn = rotated && s_pos[t] >= 0 && (!APPEND || hv < 0);
+        const bool turn = rotated && s_pos[t] >= 0 && (!APPEND || hv < 0);
         if (hk < 0) {
             if ((p.inplace & 1) && !turn) continue;
             dst = (T*)p.q_out.data + tok * p.q_out.ts + h * p.q_out.hs;
@@ -204,17 +258,7 @@ __global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < V; ++e) c[e] = tc[u * V + e], s[e] = ts[u * V + e];
             }
-            // the 2V elements, pair by pair, in 32 bits; one rounding each
-            T* xa = x.a.e;
-            T* xb = x.b.e;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                T& ra = PAIRED ? (2 * e < V ? xa[2 * e] : xb[2 * e - V]) : xa[e];
-                T& rb = PAIRED ? (2 * e + 1 < V ? xa[2 * e + 1] : xb[2 * e + 1 - V]) : xb[e];
-                const float a = to_f(ra), b = to_f(rb);
-                ra = from_f<T>(fmaf(a, c[e], -(b * s[e])));
-                rb = from_f<T>(fmaf(a, s[e], b * c[e]));
-            }
+            turn_pairs<T, V, PAIRED>(x.a, x.b, c, s);
         }
         *(Vt*)(dst + e0) = x.a;
         if (two) *(Vt*)(dst + e1) = x.b;
