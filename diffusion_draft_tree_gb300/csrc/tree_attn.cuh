@@ -181,7 +181,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
         bar_vempty[NS], bar_sfull[2][2],
-        bar_pfull[2][2], bar_odone[2], bar_recv;
+        bar_pfull[2][2], bar_odone[2][2], bar_recv;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
@@ -205,7 +205,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bar_sfull[k][1], 1);
             mbar_init(&bar_pfull[k][0], 128);
             mbar_init(&bar_pfull[k][1], 128);
-            mbar_init(&bar_odone[k], 1);
+            mbar_init(&bar_odone[k][0], 1);
+            mbar_init(&bar_odone[k][1], 1);
         }
         mbar_init(&bar_recv, 1);
         s_abort = 0;
@@ -325,6 +326,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int ahead = PAGED && dual ? 2 : 1;
     auto buffer = [&](int j) { return ahead == 2 ? (uint32_t)(j & 1) * 64u : 0u; };
     // ... and a barrier for each, as either side may then be a tile ahead of the other
+    // (a wait tells two phases apart, not three: with one barrier for all tiles, a
+    // group at its last tile took the end of the third last for that of its own)
     auto bar_of = [&](int j) { return ahead == 2 ? j & 1 : 0; };
     auto phase_of = [&](int j) { return (uint32_t)(ahead == 2 ? j >> 1 : j) & 1u; };
     if (u00 > n) {  // every query row of both tiles is padding: zeros, once
@@ -505,7 +508,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         mma_ts_warp(lead, d0, a0 + p_col(kk), b0 + kk * (2048 >> 4), idesc_pv,
                                     kk > 0 ? 1u : (uint32_t)(j > 0));
                     }
-                    mma_commit_warp(lead, &bar_odone[k]);
+                    mma_commit_warp(lead, &bar_odone[k][bar_of(j)]);
                     if (k == 1 || !two) mma_commit_warp(lead, &bar_vempty[s]);
                 }
                 if (ok && jq < nt) {
@@ -658,7 +661,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // O_k is stable here: the commit that signalled S_k covers the
                 // previous tile's P_k V product -- unless scores run two tiles ahead.
                 if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) {
-                    if (ahead == 2 && !mbar_wait(&bar_odone[k], (j - 1) & 1, &s_abort)) { fail(); ok = false; break; }
+                    if (ahead == 2 && !mbar_wait(&bar_odone[k][bar_of(j - 1)], phase_of(j - 1), &s_abort)) { fail(); ok = false; break; }
                     tc_fence_after();
                     rescale_o(factor);
                 }
@@ -787,7 +790,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
 
         // ---- epilogue (every softmax thread runs the same barrier sequence) ----
-        if (work && ok && !mbar_wait(&bar_odone[k], (nt - 1) & 1, &s_abort)) { fail(); ok = false; }
+        if (work && ok && !mbar_wait(&bar_odone[k][bar_of(nt - 1)], phase_of(nt - 1), &s_abort)) { fail(); ok = false; }
         // (paged splits in a cluster: everything up to the exchange stays where it is)
         const bool exchange = PAGED && p.merge == kMergeCluster && splits > 1;
         if (exchange) s_ml[k * BM + r] = make_float2(m_run, l);

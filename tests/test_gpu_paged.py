@@ -532,6 +532,37 @@ def test_attention_captured_and_replayed(cuda_device, N, lens):
             pu.check_attention(o, z, ref, BF16, 128)
 
 
+@pytest.mark.parametrize("B,P,page", [(16, 8000, 64), (16, 3001, 16)])
+def test_attention_lone_tiles_of_a_full_gpu(cuda_device, B, P, page):
+    """128 nodes and the root are four query tiles and four rows: the lone tile of
+    every (sequence, KV head), with the GPU full and every wait a real one, run
+    after run against the formula."""
+    N, Hq, Hkv, D = 128, 32, 8, 128
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    per = -(-P // page)
+    k, v = rn(B * per, Hkv, page, D), rn(B * per, Hkv, page, D)
+    table = torch.randperm(B * per, generator=gen, device="cuda").int().view(B, per)
+    q, kt, vt = rn(B, N + 1, Hq, D), rn(B, N + 1, Hkv, D), rn(B, N + 1, Hkv, D)
+    mask, n = pu.tree(_gen(P), B, N, [N] * B)
+    cache, plen, n, mask = ops.PagedCache(k, v, table), torch.full((B,), P).int().cuda(), n.cuda(), mask.cuda()
+    ws = ops.paged_attn_workspace(q, cache)
+    u = N                                     # the node of the lone tile
+    bits = ((mask[:, u, torch.arange(N + 1, device="cuda") // 32] >> (torch.arange(N + 1, device="cuda") % 32)) & 1).bool()
+    ref = torch.empty(B, Hq, D, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        for g in range(Hkv):
+            kk = torch.cat([k[table[b].long(), g].reshape(-1, D)[:P], kt[b, bits[b], g]]).double()
+            vv = torch.cat([v[table[b].long(), g].reshape(-1, D)[:P], vt[b, bits[b], g]]).double()
+            x = q[b, u, g * 4:g * 4 + 4].double() @ kk.T / D ** 0.5
+            ref[b, g * 4:g * 4 + 4] = x.softmax(1) @ vv
+    for _ in range(6):
+        out, _ = ops.tree_attn_paged(q, cache, kt, vt, plen, n, mask, workspace=ws)
+        ops.ddtree_device_check()
+        # (averages of 3000 values and more: |out| stays below 0.5, sum w|v| below 1.5)
+        assert float((out[:, u].double() - ref).abs().max()) <= 2 ** -8 * (0.5 + 1.5)
+
+
 def test_attention_is_repeatable(cuda_device):
     """Run after run the same bits: merges do not depend on which split ends last."""
     for N, lens in ((0, [5000] * 20), (128, [3000, 2000]), (64, [9000] * 20)):
