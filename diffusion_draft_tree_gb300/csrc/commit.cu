@@ -76,9 +76,14 @@ commit_kernel(uint4* __restrict__ k_cache, uint4* __restrict__ v_cache, int64_t 
 // checks the whole path and its pages with one warp -- lane i row i, L + 1 <= 17
 // rows -- so that all of a sequence's CTAs reach the same verdict without
 // talking to each other, then copies its row's Hkv heads of K and V, 16 bytes a
-// thread.  A row of a few KB is latency, not bandwidth: with a CTA a row every
-// copy is in flight at once, where one CTA a sequence would take up to 17 turns.
-__global__ void __launch_bounds__(kThreads)
+// thread.  A row of a few KB is latency, not bandwidth: three dependent round
+// trips (lengths, nodes and pages, the row).  With a CTA a row every copy is in
+// flight at once, where one CTA a sequence would take up to 17 turns, and with
+// 128 threads a CTA all rows of 128 sequences are resident at once (4.2 us; 256
+// threads 4.8, 64 threads 4.5).
+constexpr int kPagedThreads = 128, kAhead = 2;
+
+__global__ void __launch_bounds__(kPagedThreads)
 commit_paged_kernel(const __grid_constant__ PagedArgs c, const RowsArg kt, const RowsArg vt,
                     const int32_t* __restrict__ accept_len,
                     const int32_t* __restrict__ accepted_nodes,
@@ -117,19 +122,32 @@ commit_paged_kernel(const __grid_constant__ PagedArgs c, const RowsArg kt, const
     const int vd = c.D / 8;
     const int64_t tok = (int64_t)b * (N + 1) + s_node;
     const int64_t dst = s_page * c.page_stride + (P + row) % c.page_size * c.slot_stride;
-    for (int i = tid; i < 2 * c.Hkv * vd; i += kThreads) {
-        const int which = i / (c.Hkv * vd), j = i - which * c.Hkv * vd;
+    const int total = 2 * c.Hkv * vd;  // vectors, K's then V's
+    auto place = [&](const RowsArg& src, int j) {
         const int g = j / vd, e = (j - g * vd) * 8;
-        const RowsArg& src = which ? vt : kt;
-        uint16_t* to = (uint16_t*)(which ? c.v : c.k) + dst + g * c.head_stride + e;
-        *(uint4*)to = __ldg((const uint4*)((const uint16_t*)src.data + tok * src.ts + g * src.hs + e));
+        return (const uint4*)((const uint16_t*)src.data + tok * src.ts + g * src.hs + e);
+    };
+    for (int i0 = tid; i0 < total; i0 += kAhead * kPagedThreads) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * kPagedThreads, j = i < total / 2 ? i : i - total / 2;
+            if (i < total) x[k] = __ldg(place(i < total / 2 ? kt : vt, j));
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * kPagedThreads, j = i < total / 2 ? i : i - total / 2;
+            const int g = j / vd, e = (j - g * vd) * 8;
+            if (i < total)
+                *(uint4*)((uint16_t*)(i < total / 2 ? c.k : c.v) + dst + g * c.head_stride + e) = x[k];
+        }
     }
 }
 
 }  // namespace
 
 cudaError_t launch_commit_paged(const CommitPagedArgs& a, cudaStream_t s) {
-    return launch_pdl(commit_paged_kernel, dim3(a.L + 1, a.B), dim3(kThreads), 0, s, a.cache,
+    return launch_pdl(commit_paged_kernel, dim3(a.L + 1, a.B), dim3(kPagedThreads), 0, s, a.cache,
                       a.k_tree, a.v_tree, a.accept_len, a.accepted_nodes, a.prefix_len, a.new_len,
                       a.L, a.N, a.err);
 }
