@@ -284,6 +284,11 @@ bool pair_ok(const ddtree_rows* in, const ddtree_rows* out, int dtype, int D) {
     return in->data != out->data || (in->token_stride == out->token_stride &&
                                      (in->heads == 1 || in->head_stride == out->head_stride));
 }
+// Neither output is the other, nor the other's input.
+bool apart(const ddtree_rows* q, const ddtree_rows* q_out, const ddtree_rows* k,
+           const ddtree_rows* k_out) {
+    return q_out->data != k->data && (!k_out || (k_out->data != q->data && k_out->data != q_out->data));
+}
 ddt::RowsArg rows_arg(const ddtree_rows* r) {
     return r ? ddt::RowsArg{r->data, r->heads, r->token_stride, r->head_stride} : ddt::RowsArg{};
 }
@@ -379,7 +384,7 @@ ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const 
     if (D > DDTREE_MAX_ROPE_D) return DDTREE_ERR_UNSUPPORTED;
     if (T == 0) return DDTREE_OK;
     if (!pos || !aligned(pos, 4) || !pair_ok(q, q_out, dtype, D) || (k || k_out ? !pair_ok(k, k_out, dtype, D) : false) ||
-        !rotary_ok(rot, D))
+        !rotary_ok(rot, D) || (k && !apart(q, q_out, k, k_out)))
         return DDTREE_ERR_INVALID_ARG;
     if ((int64_t)q->heads + (k ? k->heads : 0) > 65535) return DDTREE_ERR_UNSUPPORTED;
     ddt::RopeArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(k_out), dtype, T, D, pos,
@@ -399,7 +404,8 @@ ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, in
     if (!seq || !pos || !aligned4({seq, pos})) return DDTREE_ERR_INVALID_ARG;
     if (!rows_ok(k, dt, D, false) || !rows_ok(v, dt, D, false) || k->heads != cache->Hkv ||
         v->heads != cache->Hkv || (q || q_out ? !pair_ok(q, q_out, dt, D) : false) ||
-        (rot && !rotary_ok(rot, D)))
+        (rot && !rotary_ok(rot, D)) || k->data == cache->k_pages || v->data == cache->v_pages ||
+        (q && !(apart(q, q_out, k, nullptr) && apart(q, q_out, v, nullptr))))
         return DDTREE_ERR_INVALID_ARG;
     if (2 * (int64_t)cache->Hkv + (q ? q->heads : 0) > 65535) return DDTREE_ERR_UNSUPPORTED;
     ddt::AppendArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(v), T, B, seq, pos,

@@ -13,6 +13,7 @@ the outputs with torch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -334,6 +335,19 @@ def _raw(name: str, stream: Optional[torch.cuda.Stream], index: int):
     return stream.cuda_stream
 
 
+def _empty(stream: Optional[torch.cuda.Stream], *specs):
+    """New tensors (shape, dtype, device) for a call on `stream` whose results the
+    caller's current stream reads.  Memory comes back from the allocator in the
+    order of the stream that it was taken on: that is the call's."""
+    if stream is None:
+        return [torch.empty(n, dtype=t, device=d) for n, t, d in specs]
+    with torch.cuda.stream(stream):
+        new = [torch.empty(n, dtype=t, device=d) for n, t, d in specs]
+    for x in new:
+        x.record_stream(torch.cuda.current_stream(x.device))
+    return new
+
+
 def _index(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("ddtree kernels take CUDA tensors")
@@ -426,8 +440,8 @@ def ddtree_rope(q, k, pos, rotary: Rotary, q_out=None, k_out=None, inverse=False
 
 def rope(q, k, pos, rotary: Rotary, inverse=False, stream=None):
     """ddtree_rope into new tensors: (q, k) rotated; k may be None."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    made = _empty(stream, *[(x.shape, x.dtype, x.device) for x in (q, k) if x is not None])
+    q_out, k_out = made[0], made[1] if len(made) > 1 else None
     ddtree_rope(q, k, pos, rotary, q_out, k_out, inverse, stream)
     return q_out, k_out
 
@@ -468,10 +482,12 @@ def ddtree_tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_n
 def tree_attn_paged(q, cache: PagedCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask,
                     scale=None, want_lse=True, workspace=None, stream=None):
     B, R, Hq, _ = q.shape
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, R, Hq), dtype=torch.float32, device=q.device) if want_lse else None
-    if workspace is None:
-        workspace = paged_attn_workspace(q, cache)
+    specs = [(q.shape, q.dtype, q.device), ((B, R, Hq), torch.float32, q.device)]
+    made = _empty(stream, *specs[:2 if want_lse else 1])
+    out, lse = made[0], made[1] if want_lse else None
+    if workspace is None:  # (its zeros have to be on the call's stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = paged_attn_workspace(q, cache)
     ddtree_tree_attn_paged(q, cache, k_tree, v_tree, prefix_len, n_nodes, anc_mask, out, lse,
                            scale, workspace, stream)
     return out, lse

@@ -300,8 +300,10 @@ typedef struct {
  * values.  Position p of sequence b is slot p % page_size of page
  * page_table[b * table_stride + p / page_size].  Entries past a sequence's
  * last position are not read and may hold anything; an entry that is read and
- * lies outside [0, num_pages) is never dereferenced, only recorded (reason 7).  Pages may be shared between sequences by calls that only read them.
- * max_pages * page_size is at most 2^30. */
+ * lies outside [0, num_pages) is never dereferenced, only recorded (reason 7).
+ * Pages may be shared between sequences by calls that only read them; a call
+ * that writes pages takes no input that overlaps the pool.  max_pages *
+ * page_size is at most 2^30. */
 typedef struct {
     void *k_pages, *v_pages; /* DEVICE */
     int32_t dtype;           /* DDTREE_BF16 or DDTREE_FP16 */
@@ -356,8 +358,9 @@ ddtree_status ddtree_rope_frequencies(int rot_dim, double base, int scaling, dou
 ddtree_status ddtree_rope_turns(const double* inv_freq, int n, uint64_t* turns);
 
 /* Rotary positions of queries and, if given, keys of T tokens.
- *   q, k       in (k nullable, at most 65535 heads together); q_out, k_out out: the same tensor (in place) or
- *              one that does not overlap any input.  Elements past rot_dim are
+ *   q, k       in (k nullable, at most 65535 heads together); q_out, k_out out:
+ *              each its input's own tensor (in place) or one that overlaps no
+ *              input, and not one tensor for both.  Elements past rot_dim are
  *              copied.  D 1..DDTREE_MAX_ROPE_D.
  *   dtype      DDTREE_BF16, DDTREE_FP16 or DDTREE_FP32; the product is formed
  *              in 32 bits and rounded once.
@@ -399,10 +402,10 @@ ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, in
  *   pointer 16-byte aligned, every stride a multiple of 8 elements and at least D.
  *   N = 0 is plain decoding: one token a sequence.
  * Outputs: out [B][N+1][Hq][D] in the cache's dtype and lse fp32 [B][N+1][Hq]
- * (nullable), dense; neither overlaps an input.  A node whose mask row leaves it no key (an empty prefix
- * and no bit set) gets zeros and -inf, like the rows past n_nodes.
- * A page whose number is outside the pool counts as keys and values of zero and
- * is recorded; a prefix_len or n_nodes out of range leaves the
+ * (nullable), dense; neither overlaps an input.  A node whose mask row leaves it
+ * no key (an empty prefix and no bit set) gets zeros and -inf, like the rows past
+ * n_nodes.  A page whose number is outside the pool counts as keys and values of
+ * zero and is recorded; a prefix_len or n_nodes out of range leaves the
  * sequence's outputs unwritten and is recorded.
  * Softmax statistics, partial outputs and their merge are held in 32 bits; the
  * softmax weights are rounded to the cache's dtype for the product with v.

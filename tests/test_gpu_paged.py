@@ -378,6 +378,25 @@ def test_attention_of_large_batches(cuda_device, B, hi, N, Hq, Hkv, D, page, dty
         pu.check_attention(out, lse, ref, dtype, D)
 
 
+def test_calls_on_a_stream_ahead_of_the_current_one(cuda_device):
+    """What a call allocates itself -- the workspace's zeros above all -- is on its
+    own stream: the current one may be far behind."""
+    c = _attn_case(8, [5000] * 20, 64, 32, 8, 128, 16, BF16)
+    rot = ops.Rotary(128)
+    pos = torch.arange(20 * 65, device="cuda").int().view(20, 65)
+    want = ops.tree_attn_paged(**c)
+    want_q, want_k = ops.rope(c["q"], c["k_tree"], pos, rot)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)                # ~10 ms of the current stream
+    out, lse = ops.tree_attn_paged(**c, stream=side)
+    q, k = ops.rope(c["q"], c["k_tree"], pos, rot, stream=side)
+    side.synchronize()
+    ops.ddtree_device_check()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(q, want_q) and torch.equal(torch.nan_to_num(k), torch.nan_to_num(want_k))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_attention_random_shapes(cuda_device, seed):
     """Seeded shapes over the whole range, rows kernel and general kernel, one CTA

@@ -133,6 +133,11 @@ def test_rope_refusals():
     assert _rope(k=_rows()) == 1                        # k without k_out
     assert _rope(ko=_rows()) == 1
     assert _rope(dtype=1, q=_rows(data=0x10002)) == 1   # off the 4-byte grid
+    far, other = _rows(data=0x90000), _rows(data=0xa0000)
+    assert _rope(k=_rows(), ko=_rows()) == 1            # one tensor turned twice in place
+    assert _rope(qo=far, k=far, ko=other) == 1          # q_out is k
+    assert _rope(qo=other, k=far, ko=_rows()) == 1      # k_out is q
+    assert _rope(qo=other, k=far, ko=other) == 1        # one output for both
     assert _rope(T=0, pos=None) == 0                    # nothing to do
 
 
@@ -153,6 +158,10 @@ def test_append_refusals():
     assert _append(q=_rows()) == 1                      # q without q_out
     assert _append(qo=_rows()) == 1
     assert _append(rot=_rot(rot_dim=256)) == 1
+    assert _append(q=_rows(), qo=_rows()) == 1          # q is k: read while it is turned
+    assert _append(v=_rows(data=0x90000), k=_rows(data=0xa0000), q=_rows(),
+                   qo=_rows(data=0x90000)) == 1         # q_out is v
+    assert _append(k=_rows(data=0x10000), cache=_cache(k_pages=0x10000)) == 1
     assert _append(cache=_cache(D=600, page_stride=60000, head_stride=30000, slot_stride=600)) == 2
     assert _append(T=0, seq=None, pos=None) == 0
 
