@@ -45,7 +45,6 @@
 #include <vector>
 #include <tuple>
 #include <type_traits>
-#include <queue>
 #include <map>
 
 #include "tree_attn_common.cuh"
@@ -70,6 +69,10 @@ constexpr float kRescaleLog2 = 8.f;
 DDT_DEV uint32_t p_col(int kk) { return kk < 6 ? (uint32_t)(kk * 8) : (uint32_t)(96 + (kk - 6) * 8); }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSplits = 16;  // KV splits of one unit = CTAs of one cluster
+constexpr int kMinSplit = 32;       // (many units) key tiles of a split, at least
+constexpr int kWays = 3;            // ways of cutting a paged batch's lists that are weighed
+constexpr int kRankedSeqs = 96;     // ... sequences, at most
+static_assert(kWays * kRankedSeqs <= kThreads, "a thread a sequence and way");
 constexpr int kLptMaxItems = 128;  // (sequence, split) items ranked in each CTA, at most
 // How the KV splits of a unit combine: a single split stores directly; few
 // units run each unit's splits as one cluster and merge on chip; many units
@@ -127,6 +130,8 @@ struct PagedParams : Params {
     int num_pages, ps_log2;  // pages of the pool; log2(positions per page)
     int npt;                 // nodes per query tile, at most BM / G
     int single;              // a unit is one query tile, not a pair
+    int share;               // key tiles of a split per 2^16 tiles of the longest list
+    int sms;                 // of the device
 };
 
 // Named barrier over the 256 softmax threads (both query tiles).
@@ -157,6 +162,103 @@ constexpr int kChunk4 = 2 * BM * 16;
 template <int D>
 constexpr bool merge_fits(int S) {
     return S * (chunk_slots<D>(S) * kChunk4 + Cfg<D>::ML_BYTES) <= Cfg<D>::SMEM - 1024;
+}
+
+// A table is as wide as the longest sequence it may ever hold, so a paged batch's
+// lists are cut here, where their lengths are known: not at all, at the plan's
+// share of the longest one, or at its thirds.  A job -- a piece of a sequence's
+// list, for one of its `jobs` units -- costs its tiles and 3, and 8 more for the
+// merge if the list is cut; started longest first it begins at (cost of the jobs
+// before it) / SMs at the latest.  The way whose latest end comes first is taken.
+// Longest first puts the whole pieces before all others, in the sequences' order,
+// and then one job of each sequence, its last piece or its list, by length: a
+// thread a sequence and way goes over those.
+// Against the plan's share alone, cut from a table exactly as wide as the longest
+// list (us, 8 KV heads, G = 4, D = 128, bf16): 16 sequences of 1K to 32K, N = 128
+// 518 -> 500, N = 127 355 -> 364; 30 of 100 to 16K, N = 100 381 -> 329; 8 of 32K 495 ->
+// 500; and under a table 4 times as wide 8 of 32K 624 -> 505.
+// Returns the sequence, piece and tiles per piece of the item of rank `rk`, -1 if
+// there is none.  `smem` is the kernel's dynamic shared memory, before its first copy
+// is issued.  Not inlined: inside the kernel it cost the issuing warps' loops their
+// uniform registers (long context 2.56 -> 3.68 ms).
+__device__ __noinline__ int3 ranked_item(const int32_t* prefix_len, const int32_t* n_nodes, int B, int N,
+                                         int64_t cap, int jobs, int smax, int share, int sms, int rk,
+                                         uint8_t* smem) {
+    __shared__ int s_end[kWays], s_item[2];
+    float* s_cost = reinterpret_cast<float*>(smem);                       // [kWays][kRankedSeqs]
+    int* s_whole = reinterpret_cast<int*>(s_cost + kWays * kRankedSeqs);  // [kWays][kRankedSeqs]
+    constexpr int kLanes = kRankedSeqs / 32;
+    const int tid = threadIdx.x, my_way = tid / kRankedSeqs, i = tid % kRankedSeqs;
+    const int ways = smax > 1 ? kWays : 1, Bp = (B + 3) & ~3;
+    // every warp reads all lengths, once and at once: this is before everything else
+    int P[kLanes], n[kLanes], tot = 0, longest = 1;
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) {
+        const int at = k * 32 + (tid & 31);
+        P[k] = at < B ? prefix_len[at] : -1;
+        n[k] = at < B ? n_nodes[at] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) {
+        const bool ok = P[k] >= 0 && P[k] <= cap && n[k] >= 0 && n[k] <= N;
+        const int t = ok ? (P[k] + BN - 1) / BN + (n[k] + BN) / BN : 0;
+        longest = max(longest, t);
+        if (i / 32 == k) tot = t;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    auto length = [&](int way) {
+        return way == 0 ? longest
+                        : max(kMinSplit, way == 1 ? (int)(((int64_t)longest * share + 65535) >> 16) : (longest + 2) / 3);
+    };
+    const bool mine = my_way < ways && i < Bp;
+    const int len = length(my_way);
+    // pieces of `len` before the last: no way has more pieces than the plan, at most 4
+    const int whole = (tot > len ? 1 : 0) + (tot > 2 * len ? 1 : 0) + (tot > 3 * len ? 1 : 0);
+    const float cost = i < B ? (tot > 0 ? (float)(tot - whole * len + (whole ? 11 : 3)) : 0.f) : -1.f;
+    if (mine) {
+        s_cost[tid] = cost;
+        s_whole[tid] = whole;
+    }
+    if (tid < kWays) s_end[tid] = tid < ways ? 0 : INT32_MAX;
+    if (tid < 2) s_item[tid] = -1;
+    __syncthreads();
+    int rank = 0, wholes = 0, wholes_before = 0;
+    if (mine && i < B) {
+        float before = 0.f;
+        for (int j0 = 0; j0 < Bp; j0 += 4) {
+            const float4 c4 = *(const float4*)&s_cost[my_way * kRankedSeqs + j0];
+            const int4 w4 = *(const int4*)&s_whole[my_way * kRankedSeqs + j0];
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+            const int w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool first = c[k] > cost || (c[k] == cost && j0 + k < i);
+                rank += first ? 1 : 0;
+                before += first ? c[k] : 0.f;
+                wholes += w[k];
+                wholes_before += j0 + k < i ? w[k] : 0;
+            }
+        }
+        // (ends times SMs)
+        const float one = (float)(len + 11), all = one * wholes;
+        float end = (all + before) * jobs + cost * (jobs - 1 + sms);
+        if (wholes) end = fmaxf(end, all * jobs + one * (sms - 1));
+        atomicMax(&s_end[my_way], __float_as_int(end));  // (not negative: ordered as ints)
+    }
+    __syncthreads();
+    int way = 0;
+#pragma unroll
+    for (int w = 1; w < kWays; ++w)
+        if (s_end[w] < s_end[way]) way = w;
+    if (mine && i < B && my_way == way) {
+        if (rk >= wholes_before && rk < wholes_before + whole) {
+            s_item[0] = i, s_item[1] = rk - wholes_before;
+        } else if (rk == wholes + rank) {
+            s_item[0] = i, s_item[1] = whole;
+        }
+    }
+    __syncthreads();  // (and no copy lands in the scratch while it is read)
+    return make_int3(s_item[0], s_item[1], length(way));
 }
 
 // One CTA = one (sequence b, KV head g, pair of 128-row query tiles, KV split).
@@ -257,8 +359,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         b = idx / p.Hkv;
     }
     const int R = p.N + 1, G = p.G;
+    int tps = p.tps;
     pdl_wait();
-    if (p.merge != kMergeCluster && p.lpt) {
+    if constexpr (PAGED) {
+        if (p.merge != kMergeCluster && p.lpt) {
+            const int3 x = ranked_item(p.prefix_len, p.n_nodes, p.B, p.N, p.cache_cap,
+                                       p.Hkv * p.mpairs, p.smax, p.share, p.sms, idx / p.Hkv, smem_raw);
+            if (x.x < 0) {
+                free_tmem();
+                return;
+            }
+            b = x.x, split = x.y, tps = x.z;
+        }
+    } else if (p.merge != kMergeCluster && p.lpt) {
         // (dynamic shared memory is free until the first copy below is issued)
         int* s_w = reinterpret_cast<int*>(smem_raw);  // [kLptMaxItems] key tiles
         int* s_perm = s_w + kLptMaxItems;              // [kLptMaxItems] item of rank r
@@ -289,6 +402,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         split = item - b * p.smax;
         __syncthreads();  // (the scratch is read before any copy lands there)
     }
+    if constexpr (PAGED) {
+        // One number a warp, which the compiler then keeps in uniform registers: as
+        // they were, the 70B-class long context took 2.77 ms, shuffled 2.58, reduced 2.56.
+        b = __reduce_max_sync(0xffffffffu, b);
+        split = __reduce_max_sync(0xffffffffu, split);
+        tps = __reduce_max_sync(0xffffffffu, tps);
+    }
     const int P = p.prefix_len[b];
     const int n = p.n_nodes[b];
     if (P < 0 || P > p.cache_cap || n < 0 || n > p.N) {  // (the whole cluster exits here)
@@ -299,7 +419,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     const int npt = (P + BN - 1) / BN;      // prefix tiles
     const int ntt = (n + 1 + BN - 1) / BN;  // tree tiles
-    int tps = p.tps;
     int nodes_per_tile = BM / G;
     if constexpr (PAGED) {
         nodes_per_tile = p.npt;
@@ -1263,17 +1382,17 @@ long lpt_span(long units, int T, int tps, int sms) {
     std::vector<long> sizes;
     for (int s0 = 0; s0 < T; s0 += tps) sizes.push_back(std::min(T, s0 + tps) - s0 + 2);
     std::sort(sizes.begin(), sizes.end(), std::greater<long>());
-    std::priority_queue<long, std::vector<long>, std::greater<long>> sm;
-    for (int i = 0; i < sms; ++i) sm.push(0);
-    long span = 0;
+    std::map<long, long> sm{{0, sms}};  // load -> SMs that have it: equal pieces go out together
     for (const long z : sizes)
-        for (long u = 0; u < units; ++u) {
-            const long e = sm.top() + z;
-            sm.pop();
-            sm.push(e);
-            span = std::max(span, e);
+        for (long left = units; left > 0;) {
+            const auto [load, idle] = *sm.begin();
+            const long take = std::min(idle, left);
+            sm.erase(sm.begin());
+            if (take < idle) sm[load] = idle - take;
+            sm[load + z] += take;
+            left -= take;
         }
-    return span;
+    return sm.rbegin()->first;
 }
 
 // Many units fill the GPU without clusters: split only long tile lists, into
@@ -1287,8 +1406,8 @@ long lpt_span(long units, int T, int tps, int sms) {
 Plan plan_many(const Plan& base, Tiles t, long units, int sms) {
     Plan pl = base;
     const int T = t.prefix + t.tree;
-    pl.tps = T > 64 ? std::max(32, (T + 3) / 4) : T;
-    if (T > 64 && pl.tps > 32) {
+    pl.tps = T > 64 ? std::max(kMinSplit, (T + 3) / 4) : T;
+    if (T > 64 && pl.tps > kMinSplit) {
         static std::mutex mu;
         static std::map<std::tuple<int, long, int>, int> cache;
         std::lock_guard<std::mutex> lock(mu);
@@ -1315,6 +1434,12 @@ Plan plan_many(const Plan& base, Tiles t, long units, int sms) {
     pl.merge = pl.smax > 1 ? kMergeGlobal : kMergeNone;
     return pl;
 }
+
+// The same over a paged cache, where only the kernel knows how far the lists fall
+// short of the table: it takes the plan's share of the longest list (or cuts
+// otherwise, see there), and so the plan is made for kPlanTiles tiles at most.
+constexpr int kPlanTiles = 2048;
+Tiles planned(Tiles t) { return {std::min(t.prefix, kPlanTiles), t.tree}; }
 
 // Few units: split each unit's tiles over a cluster of S CTAs, with the fewest
 // tiles per split (at least 2) for which every unit's cluster is resident at

@@ -20,7 +20,7 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     const int sms = num_sms();
     PagedPlan pl{};
     if (units >= sms) {
-        (Plan&)pl = plan_many(base, t, units, sms);
+        (Plan&)pl = plan_many(base, planned(t), units, sms);
         pl.npt = BM / G;
     } else {
         pl = plan_paged_few(a.B, a.N, G, Hkv, t, sms, [&](int S) {
@@ -49,7 +49,12 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     p.B = a.B; p.N = a.N; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.W = (a.N + 1 + 31) / 32;
     p.mtiles = pl.mtiles; p.mpairs = pl.mpairs; p.tps = pl.tps; p.smax = pl.smax;
     p.merge = pl.merge;
-    p.lpt = (pl.merge != kMergeCluster && (long)a.B * pl.smax <= kLptMaxItems) ? 1 : 0;
+    const int64_t plan_tiles = planned(t).prefix + t.tree, table_tiles = t.prefix + t.tree;
+    p.share = (int)((pl.tps * (int64_t)65536 + plan_tiles - 1) / plan_tiles);
+    p.sms = sms;
+    p.lpt = (pl.merge != kMergeCluster && a.B <= kRankedSeqs) ? 1 : 0;
+    if (pl.merge == kMergeGlobal && !p.lpt)  // not ranked: the plan's share of the table
+        p.tps = (int)((pl.tps * table_tiles + plan_tiles - 1) / plan_tiles);
     p.cache_cap = cap;
     p.scale_log2 = a.scale * kLog2e;
     p.err = a.err;
@@ -74,7 +79,7 @@ size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t 
     const Plan base = plan_base(N, Hq, Hkv);
     const long units = plan_units(base, B, Hkv);
     if (units < num_sms()) return 0;
-    return attn_layout(plan_many(base, max_tiles(N, cache_cap), units, num_sms()), B, Hkv, D, 4).total;
+    return attn_layout(plan_many(base, planned(max_tiles(N, cache_cap)), units, num_sms()), B, Hkv, D, 4).total;
 }
 
 cudaError_t launch_tree_attn_paged(const PagedAttnArgs& a, cudaStream_t s) {

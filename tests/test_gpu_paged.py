@@ -378,6 +378,25 @@ def test_attention_of_large_batches(cuda_device, B, hi, N, Hq, Hkv, D, page, dty
         pu.check_attention(out, lse, ref, dtype, D)
 
 
+@pytest.mark.parametrize("lens,width", [
+    ([5000, 9, 4000, 700] * 5, 4096),        # ranked by length, splits of the longest list
+    ([8300] * 8 + [0, 127, 128], 1 << 16),   # a table for a million positions
+    ([300] * 12, 4096),                      # no list worth a split
+    ([5000, 0, 60] * 40, 2048),              # too many to rank: thirds of the table
+])
+def test_attention_under_wide_tables(cuda_device, lens, width):
+    """Tables far wider than the longest sequence, many query tiles; the workspace
+    serves other lengths after that."""
+    c = _attn_case(len(lens), lens, 64, 32, 8, 128, 16, BF16, width=width)
+    ws = ops.paged_attn_workspace(c["q"], c["cache"])
+    for shift in range(2):
+        if shift:
+            c["prefix_len"] = c["prefix_len"] - torch.clamp(c["prefix_len"] // 2, max=1500)
+        out, lse = ops.tree_attn_paged(**c, workspace=ws)
+        ops.ddtree_device_check()
+        pu.check_attention(out, lse, _ref(c), BF16, 128)
+
+
 def test_calls_on_a_stream_ahead_of_the_current_one(cuda_device):
     """What a call allocates itself -- the workspace's zeros above all -- is on its
     own stream: the current one may be far behind."""
