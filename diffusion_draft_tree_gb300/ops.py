@@ -32,8 +32,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error
           4: "kernel recorded bad device data or a timeout"}
 
 
-# The structs of include/ddtree.h, packed with the platform's own alignment.
-_pack_rows = struct.Struct("@Piqq").pack              # ddtree_rows
+# Structs of include/ddtree.h, packed with the platform's own alignment.
 _pack_cache = struct.Struct("@PPiiiiiqqqPiq").pack    # ddtree_paged_cache
 _pack_rotary = struct.Struct("@Piif4x").pack          # ddtree_rotary
 

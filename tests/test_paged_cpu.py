@@ -2,6 +2,7 @@
 against their formulas, and every refusal of a bad argument before a launch."""
 import ctypes
 import math
+import struct
 
 import pytest
 
@@ -85,7 +86,7 @@ def test_turns_are_fractions_of_a_turn():
 
 
 def _rows(data=0x10000, heads=2, ts=256, hs=128):
-    return ops._pack_rows(data, heads, ts, hs)
+    return struct.pack("@Piqq", data, heads, ts, hs)  # ddtree_rows
 
 
 def _cache(**kw):
