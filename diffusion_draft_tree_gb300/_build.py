@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libddtree.so")
 BINDING = os.path.join(PKG, "_ddtree.so")
 SOURCES = ["api.cu", "topk.cu", "build.cu", "build_level.cu", "tree_attn.cu", "accept.cu",
-           "accept_path.cu", "commit.cu", "rotary.cu", "tree_attn_paged.cu",
+           "accept_path.cu", "commit.cu", "rotary.cu", "tree_attn_paged.cu", "tree_attn_left.cu",
            "tree_attn_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

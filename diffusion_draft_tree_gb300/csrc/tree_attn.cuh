@@ -104,8 +104,13 @@ struct Cfg {
     }
 };
 
-// Where the prefix lives, and the 16-bit type of everything.
-constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2;
+// Where the prefix lives, and the 16-bit type of everything; LEFT: with two warps for
+// the rows that the query tiles leave over.
+constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4;
+constexpr bool is_left(int mode) { return mode >= kLeftBf16; }
+constexpr bool is_f16(int mode) { return mode == kPagedFp16 || mode == kLeftFp16; }
+constexpr int threads_of(int mode) { return kThreads + (is_left(mode) ? 64 : 0); }
+constexpr int kLeftRows = 8;  // rows left over, at most: the narrow side of mma.sync
 
 struct Params {
     const int32_t* prefix_len;
@@ -132,6 +137,13 @@ struct PagedParams : Params {
     int single;              // a unit is one query tile, not a pair
     int share;               // key tiles of a split per 2^16 tiles of the longest list
     int sms;                 // of the device
+    // rows left over by the query tiles (LEFT): those of the last nodes, the first of
+    // which is mtiles npt
+    int left;                // their number
+    const uint16_t* q;       // the queries, in rows
+    int64_t q_ts, q_hs;
+    float* part_left;        // global merge: [B*Hkv][smax][kLeftRows][D + 4] O, m, l
+    unsigned int* tickets_left;  // ... [B*Hkv]
 };
 
 // Named barrier over the 256 softmax threads (both query tiles).
@@ -261,6 +273,273 @@ __device__ __noinline__ int3 ranked_item(const int32_t* prefix_len, const int32_
     return make_int3(s_item[0], s_item[1], length(way));
 }
 
+// The rows that a unit's query tiles leave over, at most kLeftRows (N + 1 nodes with N
+// a power of two: one node's G rows).  As a query tile of their own, a CTA's lone
+// tile, they cost 0.8 of what 256 rows do; here two warps more take them along on
+// mma.sync, from the K and V tiles that the pairs read anyway.  The key tiles go round
+// the pairs: mma.sync runs beside the pair's tcgen05 products at 32 cycles a product
+// and scheduler, so that a tile takes these warps 3.6 thousand cycles where the pair
+// needs 2.8 (left out, the products gave 434 us instead of 497 at one pair a unit, the
+// shared-memory reads nothing).  Rows are the products' narrow side, S^T = K Q^T and
+// O^T += V^T P^T, 8 rows wide instead of 16; 4 warps would leave 128 registers a
+// thread.  Warp w takes keys [64 w, 64 w + 64) of a tile, its scores, weights,
+// statistics and outputs in registers; K is let go after the scores, V after the
+// products, and the copies wait for these warps as for the tensor core.  The two
+// meet in shared memory, and the pairs and splits in the workspace: the last of
+// them, by an atomic ticket, joins their parts in order.
+// us against a lone tile (D = 128, bf16, 8 KV heads, G = 4): 16 sequences of 1K to 32K,
+// N = 128 498 -> 421; 8 of 32K 500 -> 412; 16 of 20K, N = 64 428 -> 378; 60 of up to
+// 16K, N = 64 622 -> 500.
+struct LeftArgs {
+    const uint16_t* q;  // row 0 (the first node's first head), and from there by strides
+    int64_t q_ts, q_hs;
+    const uint32_t* mask;  // its ancestor words
+    uint16_t* out;
+    float* lse;
+    float* part;  // [split][mpair][kLeftRows][D + 4]
+    unsigned int* ticket;
+    uint64_t *kfull, *kempty, *vfull, *vempty;
+    uint8_t *sk, *sv;
+    volatile int* abort;
+    int W, Hq, G, rows, nodes;  // nodes: live ones among them, may be <= 0
+    int n, P, t_begin, nprefix, nt, tree_first, split, splits, mpair, mpairs;
+    float sl2;
+    uint32_t* err;
+};
+
+// Named barrier over the two warps.
+DDT_DEV void left_bar() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
+
+template <int D, bool F16>
+__device__ __noinline__ void left_rows(const LeftArgs& a) {
+    using C = Cfg<D>;
+    constexpr int NS = C::NS, NH = C::NH;
+    __shared__ __align__(16) float s_o[2][kLeftRows][D + 4];
+    __shared__ float2 s_ml[2][kLeftRows];
+    __shared__ int s_state;  // bit w: warp w gave up; bit 2: the last part
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 1, t = threadIdx.x & 63;
+    const int r0 = 2 * (lane & 3), r1 = r0 + 1, u0 = r0 / a.G, u1 = r1 / a.G;  // two rows, their nodes
+    const bool live0 = r0 < a.rows && u0 < a.nodes, live1 = r1 < a.rows && u1 < a.nodes;
+    if (t == 0) s_state = 0;
+    uint32_t q[D / 16][2];  // Q^T, the right operand: row lane / 4
+    const int rq = lane >> 2, uq = rq / a.G;
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(a.q + uq * a.q_ts + (rq - uq * a.G) * a.q_hs);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            q[kk][e] = rq < a.rows && uq < a.nodes ? __ldg(row + kk * 8 + e * 4 + (lane & 3)) : 0u;
+    float o[D / 16][4];  // O^T: columns 16 i + lane / 4 (+ 8), rows r0, r1
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    left_bar();
+    bool ok = true;
+    int turn = a.t_begin % a.mpairs;
+    for (int j = 0; j < a.nt; ++j) {
+        const int s = j % NS;
+        const bool mine = a.nodes > 0 && turn == a.mpair;
+        if (++turn == a.mpairs) turn = 0;
+        const bool tree = j >= a.nprefix;
+        const int a0 = (a.tree_first + j - a.nprefix) * BN;
+        // keys of the warp's 64 that exist, and of those the ones that the rows see
+        const int lim = (tree ? a.n + 1 - a0 : a.P - (a.t_begin + j) * BN) - 64 * w;
+        if (!mine || lim <= 0) {  // (a tile is let go once it is there: one arrival a copy)
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.kfull[s], (j / NS) & 1, a.abort)))) break;
+            if (lane == 0) mbar_arrive(&a.kempty[s]);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.vfull[s], (j / NS) & 1, a.abort)))) break;
+            if (lane == 0) mbar_arrive(&a.vempty[s]);
+            continue;
+        }
+        const bool whole = !tree && lim >= 64;
+        uint32_t see0[2], see1[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int rem = lim - 32 * c;
+            see0[c] = see1[c] = rem >= 32 ? ~0u : (rem <= 0 ? 0u : (1u << rem) - 1u);
+            if (tree) {
+                const int word = a0 / 32 + 2 * w + c;
+                see0[c] &= live0 && word < a.W ? __ldg(&a.mask[u0 * a.W + word]) : 0u;
+                see1[c] &= live1 && word < a.W ? __ldg(&a.mask[u1 * a.W + word]) : 0u;
+            }
+        }
+        // ---- scores, S^T = K Q^T: 4 blocks of 16 keys --------------------------------------
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.kfull[s], (j / NS) & 1, a.abort)))) break;
+        const uint32_t ka = smem_u32(a.sk) + s * C::KV_BYTES, va = smem_u32(a.sv) + s * C::KV_BYTES;
+        float x[4][4];
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[kg][e] = 0.f;
+        {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t f[4][4];
+#pragma unroll
+                for (int kg = 0; kg < 4; ++kg)
+                    ldsm_x4(ka + (kk >> 2) * kHalfBytes +
+                                swz(64 * w + kg * 16 + (lane & 15), (kk & 3) * 2 + (lane >> 4)),
+                            f[kg]);
+#pragma unroll
+                for (int kg = 0; kg < 4; ++kg) mma16816<F16>(x[kg], f[kg], q[kk][0], q[kk][1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a.kempty[s]);
+        // ---- weights: keys 16 kg + lane / 4 (+ 8) of rows r0, r1 ------------------------------
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = x[kg][e] * a.sl2;
+                const uint32_t see = e & 1 ? see1[kg >> 1] : see0[kg >> 1];
+                if (!whole && !((see >> ((kg & 1) * 16 + (lane >> 2) + (e >> 1) * 8)) & 1u)) v = -INFINITY;
+                x[kg][e] = v;
+                if (e & 1) mx1 = fmaxf(mx1, v);
+                else mx0 = fmaxf(mx0, v);
+            }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+        }
+        const bool up0 = mx0 > m0 + kRescaleLog2, up1 = mx1 > m1 + kRescaleLog2;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float f0 = up0 ? fast_exp2(m0 - mx0) : 1.f, f1 = up1 ? fast_exp2(m1 - mx1) : 1.f;
+            m0 = up0 ? mx0 : m0;
+            m1 = up1 ? mx1 : m1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                o[i][0] *= f0, o[i][2] *= f0;
+                o[i][1] *= f1, o[i][3] *= f1;
+            }
+        }
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        uint32_t pw[8];  // rounded to the cache's type and turned: keys by twos of row lane / 4
+#pragma unroll
+        for (int kb = 0; kb < 8; ++kb) {
+            const float e0 = fast_exp2(x[kb >> 1][2 * (kb & 1)] - b0), e1 = fast_exp2(x[kb >> 1][2 * (kb & 1) + 1] - b1);
+            l0 += e0;  // (the sums take them unrounded)
+            l1 += e1;
+            pw[kb] = movmatrix_t(pack16<F16>(e0, e1));
+        }
+        // ---- O^T += V^T P^T ---------------------------------------------------------------------
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.vfull[s], (j / NS) & 1, a.abort)))) break;
+        {
+            if (lim < 64) {  // rows of V past the sequence may hold anything, and 0 x NaN is NaN
+                for (int c = lane; c < (64 - lim) * NH * 8; c += 32) {
+                    const int key = 64 * w + lim + c / (NH * 8), h = (c >> 3) % NH;
+                    *(uint4*)(a.sv + s * C::KV_BYTES + h * kHalfBytes + key * 128 + (c & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();  // (the next copy into the stage comes after)
+                __syncwarp();
+            }
+#pragma unroll
+            for (int x4 = 0; x4 < 4 * NH; ++x4) {  // keys 16 (x4 / NH) .., columns 64 (x4 % NH) ..
+                const int kg = x4 / NH, h = x4 % NH;
+                uint32_t f[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ldsm_x4_t(va + h * kHalfBytes +
+                                  swz(64 * w + kg * 16 + (lane >> 4) * 8 + (lane & 7), i * 2 + ((lane >> 3) & 1)),
+                              f[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma16816<F16>(o[4 * h + i], f[i], pw[2 * kg], pw[2 * kg + 1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a.vempty[s]);
+    }
+    if (!ok && lane == 0) {
+        record_error(a.err, ERR_ATTN | ERR_WAIT_TIMEOUT);
+        *a.abort = 1;
+        atomicOr(&s_state, 1 << w);
+    }
+    auto finish = [&](int r, int c, float4 v, float M, float L) {
+        const bool live = r / a.G < a.nodes && L > 0.f;
+        const float inv = live ? 1.f / L : 0.f;
+        uint2 y = make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv));
+        if (!live) y = make_uint2(0, 0);
+        const size_t at = (size_t)(r / a.G) * a.Hq + r % a.G;
+        reinterpret_cast<uint2*>(a.out + at * D)[c] = y;
+        if (c == 0 && a.lse) a.lse[at] = live ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+    };
+    if (a.nodes <= 0) {  // every row is padding: zeros, once
+        for (int i = t; a.mpair == 0 && a.split == 0 && i < a.rows * (D / 4); i += 64)
+            finish(i / (D / 4), i % (D / 4), make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
+        return;
+    }
+    // ---- the two halves of the keys meet --------------------------------------------------------
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_o[w][e & 1 ? r1 : r0][16 * i + (lane >> 2) + (e >> 1) * 8] = o[i][e];
+    if (lane < 4) {
+        s_ml[w][r0] = make_float2(m0, l0);
+        s_ml[w][r1] = make_float2(m1, l1);
+    }
+    left_bar();
+    const bool fine = (s_state & 3) == 0;
+    const int parts = a.splits * a.mpairs, part = a.split * a.mpairs + a.mpair;
+    if (fine) {
+        for (int i = t; i < a.rows * (D / 4); i += 64) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            const float2 ml0 = s_ml[0][r], ml1 = s_ml[1][r];
+            const float M = fmaxf(ml0.x, ml1.x), ref = M == -INFINITY ? 0.f : M;
+            const float f0 = fast_exp2(ml0.x - ref), f1 = fast_exp2(ml1.x - ref);
+            const float4 x = *(const float4*)&s_o[0][r][4 * c], y = *(const float4*)&s_o[1][r][4 * c];
+            const float4 v = make_float4(f0 * x.x + f1 * y.x, f0 * x.y + f1 * y.y, f0 * x.z + f1 * y.z,
+                                         f0 * x.w + f1 * y.w);
+            const float L = f0 * ml0.y + f1 * ml1.y;
+            if (parts == 1) {
+                finish(r, c, v, M, L);
+            } else {
+                float* to = a.part + ((size_t)part * kLeftRows + r) * (D + 4);
+                *(float4*)&to[4 * c] = v;
+                if (c == 0) *(float2*)&to[D] = make_float2(M, L);
+            }
+        }
+    }
+    if (parts == 1) return;
+    __threadfence();
+    left_bar();
+    // (every part takes its ticket, so that the counter returns to zero)
+    if (t == 0 && ticket_is_last(a.ticket, (unsigned)parts)) atomicOr(&s_state, 4);
+    left_bar();
+    if (!fine || !(s_state & 4)) return;
+    for (int i = t; i < a.rows * (D / 4); i += 64) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float M = -INFINITY, L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int s = 0; s < parts; ++s)
+            M = fmaxf(M, __ldcg(&a.part[((size_t)s * kLeftRows + r) * (D + 4) + D]));
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float* from = a.part + ((size_t)s * kLeftRows + r) * (D + 4);
+            const float2 ml = __ldcg((const float2*)&from[D]);
+            const float4 x = __ldcg((const float4*)&from[4 * c]);
+            const float f = fast_exp2(ml.x - ref);
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+            L = fmaf(f, ml.y, L);
+        }
+        finish(r, c, v, M, L);
+    }
+}
+
 // One CTA = one (sequence b, KV head g, pair of 128-row query tiles, KV split).
 // Warp 0: TMA producer.  Warp 1: TMEM owner and MMA issuer.  Warps 2-5: softmax
 // of query tile 0; warps 6-9: softmax of query tile 1.  Per KV tile j the
@@ -271,14 +550,14 @@ __device__ __noinline__ int3 ranked_item(const int32_t* prefix_len, const int32_
 // A unit's key tiles are its prefix tiles followed by its tree tiles; split s
 // takes tiles [s tps, (s+1) tps) of that list.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(MODE), 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc,
                  const __grid_constant__ CUtensorMap tm_kt,
                  const __grid_constant__ CUtensorMap tm_vt,
                  const std::conditional_t<MODE == kDense, Params, PagedParams> p) {
     using C = Cfg<D>;
-    constexpr bool PAGED = MODE != kDense, F16 = MODE == kPagedFp16;
+    constexpr bool PAGED = MODE != kDense, F16 = is_f16(MODE), LEFT = is_left(MODE);
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
@@ -296,11 +575,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // ---- set-up that reads no global memory (overlaps the previous kernel) -------
     if (tid == 0) {
         mbar_init(&bar_q, 1);
+        constexpr int readers = LEFT ? 3 : 1;  // the tensor core, and two warps for the rows left over
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar_kfull[s], 1);
-            mbar_init(&bar_kempty[s], 1);
+            mbar_init(&bar_kempty[s], readers);
             mbar_init(&bar_vfull[s], 1);
-            mbar_init(&bar_vempty[s], 1);
+            mbar_init(&bar_vempty[s], readers);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&bar_sfull[k][0], 1);
@@ -435,9 +715,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int u00 = mt0 * nodes_per_tile, u01 = mt1 * nodes_per_tile;
     const bool has1 = tile1 && (u01 <= n);      // ... and holds a live node
     // The last query tile of an odd count (R G = 128 m + G r, e.g. N + 1 nodes with
-    // N a power of two) is alone: both softmax groups then work on it, each on
+    // N a power of two), unless its few rows are taken along (LEFT), is alone: both softmax groups then work on it, each on
     // one 64-key half of every key tile, and merge their (m, l, O) at the end.
-    const bool dual = !tile1;
+    const bool dual = !LEFT && !tile1;
     const bool two = has1 || dual;              // two S / P / O groups in flight
     // A lone tile's scores take 64 of each group's 128 columns.  The paged forms use
     // the others for the next key tile, whose product then runs while this one is
@@ -451,7 +731,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto phase_of = [&](int j) { return (uint32_t)(ahead == 2 ? j >> 1 : j) & 1u; };
     if (u00 > n) {  // every query row of both tiles is padding: zeros, once
         if (split == 0) {
-            for (int r = tid; r < 2 * BM; r += kThreads) {
+            for (int r = tid; r < 2 * BM; r += threads_of(MODE)) {
                 int u = u00 + r / G, h = g * G + r % G;
                 if constexpr (PAGED) {
                     const int rr = r % BM;
@@ -648,6 +928,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         }
         if (!ok) fail();
+    } else if (LEFT && warp >= 10) {
+        if constexpr (LEFT) {
+            const int u = p.mtiles * nodes_per_tile;  // the first node left over
+            const size_t unit = (size_t)b * p.Hkv + g, row = ((size_t)b * R + u) * p.Hq + g * G;
+            LeftArgs a;
+            a.q = p.q + ((int64_t)b * R + u) * p.q_ts + (int64_t)g * G * p.q_hs;
+            a.q_ts = p.q_ts, a.q_hs = p.q_hs;
+            a.mask = p.anc_mask + ((size_t)b * R + u) * p.W;
+            a.out = p.out + row * D;
+            a.lse = p.lse ? p.lse + row : nullptr;
+            a.part = p.part_left + unit * p.smax * p.mpairs * (kLeftRows * (D + 4));
+            a.ticket = p.tickets_left + unit;
+            a.kfull = bar_kfull, a.kempty = bar_kempty, a.vfull = bar_vfull, a.vempty = bar_vempty;
+            a.sk = sk, a.sv = sv;
+            a.abort = &s_abort;
+            a.W = p.W, a.Hq = p.Hq, a.G = G, a.rows = p.left, a.nodes = n - u + 1;
+            a.n = n, a.P = P, a.t_begin = t_begin, a.nprefix = nprefix, a.nt = nt;
+            a.tree_first = tree_first, a.split = split, a.splits = splits;
+            a.mpair = mpair, a.mpairs = p.mpairs;
+            a.sl2 = p.scale_log2;
+            a.err = p.err;
+            left_rows<D, F16>(a);
+        }
     } else {
         // ==================== softmax / epilogue, one thread per query row ====================
         const int k = (warp - 2) >> 2;            // query tile of this group
@@ -1121,7 +1424,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_before();
     __syncthreads();
     pdl_trigger();
-    if constexpr (PAGED) {
+    if constexpr (PAGED && !LEFT) {
         if (p.merge == kMergeCluster && splits > 1) {
             // Every rank of the cluster merges its chunks of the head dimension for
             // all rows, idle ranks too: each split's threads store their rows'
@@ -1500,20 +1803,47 @@ PagedPlan plan_paged_few(int B, int N, int G, int Hkv, Tiles t, int sms, Active 
     return best;
 }
 
+// The plan of a paged batch's many units, with the rows that the query tiles leave over
+// taken along by the pairs (`left` of them) where that is one operand's worth.
+struct ManyPlan : Plan {
+    int left;
+};
+ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms) {
+    ManyPlan pl{};
+    (Plan&)pl = plan_base(N, Hq, Hkv);
+    const int G = Hq / Hkv, left = (N + 1 - (pl.mtiles - 1) * (BM / G)) * G;
+    if (plan_units(pl, B, Hkv) < sms) return pl;  // few units (smax = 0)
+    if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows) {
+        --pl.mtiles;
+        --pl.mpairs;
+        pl.left = left;
+    }
+    (Plan&)pl = plan_many(pl, planned(t), plan_units(pl, B, Hkv), sms);
+    return pl;
+}
+
 struct WsLayout {
-    size_t tickets, part_o, part_ml, total;
+    size_t tickets, part_o, part_ml, tickets_left, part_left, total;
 };
 
 // Workspace of the global merge (empty for the other plans); a partial output
 // takes `elem` bytes a value.
-WsLayout attn_layout(const Plan& pl, int B, int Hkv, int D, int elem) {
+WsLayout attn_layout(const Plan& pl, int B, int Hkv, int D, int elem, int left = 0) {
     WsLayout w{};
-    if (pl.merge != kMergeGlobal) return w;
+    if (pl.merge != kMergeGlobal && !(left && pl.mpairs > 1)) return w;
     const size_t tiles = (size_t)B * Hkv * pl.mtiles;  // partials per query tile
-    w.tickets = 0;  // one counter per (sequence, KV head, tile pair)
-    w.part_o = align_up((size_t)B * Hkv * pl.mpairs * 4, 256);
-    w.part_ml = align_up(w.part_o + tiles * pl.smax * (size_t)D * BM * elem, 256);
-    w.total = align_up(w.part_ml + tiles * pl.smax * 2 * BM * 4, 256);
+    if (pl.merge == kMergeGlobal) {
+        w.tickets = 0;  // one counter per (sequence, KV head, tile pair)
+        w.part_o = align_up((size_t)B * Hkv * pl.mpairs * 4, 256);
+        w.part_ml = align_up(w.part_o + tiles * pl.smax * (size_t)D * BM * elem, 256);
+        w.total = align_up(w.part_ml + tiles * pl.smax * 2 * BM * 4, 256);
+    }
+    if (left) {  // (merged over the splits and the pairs)
+        const size_t heads = (size_t)B * Hkv;
+        w.tickets_left = w.total;
+        w.part_left = align_up(w.tickets_left + heads * 4, 256);
+        w.total = align_up(w.part_left + heads * pl.smax * pl.mpairs * kLeftRows * (D + 4) * 4, 256);
+    }
     return w;
 }
 

@@ -397,6 +397,53 @@ def test_attention_under_wide_tables(cuda_device, lens, width):
         pu.check_attention(out, lse, _ref(c), BF16, 128)
 
 
+@pytest.mark.parametrize("N,G,D,dtype,hi,width", [
+    (64, 4, 128, BF16, 5000, None),    # one pair a unit and one node, lists cut
+    (64, 4, 64, FP16, 900, None),      # ... whole
+    (65, 4, 128, FP16, 700, 512),      # two nodes left over
+    (128, 4, 128, BF16, 9000, None),   # two pairs share the key tiles
+    (256, 8, 64, BF16, 300, None),     # eight pairs, lists shorter than that
+    (32, 8, 128, BF16, 4000, 4096),    # 8 rows
+    (84, 3, 128, FP16, 2000, None),    # tiles of 126 rows
+    (263, 1, 128, BF16, 600, None),    # eight nodes of one row
+    (128, 1, 64, FP16, 100, None),     # a single row; one list of a tile or two
+])
+def test_attention_rows_left_over(cuda_device, N, G, D, dtype, hi, width):
+    """A few rows more than whole query tiles: prefixes of any length, last nodes that
+    are there, that are not, and trees too small for a pair; a workspace for all."""
+    B, Hkv = 22, 8
+    lens = [(hi - 41 * b) % (hi + 1) if b % 4 else b // 4 for b in range(B)]
+    lens[3] = hi
+    live = [N if b % 3 else [N - 1, N // 2, 0, N][b // 3 % 4] for b in range(B)]
+    c = _attn_case(N + G, lens, N, Hkv * G, Hkv, D, 16, dtype, live=live, width=width)
+    c["anc_mask"][5, N] = 0                       # a last node that sees its prefix alone ...
+    c["prefix_len"][5] = 0                        # ... and has none
+    ws = ops.paged_attn_workspace(c["q"], c["cache"])
+    first = None
+    for _ in range(3):
+        out, lse = ops.tree_attn_paged(**c, workspace=ws)
+        ops.ddtree_device_check()
+        if first is None:
+            pu.check_attention(out, lse, _ref(c), dtype, D)
+            assert bool((out[5, N] == 0).all()) and bool((lse[5, N] == -np.inf).all())
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])   # bit for bit
+    # captured twice over one workspace, replayed in turn
+    outs = [torch.full_like(out, 7.0) for _ in range(2)]
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.ddtree_tree_attn_paged(c["q"], c["cache"], c["k_tree"], c["v_tree"], c["prefix_len"],
+                                       c["n_nodes"], c["anc_mask"], o, workspace=ws)
+        graphs.append(g)
+    for g in graphs * 2:
+        g.replay()
+    torch.cuda.synchronize()
+    ops.ddtree_device_check()
+    assert torch.equal(outs[0], first[0]) and torch.equal(outs[1], first[0])
+
+
 def test_calls_on_a_stream_ahead_of_the_current_one(cuda_device):
     """What a call allocates itself -- the workspace's zeros above all -- is on its
     own stream: the current one may be far behind."""
