@@ -28,15 +28,17 @@
 // one-lane branch a tile's four products took 3.1 to 3.8 thousand cycles where
 // the tensor core needs 2.5; this way they take 2.8 (128-key tiles, D = 128).
 //
-// The kernel comes in three forms.  kDense reads the prefix from one block per
+// The kernel comes in several forms.  kDense reads the prefix from one block per
 // sequence.  kPagedBf16 / kPagedFp16 read it from pages: a 128-key tile is
 // 128 / page_size copies, one page each, into the same swizzled tile, so nothing
 // behind them changes.  These forms also keep a split's partial output in 32 bits
 // when splits are merged, sum the unrounded weights (the logsumexp then keeps 32
 // bits however few the keys), write -inf over the scores that a row does not see
 // instead of masking in the softmax (one code path), take any G <= 128 (a query
-// tile holds up to floor(128 / G) nodes) and cut a sequence's tiles over its whole
-// cluster by its own length rather than by the table's capacity.
+// tile holds up to floor(128 / G) nodes) and cut a sequence's tiles by its own
+// length rather than by the table's capacity.  kLeftBf16 / kLeftFp16 are those for
+// many units with two warps more, for a few rows that whole pairs of tiles leave
+// over (left_rows).
 #pragma once
 
 #include <mutex>

@@ -22,7 +22,7 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     if (many.smax) {
         (Plan&)pl = many;
         pl.npt = BM / G;
-    } else {
+    } else if constexpr (!is_left(MODE)) {
         pl = plan_paged_few(a.B, a.N, G, Hkv, t, sms, [&](int S) {
             return merge_fits<D>(S) ? active_clusters<D, MODE>(dev, S) : 0;
         });
