@@ -467,18 +467,26 @@ ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_
 
 namespace {
 
-// One warp waits, through the bounded wait every kernel of the library uses, on
-// an mbarrier that nothing arrives on; when the bound passes it records the
-// timeout in the error word and returns, as a kernel whose copy never landed
-// does.
+// Two warps wait, through the bounded wait every kernel of the library uses, on
+// an mbarrier that nothing arrives on.  When the first one's bound passes it sets
+// the abort flag, which ends the second one's wait, and both leave as whole warps,
+// as a kernel whose copy never landed does; the timeout is recorded in the error
+// word.
 __global__ void selftest_wait_kernel(uint64_t limit_ns, uint32_t* err) {
     __shared__ __align__(8) uint64_t bar;
+    __shared__ volatile int s_abort;
     if (threadIdx.x == 0) {
         ddt::sm100::mbar_init(&bar, 1);
         ddt::sm100::mbar_init_fence();
+        s_abort = 0;
     }
-    __syncwarp();
-    if (threadIdx.x == 0 && !ddt::sm100::mbar_wait(&bar, 0, nullptr, limit_ns))
+    __syncthreads();
+    const bool first = threadIdx.x < 32;
+    const bool ok = first ? ddt::sm100::mbar_wait_warp(&bar, 0, &s_abort, limit_ns)
+                          : ddt::sm100::mbar_wait_warp(&bar, 0, &s_abort);
+    if (first && !ok) s_abort = 1;
+    const int gave_up = __syncthreads_count(!ok);
+    if (threadIdx.x == 0 && gave_up == (int)blockDim.x)
         ddt::record_error(err, ddt::ERR_SELFTEST | ddt::ERR_WAIT_TIMEOUT);
 }
 
@@ -488,7 +496,7 @@ ddtree_status ddtree_selftest_wait(uint32_t limit_us, void* stream) {
     if (limit_us < 1 || limit_us > 1000000) return DDTREE_ERR_INVALID_ARG;
     uint32_t* err = error_word();
     if (!err) return DDTREE_ERR_CUDA;
-    selftest_wait_kernel<<<1, 32, 0, (cudaStream_t)stream>>>((uint64_t)limit_us * 1000ull, err);
+    selftest_wait_kernel<<<1, 64, 0, (cudaStream_t)stream>>>((uint64_t)limit_us * 1000ull, err);
     return launched(cudaGetLastError());
 }
 

@@ -63,6 +63,14 @@ DDT_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
+// The same by all lanes of a warp that then go the same way.  Each lane polls for
+// itself, and once a wait has run out elsewhere one lane may see the barrier where
+// another sees the abort flag: the vote makes it one answer, so that a warp that gives
+// up leaves its loop, with its warp-wide instructions, as a whole.
+DDT_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                            uint64_t limit_ns = 2000000000ull) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
+}
 
 // ---- TMA (bulk tensor copy global -> shared, completes on an mbarrier) -----------
 // Issued by the lane of a whole warp whose `lead` is set (elect_one, below).

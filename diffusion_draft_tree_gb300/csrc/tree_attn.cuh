@@ -349,9 +349,9 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
         // keys of the warp's 64 that exist, and of those the ones that the rows see
         const int lim = (tree ? a.n + 1 - a0 : a.P - (a.t_begin + j) * BN) - 64 * w;
         if (!mine || lim <= 0) {  // (a tile is let go once it is there: one arrival a copy)
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.kfull[s], (j / NS) & 1, a.abort)))) break;
+            if (!(ok = mbar_wait_warp(&a.kfull[s], (j / NS) & 1, a.abort))) break;
             if (lane == 0) mbar_arrive(&a.kempty[s]);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.vfull[s], (j / NS) & 1, a.abort)))) break;
+            if (!(ok = mbar_wait_warp(&a.vfull[s], (j / NS) & 1, a.abort))) break;
             if (lane == 0) mbar_arrive(&a.vempty[s]);
             continue;
         }
@@ -368,7 +368,7 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
             }
         }
         // ---- scores, S^T = K Q^T: 4 blocks of 16 keys --------------------------------------
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.kfull[s], (j / NS) & 1, a.abort)))) break;
+        if (!(ok = mbar_wait_warp(&a.kfull[s], (j / NS) & 1, a.abort))) break;
         const uint32_t ka = smem_u32(a.sk) + s * C::KV_BYTES, va = smem_u32(a.sv) + s * C::KV_BYTES;
         float x[4][4];
 #pragma unroll
@@ -431,7 +431,7 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
             pw[kb] = movmatrix_t(pack16<F16>(e0, e1));
         }
         // ---- O^T += V^T P^T ---------------------------------------------------------------------
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&a.vfull[s], (j / NS) & 1, a.abort)))) break;
+        if (!(ok = mbar_wait_warp(&a.vfull[s], (j / NS) & 1, a.abort))) break;
         {
             if (lim < 64) {  // rows of V past the sequence may hold anything, and 0 x NaN is NaN
                 for (int c = lane; c < (64 - lim) * NH * 8; c += 32) {
@@ -564,7 +564,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
         bar_vempty[NS], bar_sfull[2][2],
-        bar_pfull[2][2], bar_odone[2][2], bar_recv;
+        bar_pfull[2][2], bar_odone[2][2], bar_recv, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
@@ -593,6 +593,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bar_odone[k][1], 1);
         }
         mbar_init(&bar_recv, 1);
+        mbar_init(&bar_drain, 1);
         s_abort = 0;
         mbar_init_fence();
         tma_prefetch_desc(&tm_q);
@@ -838,7 +839,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const CUtensorMap* map = v ? &tm_vc : &tm_kc;
                 uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
                 const uint32_t to = smem_u32(v ? sv : sk) + s * C::KV_BYTES;
-                ok = mbar_wait(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
+                ok = mbar_wait_warp(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
                 __syncwarp();
@@ -889,7 +890,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t kd = smem_desc_sw128(smem_u32(sk), 16, 1024);
         const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
         const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
-        bool ok = mbar_wait(&bar_q, 0, &s_abort);
+        bool ok = mbar_wait_warp(&bar_q, 0, &s_abort);
 #pragma unroll 1
         for (int j = -ahead; ok && j < nt; ++j) {
             const int jq = j + ahead;  // the tile whose scores follow
@@ -898,8 +899,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint32_t s_k = tmem + k * BN;
                 if (j >= 0) {
                     const int s = j % NS;
-                    ok = mbar_wait(&bar_pfull[k][bar_of(j)], phase_of(j), &s_abort);
-                    if (k == 0) ok = ok && mbar_wait(&bar_vfull[s], (j / NS) & 1, &s_abort);
+                    ok = mbar_wait_warp(&bar_pfull[k][bar_of(j)], phase_of(j), &s_abort);
+                    if (k == 0) ok = ok && mbar_wait_warp(&bar_vfull[s], (j / NS) & 1, &s_abort);
                     tc_fence_after();
                     const uint64_t b0 = vd + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half;
                     const uint32_t d0 = tmem + 256 + k * D, a0 = s_k + buffer(j);
@@ -914,7 +915,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 if (ok && jq < nt) {
                     const int s = jq % NS;
-                    if (k == 0) ok = mbar_wait(&bar_kfull[s], (jq / NS) & 1, &s_abort);
+                    if (k == 0) ok = mbar_wait_warp(&bar_kfull[s], (jq / NS) & 1, &s_abort);
                     tc_fence_after();
                     const uint64_t a0 = qd + k * q_tile;
                     const uint64_t b0 = kd + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half;
@@ -930,6 +931,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         }
         if (!ok) fail();
+        // (where a wait gave up, here or in another warp, no product may still read
+        // memory given back; otherwise the last tile's commit says the same)
+        mma_commit_warp(lead, &bar_drain);
+        mbar_wait(&bar_drain, 0, nullptr, 100000000ull);
     } else if (LEFT && warp >= 10) {
         if constexpr (LEFT) {
             const int u = p.mtiles * nodes_per_tile;  // the first node left over
@@ -999,7 +1004,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = true;
         for (int j = 0; work && j < nt; ++j) {
             const int s = j % NS;
-            if (!mbar_wait(&bar_sfull[k][bar_of(j)], phase_of(j), &s_abort)) { fail(); ok = false; break; }
+            if (!mbar_wait_warp(&bar_sfull[k][bar_of(j)], phase_of(j), &s_abort)) { fail(); ok = false; break; }
             const uint32_t tm_s = tm_s0 + buffer(j);
             tc_fence_after();
             // ---- validity of the tile's keys: one 32-bit mask per 32 columns ----
@@ -1085,7 +1090,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // O_k is stable here: the commit that signalled S_k covers the
                 // previous tile's P_k V product -- unless scores run two tiles ahead.
                 if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) {
-                    if (ahead == 2 && !mbar_wait(&bar_odone[k][bar_of(j - 1)], phase_of(j - 1), &s_abort)) { fail(); ok = false; break; }
+                    if (ahead == 2 && !mbar_wait_warp(&bar_odone[k][bar_of(j - 1)], phase_of(j - 1), &s_abort)) { fail(); ok = false; break; }
                     tc_fence_after();
                     rescale_o(factor);
                 }
@@ -1197,24 +1202,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tmem_st_wait();
             l += sum;
-            if (k == 0 && !key_r_valid) {
+            if (k == 0 && quarter * 32 + 32 > lim_t) {  // (the warp as a whole)
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
-                if (!mbar_wait(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
+                if (!mbar_wait_warp(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
                 uint8_t* vrow = sv + s * C::KV_BYTES + r * 128;
+                if (!key_r_valid) {
 #pragma unroll
-                for (int h = 0; h < C::NH; ++h)
+                    for (int h = 0; h < C::NH; ++h)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *(uint4*)(vrow + h * kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+                        for (int i = 0; i < 8; ++i)
+                            *(uint4*)(vrow + h * kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
             }
             tc_fence_before();
             mbar_arrive(&bar_pfull[k][bar_of(j)]);
         }
 
         // ---- epilogue (every softmax thread runs the same barrier sequence) ----
-        if (work && ok && !mbar_wait(&bar_odone[k][bar_of(nt - 1)], phase_of(nt - 1), &s_abort)) { fail(); ok = false; }
+        if (work && ok && !mbar_wait_warp(&bar_odone[k][bar_of(nt - 1)], phase_of(nt - 1), &s_abort)) { fail(); ok = false; }
         // (paged splits in a cluster: everything up to the exchange stays where it is)
         const bool exchange = PAGED && p.merge == kMergeCluster && splits > 1;
         if (exchange) s_ml[k * BM + r] = make_float2(m_run, l);
@@ -1585,7 +1592,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool mine = (k == 0) || has1;
                 const bool row_out = (k == 0 || tile1) && u < R;
                 const bool row_valid = mine && u <= n;
-                if (!mbar_wait(&bar_recv, 0, nullptr) && lane == 0)
+                if (!mbar_wait_warp(&bar_recv, 0, nullptr) && lane == 0)
                     record_error(p.err, ERR_ATTN | ERR_WAIT_TIMEOUT);
                 const float2* mls[kMaxSplits];
                 const uint4* prt[kMaxSplits];  // chunk c_lo of each split's slice

@@ -275,20 +275,20 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const bool first = t == t_begin || at.tile == 0, tree = at.tile == at.tiles - 1;
             const int key0 = at.tile * kTile;
             const int boxes = tree ? 0 : min(nb, (prefix_of(at) - key0 + box - 1) / box);
-            bool ok = true;  // (all lanes wait, so that the warp stays in one piece)
+            bool ok = true;  // (of the warp as a whole)
             if (first) {
-                ok = mbar_wait(&bar_qempty, (units & 1) ^ 1, &s_abort);
+                ok = mbar_wait_warp(&bar_qempty, (units & 1) ^ 1, &s_abort);
                 if (ok) {
                     if (lane == 0) mbar_arrive_expect_tx(&bar_qfull, NH * p.rows * 128);
                     __syncwarp();
                     for (int h = 0; h < NH; ++h)
                         tma_load_3d_warp(lead, smem_u32(sq) + h * C::QSLAB, &tm_q, &bar_qfull, 64 * h,
                                          at.g * p.G, at.b * R);
+                    ++units;
                 }
-                ++units;
             }
-            ok = ok && mbar_wait(&bar_empty[s], ((it / NS) & 1) ^ 1, &s_abort);
-            if (__any_sync(0xffffffffu, !ok)) { fail(); break; }
+            ok = ok && mbar_wait_warp(&bar_empty[s], ((it / NS) & 1) ^ 1, &s_abort);
+            if (!ok) { fail(); break; }
             if (lane == 0)
                 mbar_arrive_expect_tx(&bar_full[s], 2 * NH * 128 * (tree ? R : boxes * box));
             __syncwarp();
@@ -316,6 +316,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             issued = it + 1;
         }
         // (where a wait gave up, here or below, no copy may land in memory given back)
+        if (units > 0) mbar_wait(&bar_qfull, (units - 1) & 1, nullptr, 100000000ull);
         for (int it = max(0, issued - NS); it < issued; ++it)
             mbar_wait(&bar_full[it % NS], (it / NS) & 1, nullptr, 100000000ull);
         return;
@@ -342,7 +343,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         uint32_t qf[D / 16][4];
         // A wait that gives up ends the unit's products, not its barriers: the warps
         // stay together.
-        bool ok = mbar_wait(&bar_qfull, units & 1, &s_abort);
+        bool ok = mbar_wait_warp(&bar_qfull, units & 1, &s_abort);
         if (!ok) fail();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -360,7 +361,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const int it0 = (int)(t - t_begin), it = it0 + left - 1;  // the unit's tiles of the run
         for (int k = 0; ok && k < left; ++k) {
             const int s = (it0 + k) % NS;
-            ok = mbar_wait(&bar_full[s], ((it0 + k) / NS) & 1, &s_abort);
+            ok = mbar_wait_warp(&bar_full[s], ((it0 + k) / NS) & 1, &s_abort);
             if (!ok) { fail(); break; }
             const bool tree = has_tree && k == left - 1;
             const int lim = tree ? n + 1 : min(kTile, P - (at.tile + k) * kTile);

@@ -449,9 +449,9 @@ ddtree_status ddtree_device_check(void* stream, uint32_t* detail);
  * tensor core, for another warp's results) is bounded in wall time: when the
  * bound passes, the kernel records "a bounded wait timed out" in the device
  * error word and unwinds, leaving the CUDA context usable.  This call enqueues
- * one warp that waits, through that same bounded wait, on a barrier that
- * nothing ever signals, with the bound shortened to limit_us microseconds
- * (1 .. 1000000).  A later ddtree_device_check() returns DDTREE_ERR_DEVICE
+ * two warps that wait, through that same bounded wait, on a barrier that
+ * nothing ever signals: one with the bound shortened to limit_us microseconds
+ * (1 .. 1000000), the other until the first one's abort reaches it.  A later ddtree_device_check() returns DDTREE_ERR_DEVICE
  * with detail 0x0F000004; nothing faults and the wait always ends.
  * Returns DDTREE_ERR_INVALID_ARG for a limit out of range. */
 ddtree_status ddtree_selftest_wait(uint32_t limit_us, void* stream);

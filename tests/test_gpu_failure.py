@@ -7,6 +7,7 @@ timeout, the error word must clear, and the CUDA context must still serve a
 normal call afterwards.  Nothing here faults a GPU; the wait always ends."""
 import numpy as np
 import pytest
+import torch
 
 import oracle
 from diffusion_draft_tree_gb300 import ops
@@ -42,3 +43,19 @@ def test_selftest_rejects_limits_out_of_range(cuda_device):
             ops.ddtree_selftest_wait(bad)
         assert e.value.status == 1
     ops.ddtree_device_check()
+
+
+def test_an_abort_ends_the_other_warps_wait(cuda_device):
+    """The second warp's own bound is 2 s; the first one's, 50 ms, ends both, and
+    both reach the CTA's barrier as whole warps."""
+    ops.ddtree_selftest_wait(1000)  # (loads the kernel)
+    with pytest.raises(ops.DDTreeError):
+        ops.ddtree_device_check()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    ops.ddtree_selftest_wait(50000)
+    end.record()
+    with pytest.raises(ops.DDTreeError) as e:
+        ops.ddtree_device_check()
+    assert e.value.detail == SELFTEST_TIMEOUT
+    assert 49.0 < begin.elapsed_time(end) < 1000.0

@@ -1,0 +1,37 @@
+"""Rules that the attention kernels' sources keep so that no warp is divided and no
+memory is read too early -- mistakes that show on a GPU as a hang or as wrong
+values now and then, and so are looked for in the text."""
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "diffusion_draft_tree_gb300", "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_waits_that_decide_a_branch_are_the_whole_warps():
+    """mbar_wait answers a lane; where its answer decides what a warp does next the
+    warp has to vote (mbar_wait_warp), or lanes that saw the abort flag leave
+    lanes that saw the barrier alone at the next warp-wide instruction."""
+    for name in ("tree_attn.cuh", "tree_attn_rows.cu"):
+        text = _source(name)
+        assert text.count("mbar_wait_warp(") >= 4
+        for m in re.finditer(r"\bmbar_wait\(", text):
+            before = text[:m.start()].rstrip()
+            # a drain at a role's end: the answer is not used
+            assert before.endswith((";", ")", "{", "}")), (name, text[m.start() - 60:m.end() + 40])
+
+
+def test_copies_and_products_in_flight_are_drained():
+    """Every barrier that a copy or a product may still signal when a wait gives up
+    is waited for before its role ends."""
+    tree, rows = _source("tree_attn.cuh"), _source("tree_attn_rows.cu")
+    for bar in ("bar_q", "bar_drain", "v ? &bar_vfull[j % NS] : &bar_kfull[j % NS]"):
+        bar = bar if bar.startswith("v ?") else "&" + bar
+        assert re.search(r"[;){}]\s*mbar_wait\(" + re.escape(bar) + r",[^;]*nullptr, 100000000ull\);", tree), bar
+    for bar in ("&bar_qfull", "&bar_full[it % NS]"):
+        assert re.search(r"[;){}]\s*mbar_wait\(" + re.escape(bar) + r",[^;]*nullptr, 100000000ull\);", rows), bar
