@@ -271,7 +271,10 @@ __device__ __noinline__ int3 ranked_item(const int32_t* prefix_len, const int32_
             s_item[0] = i, s_item[1] = whole;
         }
     }
-    __syncthreads();  // (and no copy lands in the scratch while it is read)
+    // Copies land in the scratch next, by another proxy: what was stored there comes
+    // before them only through this fence, and the barrier for what was read.
+    fence_proxy_async_smem();
+    __syncthreads();
     return make_int3(s_item[0], s_item[1], length(way));
 }
 
@@ -683,7 +686,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int item = s_perm[idx / p.Hkv];
         b = item / p.smax;
         split = item - b * p.smax;
-        __syncthreads();  // (the scratch is read before any copy lands there)
+        fence_proxy_async_smem();  // (copies land in the scratch next: see ranked_item)
+        __syncthreads();
     }
     if constexpr (PAGED) {
         // One number a warp, which the compiler then keeps in uniform registers: as

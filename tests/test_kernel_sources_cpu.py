@@ -35,3 +35,16 @@ def test_copies_and_products_in_flight_are_drained():
         assert re.search(r"[;){}]\s*mbar_wait\(" + re.escape(bar) + r",[^;]*nullptr, 100000000ull\);", tree), bar
     for bar in ("&bar_qfull", "&bar_full[it % NS]"):
         assert re.search(r"[;){}]\s*mbar_wait\(" + re.escape(bar) + r",[^;]*nullptr, 100000000ull\);", rows), bar
+
+
+def test_scratch_under_the_tiles_is_fenced_before_copies():
+    """Shared memory that ordinary stores filled and copies fill next: the copies are
+    another proxy's, which a CTA barrier alone does not put behind the stores."""
+    text = _source("tree_attn.cuh")
+    ranked = text[text.index("int3 ranked_item("):text.index("struct LeftArgs")]
+    dense = text[text.index("int* s_perm"):text.index("if constexpr (PAGED)", text.index("int* s_perm"))]
+    for part in (ranked, dense):
+        barriers = [m.start() for m in re.finditer(r"__syncthreads\(\)", part)]
+        last_store = max(m.start() for m in re.finditer(r"s_(cost|whole|w|perm)\[[^\]]*\] = ", part))
+        fence = part.rindex("fence_proxy_async_smem()")
+        assert last_store < fence < barriers[-1]
