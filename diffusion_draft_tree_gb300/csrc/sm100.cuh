@@ -231,13 +231,18 @@ DDT_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[15])
         : "memory");
 }
-DDT_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// After tmem_ld_wait(): ties the loaded registers to a point after the wait,
-// so that no use of them is scheduled between the load and the wait (the
-// load writes them asynchronously).
-DDT_DEV void tmem_ld_fence(uint32_t (&r)[32]) {
+// Waits for this thread's tensor-memory loads, which write their registers
+// asynchronously.  The wait names every register that it is for: as in-out operands
+// behind it, they cannot be used by anything that is scheduled before it.
+template <typename... Regs>
+DDT_DEV void tmem_ld_wait(Regs&... loaded) {
+    static_assert(sizeof...(Regs) > 0, "name the registers that are waited for");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    auto tie = [](uint32_t (&r)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    };
+    (tie(loaded), ...);
 }
 DDT_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 

@@ -996,8 +996,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t t[32];
                 tmem_ld32(tm_o + c * 32, t);
-                tmem_ld_wait();
-                tmem_ld_fence(t);
+                tmem_ld_wait(t);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     t[i] = __float_as_uint(__uint_as_float(t[i]) * factor);
@@ -1033,8 +1032,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const int rem = lim - 32 * c, w = c + key0 / 32;
                         uint32_t see = rem >= 32 ? ~0u : (rem <= 0 ? 0u : ((1u << rem) - 1u));
                         if (is_tree) see &= w < 2 ? (w == 0 ? am[0] : am[1]) : (w == 2 ? am[2] : am[3]);
-                        tmem_ld_wait();
-                        tmem_ld_fence(t);
+                        tmem_ld_wait(t);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!((see >> i) & 1u)) t[i] = 0xff800000u;
@@ -1069,21 +1067,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(q[i]));
                 };
                 tmem_ld32(tm_s, qa);
-                tmem_ld_wait();
-                tmem_ld_fence(qa);
+                tmem_ld_wait(qa);
                 tmem_ld32(tm_s + 32, qb);
                 qmax(qa);
-                tmem_ld_wait();
-                tmem_ld_fence(qb);
+                tmem_ld_wait(qb);
                 if (!dual) {
                     tmem_ld32(tm_s + 64, qa);
                     qmax(qb);
-                    tmem_ld_wait();
-                    tmem_ld_fence(qa);
+                    tmem_ld_wait(qa);
                     tmem_ld32(tm_s + 96, qb);
                     qmax(qa);
-                    tmem_ld_wait();
-                    tmem_ld_fence(qb);
+                    tmem_ld_wait(qb);
                 }
                 qmax(qb);
                 const float mt_raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -1124,16 +1118,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // the last quarter is still in qb: first, while quarter 0 loads
                 tmem_ld32(tm_s, qa);
                 qexp(qb, 3);
-                tmem_ld_wait();
-                tmem_ld_fence(qa);
+                tmem_ld_wait(qa);
                 tmem_ld32(tm_s + 32, qb);
                 qexp(qa, 0);
-                tmem_ld_wait();
-                tmem_ld_fence(qb);
+                tmem_ld_wait(qb);
                 tmem_ld32(tm_s + 64, qa);
                 qexp(qb, 1);
-                tmem_ld_wait();
-                tmem_ld_fence(qa);
+                tmem_ld_wait(qa);
                 qexp(qa, 2);
                 }
                 sum = acc.x + acc.y;
@@ -1145,7 +1136,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 uint32_t t[32], t2[32];
                 tmem_ld32(tm_s + 32 * c0, t);
                 tmem_ld32(tm_s + 32 * c0 + 32, t2);
-                tmem_ld_wait();
+                tmem_ld_wait(t, t2);
                 {
                     const uint32_t m = vm[c0], m2 = vm[c0 + 1];
 #pragma unroll
@@ -1175,7 +1166,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 uint32_t t0[32], t1[32], pk[32];
                 tmem_ld32(tm_s + half * 64, t0);
                 tmem_ld32(tm_s + half * 64 + 32, t1);
-                tmem_ld_wait();
+                tmem_ld_wait(t0, t1);
                 // few keys (partial or tree tile): the row sum takes exactly the
                 // bf16 weights the P V product sees
                 const uint32_t m0 = half ? vm[2] : vm[0], m1 = half ? vm[3] : vm[1];
@@ -1247,7 +1238,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 uint32_t t0[32], t1[32];
                 tmem_ld32(tm_o + c * 32, t0);
                 tmem_ld32(tm_o + D + c * 32, t1);
-                tmem_ld_wait();
+                tmem_ld_wait(t0, t1);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     t0[i] = __float_as_uint(w0 * __uint_as_float(t0[i]) + w1 * __uint_as_float(t1[i]));
@@ -1290,7 +1281,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tm_o + c * 32, t);
-                    tmem_ld_wait();
+                    tmem_ld_wait(t);
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = live ? __uint_as_float(t[i]) : 0.f;
@@ -1315,7 +1306,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tm_o + c * 32, t);
-                    tmem_ld_wait();
+                    tmem_ld_wait(t);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         part[(c * 4 + i) * 2 * BM + row2] = make_uint4(
@@ -1338,7 +1329,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tm_o + c * 32, t);
-                    tmem_ld_wait();
+                    tmem_ld_wait(t);
                     if (row_valid) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -1357,7 +1348,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tm_o + c * 32, t);
-                    tmem_ld_wait();
+                    tmem_ld_wait(t);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         po[(c * 16 + i) * BM + r] = pack_bf16x2(__uint_as_float(t[2 * i]) * inv,
@@ -1476,15 +1467,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (dual) {
                         uint32_t t1[32];
                         tmem_ld32(tm_o + D + c * 32, t1);
-                        tmem_ld_wait();
-                        tmem_ld_fence(t);
-                        tmem_ld_fence(t1);
+                        tmem_ld_wait(t, t1);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             t[i] = __float_as_uint(w0 * __uint_as_float(t[i]) + w1 * __uint_as_float(t1[i]));
                     } else {
-                        tmem_ld_wait();
-                        tmem_ld_fence(t);
+                        tmem_ld_wait(t);
                     }
                     if (row_valid) {
 #pragma unroll

@@ -48,3 +48,19 @@ def test_scratch_under_the_tiles_is_fenced_before_copies():
         last_store = max(m.start() for m in re.finditer(r"s_(cost|whole|w|perm)\[[^\]]*\] = ", part))
         fence = part.rindex("fence_proxy_async_smem()")
         assert last_store < fence < barriers[-1]
+
+
+def test_tensor_memory_loads_are_waited_for_by_name():
+    """A load from tensor memory writes its registers asynchronously: between it and
+    the wait that names them, nothing but other loads and stores uses them."""
+    text = _source("tree_attn.cuh")
+    waits = list(re.finditer(r"tmem_ld_wait\(([^)]*)\)", text))
+    assert len(waits) > 10 and all(m.group(1).strip() for m in waits)
+    loads = list(re.finditer(r"tmem_ld32\([^;]*, (\w+)\);", text))
+    assert loads
+    for m in loads:
+        name = m.group(1)
+        behind = next(w for w in waits if w.start() > m.end()
+                      and name in [x.strip() for x in w.group(1).split(",")])
+        between = text[m.end():behind.start()]
+        assert not re.search(r"\b%s\b" % name, between), (name, between)
