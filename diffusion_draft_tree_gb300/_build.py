@@ -41,16 +41,34 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_cmd(obj: str):
+def abi_key() -> str:
+    """What the module's object code depends on besides its sources: it reads torch's
+    tensors through inline C++ and is a module of this interpreter."""
+    import torch
+    return f"{torch.__version__}.{sysconfig.get_config_var('SOABI')}"
+
+
+def _linked_key() -> str:
+    try:
+        with open(os.path.join(OUT_DIR, "binding.linked")) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _binding_cmd(obj: str, key: str):
     from torch.utils import cpp_extension
     inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-w", *(f"-I{i}" for i in dict.fromkeys(inc)),
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-w", f'-DDDTREE_BUILT_FOR="{key}"', *(f"-I{i}" for i in dict.fromkeys(inc)),
             "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
 
 
-def _link_binding(obj: str):
+def _link_binding(obj: str, key: str):
     from torch.utils import cpp_extension
+    mark = os.path.join(OUT_DIR, "binding.linked")
+    if os.path.exists(mark):
+        os.remove(mark)
     tmp = BINDING + f".{os.getpid()}.tmp"
     dirs = cpp_extension.library_paths()
     r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-lddtree", "-Wl,-rpath,$ORIGIN",
@@ -60,6 +78,8 @@ def _link_binding(obj: str):
         print(r.stdout + r.stderr)
         raise RuntimeError("link of _ddtree.so failed")
     os.replace(tmp, BINDING)
+    with open(mark, "w") as f:
+        f.write(key)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -76,14 +96,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o]
             jobs.append(cmd)
-    # The module: again where its source, the header or the torch it was built
-    # against changed.
-    import torch
-    bind_obj = os.path.join(OUT_DIR, f"binding.{torch.__version__}.o")
+    # The module: again where its source, the header, or the torch or interpreter it
+    # was built against changed.  There is one module, so the key that it was linked
+    # for stands beside it: an older torch's object may be older than the module too.
+    key = abi_key()
+    bind_obj = os.path.join(OUT_DIR, f"binding.{key}.o")
     bind_src = [os.path.join(CSRC, "binding.cpp"), headers[-1]]
     new_binding = force or _stale(bind_obj, bind_src)
     if new_binding:
-        jobs.insert(0, _binding_cmd(bind_obj))
+        jobs.insert(0, _binding_cmd(bind_obj, key))
     cuda_jobs = len(jobs) - int(new_binding)
 
     def run(cmd):
@@ -105,8 +126,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link of libddtree.so failed")
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [bind_obj]):
-        _link_binding(bind_obj)
+    if force or _linked_key() != key or _stale(BINDING, [bind_obj]):
+        _link_binding(bind_obj, key)
     return LIB
 
 

@@ -298,4 +298,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ddtree", nullptr, -1, g_methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ddtree(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__ddtree(void) {
+    PyObject* m = PyModule_Create(&g_module);
+    // (the torch and interpreter whose headers it was compiled with: ops checks)
+    if (m && PyModule_AddStringConstant(m, "built_for", DDTREE_BUILT_FOR)) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

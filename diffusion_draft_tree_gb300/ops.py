@@ -96,7 +96,13 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-from . import _ddtree  # noqa: E402  (built beside libddtree.so, which it uses)
+from . import _build, _ddtree  # noqa: E402  (built beside libddtree.so, which it uses)
+
+if getattr(_ddtree, "built_for", None) != _build.abi_key():
+    # (it reads torch's tensors through their C++ layout)
+    raise ImportError(f"{_ddtree.__file__} was built for another torch or interpreter than "
+                      f"{_build.abi_key()}: build it again with "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`")
 
 EXPORTED = ("ddtree_workspace_size", "ddtree_topk", "ddtree_build", "ddtree_build_heap",
             "ddtree_tree_attn", "ddtree_accept", "ddtree_device_check", "ddtree_last_cuda_error",
