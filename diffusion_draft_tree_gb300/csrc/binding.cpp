@@ -9,6 +9,7 @@
 // status; a tensor that does not fit raises ValueError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -109,6 +110,25 @@ int32_t* token_ints(PyObject* o, const char* name, const Tensor& like, int64_t t
     return ints(o, name, like.sizes().slice(0, like.dim() - 2), index);
 }
 
+// The tensors that a call writes, behind autograd's back.  One that it differentiates
+// is refused, as torch refuses it for its own in-place and out= calls; the others'
+// versions go up, so that a backward pass that saved one of them notices.
+struct Written {
+    const Tensor* t[3] = {};
+    int n = 0;
+    void add(const Tensor& x, const char* name) {
+        if (x.requires_grad() && at::GradMode::is_enabled())
+            bad(std::string(name) + " requires grad and would be written without a graph: call under "
+                                    "torch.no_grad(), or on a detached tensor");
+        t[n++] = &x;
+    }
+    int done(int status) const {
+        for (int i = 0; i < n && status == DDTREE_OK; ++i)
+            if (!t[i]->is_inference()) t[i]->unsafeGetTensorImpl()->bump_version();
+        return status;
+    }
+};
+
 template <typename T>
 T packed(PyObject* o, const char* name) {
     T v;
@@ -161,10 +181,14 @@ int rope(PyObject* const* a) {
         bad("k_out without k");
     }
     const int32_t* pos = token_ints(a[2], "pos", q, qr.tokens, c.index);
+    Written w;
+    w.add(a[5] == Py_None ? q : tensor(a[5], "q_out"), a[5] == Py_None ? "q" : "q_out");
+    if (with_k) w.add(tensor(a[6] == Py_None ? a[1] : a[6], "k"), a[6] == Py_None ? "k" : "k_out");
     const Launch l(c.index, a[8]);
-    return ddtree_rope(&qr.r, &qo.r, with_k ? &kr.r : nullptr, with_k ? &ko.r : nullptr,
-                       code(c.dtype), (int)qr.tokens, (int)std::min<int64_t>(c.D, INT32_MAX), pos,
-                       &rot, PyObject_IsTrue(a[7]), l.stream);
+    return w.done(ddtree_rope(&qr.r, &qo.r, with_k ? &kr.r : nullptr, with_k ? &ko.r : nullptr,
+                              code(c.dtype), (int)qr.tokens,
+                              (int)std::min<int64_t>(c.D, INT32_MAX), pos, &rot,
+                              PyObject_IsTrue(a[7]), l.stream));
 }
 
 // The cache of a call and its pages' device and type.
@@ -180,7 +204,7 @@ Cache cache(PyObject* const* a) {
     return x;
 }
 
-// append(cache x 3, k, v, seq, pos, rotary, rotary_index, q, q_out, stream)
+// append(cache x 3, k, v, seq, pos, rotary, rotary_index, q, q_out, stream, k_pages, v_pages)
 int append(PyObject* const* a) {
     const Cache x = cache(a);
     a += 3;
@@ -209,10 +233,14 @@ int append(PyObject* const* a) {
     }
     const int32_t* seq = token_ints(a[2], "seq", k, kr.tokens, x.c.index);
     const int32_t* pos = token_ints(a[3], "pos", k, kr.tokens, x.c.index);
+    Written w;
+    w.add(tensor(a[9], "k_pages"), "k_pages");
+    w.add(tensor(a[10], "v_pages"), "v_pages");
+    if (with_q) w.add(tensor(a[7] == Py_None ? a[6] : a[7], "q"), a[7] == Py_None ? "q" : "q_out");
     const Launch l(x.c.index, a[8]);
-    return ddtree_append_paged(&kr.r, &vr.r, (int)kr.tokens, seq, pos, (int)x.B, &x.s,
-                               turn ? &rot : nullptr, with_q ? &qr.r : nullptr,
-                               with_q ? &qo.r : nullptr, l.stream);
+    return w.done(ddtree_append_paged(&kr.r, &vr.r, (int)kr.tokens, seq, pos, (int)x.B, &x.s,
+                                      turn ? &rot : nullptr, with_q ? &qr.r : nullptr,
+                                      with_q ? &qo.r : nullptr, l.stream));
 }
 
 // attn(cache x 3, q, k_tree, v_tree, prefix_len, n_nodes, anc_mask, out, lse, scale,
@@ -241,12 +269,16 @@ int attn(PyObject* const* a) {
     const auto* mask = (const uint32_t*)ints(a[5], "anc_mask", {B, R, (R + 31) / 32}, dev);
     const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)x.c.D) : PyFloat_AsDouble(a[8]);
     if (PyErr_Occurred()) bad("scale must be a number");
+    Written w;
+    w.add(tensor(a[6], "out"), "out");
+    if (lse) w.add(tensor(a[7], "lse"), "lse");
     const Launch l(dev, a[10]);
-    return ddtree_tree_attn_paged(&qr.r, &x.s, &kr.r, &vr.r, P, n, mask, (int)B, (int)(R - 1),
-                                  (float)scale, out, lse, ws, bytes, l.stream);
+    return w.done(ddtree_tree_attn_paged(&qr.r, &x.s, &kr.r, &vr.r, P, n, mask, (int)B, (int)(R - 1),
+                                         (float)scale, out, lse, ws, bytes, l.stream));
 }
 
-// commit(cache x 3, k_tree, v_tree, accept_len, accepted_nodes, prefix_len, new_len, stream)
+// commit(cache x 3, k_tree, v_tree, accept_len, accepted_nodes, prefix_len, new_len, stream,
+//        k_pages, v_pages)
 int commit(PyObject* const* a) {
     const Cache x = cache(a);
     a += 3;
@@ -262,9 +294,14 @@ int commit(PyObject* const* a) {
     const int32_t* acc = ints(a[3], "accepted_nodes", {x.B, L}, dev);
     const int32_t* P = ints(a[4], "prefix_len", {x.B}, dev);
     int32_t* to = a[5] == Py_None ? nullptr : ints(a[5], "new_len", {x.B}, dev);
+    Written w;
+    w.add(tensor(a[7], "k_pages"), "k_pages");
+    w.add(tensor(a[8], "v_pages"), "v_pages");
+    if (to) w.add(tensor(a[5], "new_len"), "new_len");
     const Launch l(dev, a[6]);
-    return ddtree_commit_paged(&x.s, &kr.r, &vr.r, alen, acc, P, to, (int)x.B,
-                               (int)std::min<int64_t>(L, INT32_MAX), (int)(kt.size(1) - 1), l.stream);
+    return w.done(ddtree_commit_paged(&x.s, &kr.r, &vr.r, alen, acc, P, to, (int)x.B,
+                                      (int)std::min<int64_t>(L, INT32_MAX), (int)(kt.size(1) - 1),
+                                      l.stream));
 }
 
 // The Python entry of one of these, `N` arguments; no C++ exception leaves it.
@@ -290,8 +327,8 @@ PyMethodDef method(const char* name) {
     return {name, (PyCFunction)(void (*)(void))entry<F, N>, METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<rope, 9>("rope"), method<append, 12>("append_paged"),
-                           method<attn, 14>("tree_attn_paged"), method<commit, 10>("commit_paged"),
+PyMethodDef g_methods[] = {method<rope, 9>("rope"), method<append, 14>("append_paged"),
+                           method<attn, 14>("tree_attn_paged"), method<commit, 12>("commit_paged"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ddtree", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -323,8 +323,10 @@ def accept(target_logits, tree: dict, L: int, temperature=0.0, seed=0, step=0, w
 # layout, a pool that interleaves keys and values.  Only the last dimension of a
 # tensor has to be contiguous.  Everything a call is given has to be on one
 # device, which need not be the current one; without `stream` it is enqueued on
-# that device's current stream.  The module _ddtree (csrc/binding.cpp) checks
-# and passes on the tensors.
+# that device's current stream.  No call records a gradient graph: a tensor that
+# is written may not require grad (outside torch.no_grad()), and its version goes up;
+# the gradient of a rotation is the call with inverse=True.  The module _ddtree
+# (csrc/binding.cpp) checks and passes on the tensors.
 
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
@@ -458,7 +460,8 @@ def ddtree_append_paged(k, v, seq, pos, cache: PagedCache, rotary: Optional[Rota
     written), and rotates their queries q, in place unless q_out is given."""
     turns, where = (None, None) if rotary is None else (rotary._c, rotary._index)
     st = _ddtree.append_paged(cache._c, cache._index, cache.B, k, v, seq, pos, turns, where, q,
-                              q_out, _raw("ddtree_append_paged", stream, cache._index))
+                              q_out, _raw("ddtree_append_paged", stream, cache._index), cache.k_pages,
+                              cache.v_pages)
     if st:
         raise DDTreeError("ddtree_append_paged", st)
 
@@ -505,6 +508,7 @@ def ddtree_commit_paged(cache: PagedCache, k_tree, v_tree, accept_len, accepted_
     prefix_len stays, new_len [B] receives prefix_len + accept_len + 1."""
     st = _ddtree.commit_paged(cache._c, cache._index, cache.B, k_tree, v_tree, accept_len,
                               accepted_nodes, prefix_len, new_len,
-                              _raw("ddtree_commit_paged", stream, cache._index))
+                              _raw("ddtree_commit_paged", stream, cache._index), cache.k_pages,
+                              cache.v_pages)
     if st:
         raise DDTreeError("ddtree_commit_paged", st)
