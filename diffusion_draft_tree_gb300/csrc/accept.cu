@@ -589,19 +589,6 @@ accept_kernel(const void* __restrict__ logits, int V, int64_t row_stride, int ns
     }
 }
 
-int num_sms_accept() {
-    static int cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!cached[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
 int accept_segs(int V, int dtype) {
     const int size = kSegBytes / (dtype == DDTREE_BF16 ? 2 : 4);
     return (V + size - 1) / size;
@@ -645,7 +632,7 @@ cudaError_t launch_one(const AcceptArgs& a, int nseg, bool aligned, float c_exp,
     // round-robin: every warp streams the same number of segments, and rows
     // complete wave by wave.
     const long segs = (long)a.B * R * nseg;
-    const long slots = (long)num_sms_accept();
+    const long slots = (long)num_sms();
     const long want = kChunksPerWarp * slots * (SAMPLE ? kWarps - 1 : kWarps);
     const long spc = std::max(1L, (segs + want - 1) / want);
     const long chunks = (segs + spc - 1) / spc;

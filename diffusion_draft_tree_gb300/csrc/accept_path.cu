@@ -405,9 +405,9 @@ int path_chunks(int V, int dtype) {
 // the size cannot be launched).
 template <bool BF16>
 int path_active_clusters(int dev, int size) {
-    static int cached[64][kMaxCluster + 1];
-    static bool done[64][kMaxCluster + 1];
-    if (!done[dev & 63][size]) {
+    static std::atomic<int> cached[64][kMaxCluster + 1];  // the number + 1; 0: not asked yet
+    int known = cached[dev & 63][size].load(std::memory_order_relaxed);
+    if (!known) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)size);
         cfg.blockDim = dim3(kThreads);
@@ -424,10 +424,10 @@ int path_active_clusters(int dev, int size) {
             n = 0;
             (void)cudaGetLastError();  // a refused size is not an error of the call
         }
-        cached[dev & 63][size] = n;
-        done[dev & 63][size] = true;
+        known = n + 1;
+        cached[dev & 63][size].store(known, std::memory_order_relaxed);
     }
-    return cached[dev & 63][size];
+    return known - 1;
 }
 
 // CTAs per sequence: the row's chunks spread evenly over up to kMaxCluster

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #define DDT_DEV __device__ __forceinline__
@@ -219,17 +220,18 @@ DDT_DEV int count_larger(const uint64_t* a, int n, uint64_t x) {
 }
 
 // Streaming multiprocessors of the current device (148 if the query fails).
+// (Looked up once per device; host threads may call at once.)
 inline int num_sms() {
-    static int cached[64];
+    static std::atomic<int> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!cached[dev]) {
-        int n = 0;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
             n = 148;
-        cached[dev] = n;
+        cached[dev].store(n, std::memory_order_relaxed);
     }
-    return cached[dev];
+    return n;
 }
 
 // ---------------------------------------------------------------------------

@@ -444,20 +444,6 @@ struct Plan {
     int grid;
 };
 
-// Streaming multiprocessors of the current device (148 if the query fails).
-int num_sms_topk() {
-    static int cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!cached[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
 int seg_count(int V, int dtype) {
     const int size = kSegBytes / (dtype == DDTREE_BF16 ? 2 : 4);
     return (V + size - 1) / size;
@@ -533,7 +519,7 @@ cudaError_t launch_stream(const TopkArgs& a, const Plan& p, bool aligned, TopkWs
 cudaError_t launch_topk(const TopkArgs& a, cudaStream_t s) {
     const int es = a.dtype == DDTREE_BF16 ? 2 : 4;
     const bool aligned = ((uintptr_t)a.logits % 16 == 0) && ((a.row_stride * es) % 16 == 0);
-    const Plan p = topk_plan(a.rows, a.V, a.dtype, num_sms_topk());
+    const Plan p = topk_plan(a.rows, a.V, a.dtype, num_sms());
     const WsLayout l = topk_layout(a.rows, a.V, a.dtype, a.K);
     char* base = (char*)a.ws;
     const TopkWs ws{(unsigned int*)(base + l.row_cnt), (unsigned long long*)(base + l.row_tau),

@@ -1852,10 +1852,10 @@ WsLayout attn_layout(const Plan& pl, int B, int Hkv, int D, int elem, int left =
 // (0 if that size cannot launch).  Needs the kernel's attributes set first.
 template <int D, int MODE>
 int active_clusters(int dev, int size) {
-    static int cached[64][kMaxSplits + 1];
-    static bool done[64][kMaxSplits + 1];
+    static std::atomic<int> cached[64][kMaxSplits + 1];  // the number + 1; 0: not asked yet
     if (size < 1 || size > kMaxSplits) return 0;
-    if (!done[dev & 63][size]) {
+    int known = cached[dev & 63][size].load(std::memory_order_relaxed);
+    if (!known) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)size);
         cfg.blockDim = dim3(kThreads);
@@ -1872,10 +1872,10 @@ int active_clusters(int dev, int size) {
             n = 0;
             (void)cudaGetLastError();  // a refused size is not an error of the call
         }
-        cached[dev & 63][size] = n;
-        done[dev & 63][size] = true;
+        known = n + 1;
+        cached[dev & 63][size].store(known, std::memory_order_relaxed);
     }
-    return cached[dev & 63][size];
+    return known - 1;
 }
 
 // Opts the kernel in to its shared memory and to clusters of 16, once per device.

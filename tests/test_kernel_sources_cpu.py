@@ -64,3 +64,17 @@ def test_tensor_memory_loads_are_waited_for_by_name():
                       and name in [x.strip() for x in w.group(1).split(",")])
         between = text[m.end():behind.start()]
         assert not re.search(r"\b%s\b" % name, between), (name, between)
+
+
+def test_tables_that_calls_fill_are_safe_for_threads():
+    """Function-local tables on the host, filled by the first call that needs an
+    entry: two host threads may be that call, and Arm may show one thread the flag
+    before the value."""
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith((".cu", ".cuh", ".h")):
+            continue
+        for m in re.finditer(r"^ +static (?!constexpr|_)([^;=(]*)[;=]", _source(name), re.M):
+            kind = m.group(1)
+            locked = kind.startswith(("std::once_flag", "std::atomic<", "std::mutex", "std::map<"))
+            # (filled inside a call_once)
+            assert locked or kind.startswith(("cudaError_t attr_err", "PFN_")), (name, kind)
