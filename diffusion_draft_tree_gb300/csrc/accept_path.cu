@@ -34,7 +34,7 @@ namespace ddt {
 
 namespace {
 
-constexpr int kThreads = kSampleThreads;
+constexpr int kThreads = 256;
 constexpr int kChunkBytes = 32768;
 constexpr int kMaxChunks = 128;
 constexpr int kMaxCluster = 16;

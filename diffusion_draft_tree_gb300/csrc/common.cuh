@@ -94,20 +94,6 @@ DDT_DEV uint64_t warp_sort_desc(uint64_t v) {
     return v;
 }
 
-// Both a and b sorted descending across the warp; returns the 32 largest of
-// their union, sorted descending.
-DDT_DEV uint64_t warp_merge_desc(uint64_t a, uint64_t b) {
-    const int lane = threadIdx.x & 31;
-    uint64_t rb = shfl_u64(b, 31 - lane);
-    uint64_t v = umax64(a, rb);  // bitonic
-#pragma unroll
-    for (int j = 16; j > 0; j >>= 1) {
-        uint64_t o = shfl_xor_u64(v, j);
-        v = ((lane & j) == 0) ? umax64(v, o) : umin64(v, o);
-    }
-    return v;
-}
-
 // 128-bit streaming global load that does not allocate in L1.
 DDT_DEV uint4 ld_stream_v4(const void* p) {
     uint4 r;

@@ -284,27 +284,6 @@ DDT_DEV void st_dsmem_f32x2(uint32_t caddr, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(caddr), "f"(v.x), "f"(v.y)
                  : "memory");
 }
-DDT_DEV uint4 ld_dsmem_u32x4(uint32_t caddr) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(caddr)
-                 : "memory");
-    return v;
-}
-DDT_DEV float2 ld_dsmem_f32x2(uint32_t caddr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                 : "=f"(v.x), "=f"(v.y)
-                 : "r"(caddr)
-                 : "memory");
-    return v;
-}
-DDT_DEV float ld_dsmem_f32(uint32_t caddr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
-    return v;
-}
 
 }  // namespace sm100
 }  // namespace ddt
