@@ -424,7 +424,7 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
                 o[i][1] *= f1, o[i][3] *= f1;
             }
         }
-        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        const float b0 = m0 == -INFINITY ? 0.f : m0 - kLift<F16>, b1 = m1 == -INFINITY ? 0.f : m1 - kLift<F16>;
         uint32_t pw[8];  // rounded to the cache's type and turned: keys by twos of row lane / 4
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb) {
@@ -473,7 +473,7 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
         if (!live) y = make_uint2(0, 0);
         const size_t at = (size_t)(r / a.G) * a.Hq + r % a.G;
         reinterpret_cast<uint2*>(a.out + at * D)[c] = y;
-        if (c == 0 && a.lse) a.lse[at] = live ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+        if (c == 0 && a.lse) a.lse[at] = live ? (M - kLift<F16> + __log2f(L)) * 0.6931471805599453f : -INFINITY;
     };
     if (a.nodes <= 0) {  // every row is padding: zeros, once
         for (int i = t; a.mpair == 0 && a.split == 0 && i < a.rows * (D / 4); i += 64)
@@ -1098,7 +1098,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // go to columns p_col(2c) .. +16 of S_k, whose scores are read
                 // before (the row sum takes the fp32 weights: their bf16 rounding
                 // averages out over a whole tile)
-                const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
+                const float neg = (m_use == -INFINITY) ? 0.f : kLift<F16> - m_use;
                 float2 acc = make_float2(0.f, 0.f);
                 auto qexp = [&](const uint32_t (&q)[32], int c) {
                     uint32_t pk[16];
@@ -1263,7 +1263,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         auto store_lse = [&](bool live, float M, float Ls) {
             if (p.lse)
                 p.lse[((size_t)b * R + u) * p.Hq + hh] =
-                    live ? (M + __log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+                    live ? (M - kLift<F16> + __log2f(Ls)) * 0.6931471805599453f : -INFINITY;
         };
         auto store_zero = [&]() {
             float z[32];
@@ -1539,7 +1539,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 if (split == 0 && p.lse && (!dual || k == 0))
                     p.lse[((size_t)b * R + u) * p.Hq + hh] =
-                        live ? (M + __log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+                        live ? (M - kLift<F16> + __log2f(Ls)) * 0.6931471805599453f : -INFINITY;
             }
         }
     } else if (p.merge == kMergeCluster) {

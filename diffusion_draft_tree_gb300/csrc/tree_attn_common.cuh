@@ -26,6 +26,18 @@ DDT_DEV uint32_t pack16(float lo, float hi) {
     }
 }
 
+// Softmax weights are rounded to the 16-bit type for the product with V: the tensor
+// core takes both factors in one type, and 32-bit weights as two such halves would
+// double that product.  In bf16 that is up to 2^-8 of a weight: outputs are 0.0023 of
+// their size off, where rounding the output alone makes 0.0017 (fp16 0.00022, 0.00020).
+// fp16 has no numbers below 2^-24, and a weight below that is dropped where the sum counts it; so
+// its weights are taken 2^kLift larger.  The largest is then 2^(8 + 7) -- a maximum may
+// be 2^8 behind -- and a weight keeps half a step down to 2^-21 of the row's largest
+// one and is dropped at 2^-32.  Sums and outputs carry the factor alike; only the
+// logsumexp takes it off.
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
+
 // mma.sync and its operands from shared memory, for few query rows.
 DDT_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

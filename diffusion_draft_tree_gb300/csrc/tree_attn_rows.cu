@@ -73,7 +73,7 @@ DDT_DEV void finish(const ParamsR& p, size_t row, int c, bool live, float4 v, fl
     uint2 w = make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv));
     if (!live) w = make_uint2(0, 0);
     reinterpret_cast<uint2*>(p.out + row * D)[c] = w;
-    if (c == 0 && p.lse) p.lse[row] = live ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (c == 0 && p.lse) p.lse[row] = live ? (M - kLift<F16> + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 // Row of the output that is row r of unit (b, g).
 DDT_DEV size_t out_row(const ParamsR& p, int b, int g, int r) {
@@ -433,7 +433,7 @@ tree_attn_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         o[j][2] *= f1, o[j][3] *= f1;
                     }
                 }
-                const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+                const float b0 = m0 == -INFINITY ? 0.f : m0 - kLift<F16>, b1 = m1 == -INFINITY ? 0.f : m1 - kLift<F16>;
 #pragma unroll
                 for (int nbk = 0; nbk < 2; ++nbk) {
                     x[nbk][0] = fast_exp2(x[nbk][0] - b0), x[nbk][1] = fast_exp2(x[nbk][1] - b0);
