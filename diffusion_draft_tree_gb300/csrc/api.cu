@@ -5,6 +5,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <mutex>
+#include <new>
 
 #include "common.cuh"
 #include "internal.h"
@@ -65,6 +66,17 @@ ddtree_status launched(cudaError_t e) {
 
 namespace ddt {
 int launch_status(cudaError_t e) { return (int)launched(e); }
+// For the handler around a C entry, out of which no C++ exception goes: the host's
+// memory has run out, or a lock failed.
+ddtree_status caught() {
+    try {
+        throw;
+    } catch (const std::bad_alloc&) {
+        return launched(cudaErrorMemoryAllocation);
+    } catch (...) {
+        return launched(cudaErrorUnknown);
+    }
+}
 }  // namespace ddt
 
 extern "C" {
@@ -83,7 +95,7 @@ const char* ddtree_status_str(ddtree_status s) {
 }
 
 size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, int dtype, int Hq,
-                             int Hkv, int D, int64_t cache_cap) {
+                             int Hkv, int D, int64_t cache_cap) try {
     switch (op) {
         case DDTREE_OP_TOPK:
             if (B <= 0 || V <= 0 || (dtype != DDTREE_BF16 && dtype != DDTREE_FP32)) return 0;
@@ -102,11 +114,13 @@ size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, in
             return ddt::paged_attn_workspace_bytes(B, N, Hq, Hkv, D, cache_cap);
     }
     return 0;
+} catch (...) {
+    return 0;
 }
 
 ddtree_status ddtree_topk(const void* draft_logits, int dtype, int rows, int V,
                           int64_t row_stride, int K, int32_t* topk_idx, float* topk_logp,
-                          float* lse, void* workspace, size_t ws_bytes, void* stream) {
+                          float* lse, void* workspace, size_t ws_bytes, void* stream) try {
     if (!draft_logits || !topk_idx || !topk_logp) return DDTREE_ERR_INVALID_ARG;
     if (dtype != DDTREE_BF16 && dtype != DDTREE_FP32) return DDTREE_ERR_INVALID_ARG;
     if (rows <= 0 || rows > 65535 || V <= 0 || row_stride < V || K < 1 || K > V)
@@ -120,6 +134,8 @@ ddtree_status ddtree_topk(const void* draft_logits, int dtype, int rows, int V,
     ddt::TopkArgs a{draft_logits, dtype, rows, V, row_stride, K, topk_idx, topk_logp, lse,
                     workspace, error_word()};
     return launched(ddt::launch_topk(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 namespace {
@@ -147,9 +163,11 @@ ddtree_status ddtree_build(const float* topk_logp, const int32_t* topk_idx, cons
                            const int32_t* prefix_len, int B, int L, int K, int N,
                            int32_t* parent, int32_t* depth, int32_t* rank, int32_t* token,
                            int32_t* pos_id, float* score, int32_t* child_count,
-                           uint32_t* anc_mask, int32_t* n_nodes, void* stream) {
+                           uint32_t* anc_mask, int32_t* n_nodes, void* stream) try {
     return build_common(false, topk_logp, topk_idx, bonus, prefix_len, B, L, K, N, parent, depth,
                         rank, token, pos_id, score, child_count, anc_mask, n_nodes, stream);
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_build_heap(const float* topk_logp, const int32_t* topk_idx,
@@ -157,9 +175,11 @@ ddtree_status ddtree_build_heap(const float* topk_logp, const int32_t* topk_idx,
                                 int K, int N, int32_t* parent, int32_t* depth, int32_t* rank,
                                 int32_t* token, int32_t* pos_id, float* score,
                                 int32_t* child_count, uint32_t* anc_mask, int32_t* n_nodes,
-                                void* stream) {
+                                void* stream) try {
     return build_common(true, topk_logp, topk_idx, bonus, prefix_len, B, L, K, N, parent, depth,
                         rank, token, pos_id, score, child_count, anc_mask, n_nodes, stream);
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_tree_attn(const void* q, const void* k_cache, const void* v_cache,
@@ -167,7 +187,7 @@ ddtree_status ddtree_tree_attn(const void* q, const void* k_cache, const void* v
                                const int32_t* prefix_len, const int32_t* n_nodes,
                                const uint32_t* anc_mask, int B, int N, int Hq, int Hkv, int D,
                                float scale, void* out, float* lse, void* workspace,
-                               size_t ws_bytes, void* stream) {
+                               size_t ws_bytes, void* stream) try {
     if (!q || !k_cache || !v_cache || !k_tree || !v_tree || !prefix_len || !n_nodes ||
         !anc_mask || !out)
         return DDTREE_ERR_INVALID_ARG;
@@ -185,6 +205,8 @@ ddtree_status ddtree_tree_attn(const void* q, const void* k_cache, const void* v
     ddt::AttnArgs a{q, k_cache, v_cache, cache_cap, k_tree, v_tree, prefix_len, n_nodes, anc_mask,
                     B, N, Hq, Hkv, D, scale, out, lse, workspace, error_word()};
     return launched(ddt::launch_tree_attn(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_accept(const void* target_logits, int dtype, int64_t row_stride,
@@ -192,7 +214,7 @@ ddtree_status ddtree_accept(const void* target_logits, int dtype, int64_t row_st
                             int B, int L, int N, int V, float temperature, uint64_t seed,
                             uint64_t step, int32_t* target_token, int32_t* accept_len,
                             int32_t* accepted_nodes, int32_t* out_tokens, int32_t* next_bonus,
-                            void* workspace, size_t ws_bytes, void* stream) {
+                            void* workspace, size_t ws_bytes, void* stream) try {
     if (!target_logits || !parent || !token || !n_nodes || !accept_len || !accepted_nodes ||
         !out_tokens || !next_bonus)
         return DDTREE_ERR_INVALID_ARG;
@@ -212,6 +234,8 @@ ddtree_status ddtree_accept(const void* target_logits, int dtype, int64_t row_st
                       temperature, seed, step, target_token, accept_len, accepted_nodes,
                       out_tokens, next_bonus, workspace, error_word()};
     return launched(ddt::launch_accept(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_accept_path(const void* target_logits, int dtype, int64_t row_stride,
@@ -220,7 +244,7 @@ ddtree_status ddtree_accept_path(const void* target_logits, int dtype, int64_t r
                                  float temperature, uint64_t seed, uint64_t step,
                                  int32_t* target_token, int32_t* accept_len,
                                  int32_t* accepted_nodes, int32_t* out_tokens,
-                                 int32_t* next_bonus, void* stream) {
+                                 int32_t* next_bonus, void* stream) try {
     if (!target_logits || !parent || !token || !n_nodes || !accept_len || !accepted_nodes ||
         !out_tokens || !next_bonus)
         return DDTREE_ERR_INVALID_ARG;
@@ -238,12 +262,14 @@ ddtree_status ddtree_accept_path(const void* target_logits, int dtype, int64_t r
                       temperature, seed, step, target_token, accept_len, accepted_nodes,
                       out_tokens, next_bonus, nullptr, error_word()};
     return launched(ddt::launch_accept_path(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_commit(void* k_cache, void* v_cache, int64_t cache_cap, const void* k_tree,
                             const void* v_tree, const int32_t* accept_len,
                             const int32_t* accepted_nodes, int32_t* prefix_len, int B, int L,
-                            int N, int Hkv, int D, void* stream) {
+                            int N, int Hkv, int D, void* stream) try {
     if (!k_cache || !v_cache || !k_tree || !v_tree || !accept_len || !accepted_nodes ||
         !prefix_len)
         return DDTREE_ERR_INVALID_ARG;
@@ -257,6 +283,8 @@ ddtree_status ddtree_commit(void* k_cache, void* v_cache, int64_t cache_cap, con
     ddt::CommitArgs a{k_cache, v_cache, cache_cap, k_tree, v_tree, accept_len, accepted_nodes,
                       prefix_len, B, L, N, Hkv, D, error_word()};
     return launched(ddt::launch_commit(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 // ---- the round over a paged cache ----------------------------------------------
@@ -377,7 +405,7 @@ ddtree_status ddtree_rope_turns(const double* inv_freq, int n, uint64_t* turns) 
 
 ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const ddtree_rows* k,
                           const ddtree_rows* k_out, int dtype, int T, int D, const int32_t* pos,
-                          const ddtree_rotary* rot, int inverse, void* stream) {
+                          const ddtree_rotary* rot, int inverse, void* stream) try {
     if ((dtype != DDTREE_FP32 && !dtype16(dtype)) || T < 0 || D < 1 ||
         (inverse != 0 && inverse != 1))
         return DDTREE_ERR_INVALID_ARG;
@@ -390,12 +418,14 @@ ddtree_status ddtree_rope(const ddtree_rows* q, const ddtree_rows* q_out, const 
     ddt::RopeArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(k_out), dtype, T, D, pos,
                     rot->turns, rot->rot_dim, rot->interleaved != 0, rot->scale, inverse};
     return launched(ddt::launch_rope(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, int T,
                                   const int32_t* seq, const int32_t* pos, int B,
                                   const ddtree_paged_cache* cache, const ddtree_rotary* rot,
-                                  const ddtree_rows* q, const ddtree_rows* q_out, void* stream) {
+                                  const ddtree_rows* q, const ddtree_rows* q_out, void* stream) try {
     if (ddtree_status st = cache_status(cache)) return st;
     const int dt = cache->dtype, D = cache->D;
     if (T < 0 || B <= 0) return DDTREE_ERR_INVALID_ARG;
@@ -412,6 +442,8 @@ ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, in
                       cache_arg(cache), rot ? rot->turns : nullptr, rot ? rot->rot_dim : 0,
                       rot && rot->interleaved, rot ? rot->scale : 1.f, error_word()};
     return launched(ddt::launch_append_paged(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_cache* cache,
@@ -419,7 +451,7 @@ ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_ca
                                      const int32_t* prefix_len, const int32_t* n_nodes,
                                      const uint32_t* anc_mask, int B, int N, float scale,
                                      void* out, float* lse, void* workspace, size_t ws_bytes,
-                                     void* stream) {
+                                     void* stream) try {
     if (ddtree_status st = cache_status(cache)) return st;
     const int dt = cache->dtype, D = cache->D, Hkv = cache->Hkv, ps = cache->page_size;
     if (!prefix_len || !n_nodes || !anc_mask || !out || B <= 0 || N < 0 || !(scale > 0.f) ||
@@ -443,12 +475,14 @@ ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_ca
                          prefix_len, n_nodes, anc_mask, B, N, scale, out, lse, workspace,
                          error_word()};
     return launched(ddt::launch_tree_attn_paged(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_rows* k_tree,
                                   const ddtree_rows* v_tree, const int32_t* accept_len,
                                   const int32_t* accepted_nodes, const int32_t* prefix_len,
-                                  int32_t* new_len, int B, int L, int N, void* stream) {
+                                  int32_t* new_len, int B, int L, int N, void* stream) try {
     if (ddtree_status st = cache_status(cache)) return st;
     const int dt = cache->dtype, D = cache->D;
     if (!accept_len || !accepted_nodes || !prefix_len || B <= 0 || B > 65535 || L <= 0 || N < 0)
@@ -463,6 +497,8 @@ ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_
     ddt::CommitPagedArgs a{cache_arg(cache), rows_arg(k_tree), rows_arg(v_tree), accept_len,
                            accepted_nodes, prefix_len, new_len, B, L, N, error_word()};
     return launched(ddt::launch_commit_paged(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
 
 namespace {
@@ -492,15 +528,17 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns, uint32_t* err) {
 
 }  // namespace
 
-ddtree_status ddtree_selftest_wait(uint32_t limit_us, void* stream) {
+ddtree_status ddtree_selftest_wait(uint32_t limit_us, void* stream) try {
     if (limit_us < 1 || limit_us > 1000000) return DDTREE_ERR_INVALID_ARG;
     uint32_t* err = error_word();
     if (!err) return DDTREE_ERR_CUDA;
     selftest_wait_kernel<<<1, 64, 0, (cudaStream_t)stream>>>((uint64_t)limit_us * 1000ull, err);
     return launched(cudaGetLastError());
+} catch (...) {
+    return ddt::caught();
 }
 
-ddtree_status ddtree_device_check(void* stream, uint32_t* detail) {
+ddtree_status ddtree_device_check(void* stream, uint32_t* detail) try {
     uint32_t* p = error_word();
     if (!p) return DDTREE_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
@@ -512,6 +550,8 @@ ddtree_status ddtree_device_check(void* stream, uint32_t* detail) {
     if (cudaStreamSynchronize(s) != cudaSuccess) return DDTREE_ERR_CUDA;
     if (detail) *detail = v;
     return v ? DDTREE_ERR_DEVICE : DDTREE_OK;
+} catch (...) {
+    return ddt::caught();
 }
 
 }  // extern "C"

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/ddtree.h"
+
 namespace ddt {
 
 // ---- step 1: log-softmax + top-K ------------------------------------------
@@ -172,5 +174,7 @@ uint32_t* error_word();
 // The ddtree_status for a CUDA result; a failure is remembered for
 // ddtree_last_cuda_error().
 int launch_status(cudaError_t e);
+// ... and for the exception being handled (call it in a catch block).
+ddtree_status caught();
 
 }  // namespace ddt

@@ -570,7 +570,7 @@ cudaError_t noalloc_scratch(void** out) {
 
 extern "C" ddtree_status ddtree_topk_noalloc(const void* draft_logits, int dtype, int rows, int V,
                                              int64_t row_stride, int K, int32_t* topk_idx,
-                                             float* topk_logp, float* lse, void* stream) {
+                                             float* topk_logp, float* lse, void* stream) try {
     if (!draft_logits || !topk_idx || !topk_logp) return DDTREE_ERR_INVALID_ARG;
     if (dtype != DDTREE_BF16 && dtype != DDTREE_FP32) return DDTREE_ERR_INVALID_ARG;
     if (rows <= 0 || rows > 65535 || V <= 0 || row_stride < V || K < 1 || K > V)
@@ -590,4 +590,6 @@ extern "C" ddtree_status ddtree_topk_noalloc(const void* draft_logits, int dtype
     ddt::TopkArgs a{draft_logits, dtype, rows, V, row_stride, K, topk_idx, topk_logp, lse,
                     scratch, ddt::error_word()};
     return (ddtree_status)ddt::launch_status(ddt::launch_topk(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
 }
