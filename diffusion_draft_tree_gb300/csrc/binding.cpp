@@ -86,7 +86,7 @@ Rows rows(const Tensor& t, const char* name, const Common& c) {
     if (tokens > INT32_MAX || n[h] > INT32_MAX) bad(std::string(name) + " is too large");
     // (the stride of a dimension of one entry says nothing)
     const int64_t hs = n[h] == 1 ? c.D : st[h];
-    if (tokens == 1) ts = std::max({ts, n[h] * hs, c.D});
+    if (tokens == 1) ts = std::max(n[h] * hs, c.D);
     return {{t.data_ptr(), (int32_t)n[h], ts, hs}, tokens};
 }
 Rows rows(PyObject* o, const char* name, const Common& c) { return rows(tensor(o, name), name, c); }
