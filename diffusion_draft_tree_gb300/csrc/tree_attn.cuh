@@ -1805,7 +1805,15 @@ PagedPlan plan_paged_few(int B, int N, int G, int Hkv, Tiles t, int sms, Active 
 }
 
 // The plan of a paged batch's many units, with the rows that the query tiles leave over
-// taken along by the pairs (`left` of them) where that is one operand's worth.
+// taken along by the pairs (`left` of them) where that is one operand's worth -- unless
+// a unit has one pair, which then takes all of them along, and these units leave a
+// good part of the SMs idle while their lists are too short to be cut for them: the
+// lone tiles then run on those SMs.  Lone tiles against rows taken along, us (8 KV
+// heads, G = 4, N = 64, D = 128, bf16), of lists of 9, 33, 65, 95 and 126 tiles: 10
+// sequences (80 units taken along, of 152 SMs) 26 / 35, 59 / 88, 120 / 149, 173 / 176, 220 / 214;
+// 12 (96 units) at 65, 95 and 126 tiles 157 / 171, 212 / 179, 266 / 251; 14 (112 units) at 33 and
+// 65 tiles 105 / 90, 180 / 175.
+constexpr int kLoneTiles = 80;
 struct ManyPlan : Plan {
     int left;
 };
@@ -1814,7 +1822,9 @@ ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms) {
     (Plan&)pl = plan_base(N, Hq, Hkv);
     const int G = Hq / Hkv, left = (N + 1 - (pl.mtiles - 1) * (BM / G)) * G;
     if (plan_units(pl, B, Hkv) < sms) return pl;  // few units (smax = 0)
-    if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows) {
+    const long along = (long)B * Hkv * (pl.mpairs - 1);  // units if the pairs take them
+    const bool short_wave = pl.mpairs == 2 && along * 10 < sms * 7L && t.prefix + t.tree <= kLoneTiles;
+    if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
         --pl.mtiles;
         --pl.mpairs;
         pl.left = left;
