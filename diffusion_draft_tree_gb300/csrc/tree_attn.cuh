@@ -286,8 +286,9 @@ __device__ __noinline__ int3 ranked_item(const int32_t* prefix_len, const int32_
 // and scheduler, so that a tile takes these warps 3.6 thousand cycles where the pair
 // needs 2.8 (left out, the products gave 434 us instead of 497 at one pair a unit, the
 // shared-memory reads nothing).  Rows are the products' narrow side, S^T = K Q^T and
-// O^T += V^T P^T, 8 rows wide instead of 16; 4 warps would leave 128 registers a
-// thread.  Warp w takes keys [64 w, 64 w + 64) of a tile, its scores, weights,
+// O^T += V^T P^T, 8 rows wide instead of 16; 4 warps at an equal share of the
+// registers, 128 a thread, spilled (shares moved between warpgroups are untried).
+// Warp w takes keys [64 w, 64 w + 64) of a tile, its scores, weights,
 // statistics and outputs in registers; K is let go after the scores, V after the
 // products, and the copies wait for these warps as for the tensor core.  The two
 // meet in shared memory, and the pairs and splits in the workspace: the last of
@@ -1707,6 +1708,12 @@ long lpt_span(long units, int T, int tps, int sms) {
 // up to just under a third is scored by lpt_span, and the best is taken when
 // it beats the quarter by at least 2 %.  The choice assumes every unit as long
 // as the longest; it is cached per shape.
+// Lists of 64 tiles and fewer stay whole and no piece is shorter than 32: against a
+// rule of twice that reach (33 tiles, pieces of 16), us over pages (8 KV heads, G = 4,
+// D = 128, bf16): 20 sequences of 8100, N = 63 179 / 186; 24 of 4000, N = 31 and 16 of
+// 4000, N = 64 94 / 94 and 92 / 92; 40 of 4000, N = 64 231 / 232; 20 of 100 to 8100,
+// N = 63 86 / 95; 40 of 100 to 4000, N = 127 144 / 163.  (A piece's merge costs more
+// than the cost model's 8 tiles where pieces are short.)
 Plan plan_many(const Plan& base, Tiles t, long units, int sms) {
     Plan pl = base;
     const int T = t.prefix + t.tree;
@@ -1767,12 +1774,13 @@ Plan plan_few(const Plan& base, Tiles t, long units, int sms, Active active) {
 }
 
 // Few units, paged: what a CTA's exchange with its cluster costs grows with its
-// rows (32-bit partials through distributed shared memory, which passes about 25
-// GB/s a CTA), so rows are spread over idle SMs too: a unit may be a single query
+// rows (32-bit partials through distributed shared memory, which passes about 15
+// GB/s a CTA: 512 bytes a row of D = 128), so rows are spread over idle SMs too: a unit may be a single query
 // tile, and tiles may hold fewer nodes than fit.  Every number of tiles up to
 // four times the least and every cluster size that is resident at once is
 // scored, in microseconds measured on GB300 (D = 128): a key tile takes a pair
-// of query tiles 1.5, a single one 1.2; an exchange 1 and 0.035 a row.
+// of query tiles 1.5, a single one 1.2; an exchange 1 and 0.035 a row.  (D = 64, whose
+// rows are half as long, goes by the same figures.)
 struct PagedPlan : Plan {
     int npt, single;
 };

@@ -56,7 +56,7 @@ typedef enum {
     DDTREE_OK = 0,
     DDTREE_ERR_INVALID_ARG = 1, /* null pointer, out-of-range size, misalignment */
     DDTREE_ERR_UNSUPPORTED = 2, /* legal but not implemented (e.g. D not 64/128) */
-    DDTREE_ERR_CUDA = 3,        /* a CUDA runtime call or a launch failed */
+    DDTREE_ERR_CUDA = 3,        /* a CUDA runtime call or a launch failed, or host memory ran out */
     DDTREE_ERR_DEVICE = 4       /* a kernel recorded bad device-side data or a timeout */
 } ddtree_status;
 
@@ -408,7 +408,8 @@ ddtree_status ddtree_append_paged(const ddtree_rows* k, const ddtree_rows* v, in
  * zero and is recorded; a prefix_len or n_nodes out of range leaves the
  * sequence's outputs unwritten and is recorded.
  * Softmax statistics, partial outputs and their merge are held in 32 bits; the
- * softmax weights are rounded to the cache's dtype for the product with v.
+ * softmax weights are rounded to the cache's dtype for the product with v (in
+ * fp16 to multiples of 2^-31 of the row's largest one, or finer).
  * Workspace: ddtree_workspace_size(DDTREE_OP_TREE_ATTN_PAGED, ...). */
 ddtree_status ddtree_tree_attn_paged(const ddtree_rows* q, const ddtree_paged_cache* cache,
                                      const ddtree_rows* k_tree, const ddtree_rows* v_tree,
