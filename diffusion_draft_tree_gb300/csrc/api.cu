@@ -112,6 +112,11 @@ size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, in
                 cache_cap < 0 || cache_cap > (1 << 30))
                 return 0;
             return ddt::paged_attn_workspace_bytes(B, N, Hq, Hkv, D, cache_cap);
+        case DDTREE_OP_TREE_ATTN_Q8:
+            if (B <= 0 || N < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128 || D <= 0 ||
+                cache_cap < 0 || cache_cap > (1 << 30))
+                return 0;
+            return ddt::q8_attn_workspace_bytes(B, N, Hq, Hkv, D, cache_cap);
     }
     return 0;
 } catch (...) {
@@ -497,6 +502,161 @@ ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_
     ddt::CommitPagedArgs a{cache_arg(cache), rows_arg(k_tree), rows_arg(v_tree), accept_len,
                            accepted_nodes, prefix_len, new_len, B, L, N, error_word()};
     return launched(ddt::launch_commit_paged(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
+}
+
+// ---- the round over an 8-bit paged cache ----------------------------------------
+
+namespace {
+
+// Whether a norm can be used; NULL is none.
+bool norm_ok(const ddtree_head_norm* n) {
+    return !n || (n->eps > 0.f && std::isfinite(n->eps) && aligned4({n->q_weight, n->k_weight}));
+}
+ddt::NormArgs norm_arg(const ddtree_head_norm* n) {
+    return n ? ddt::NormArgs{n->q_weight, n->k_weight, n->eps, true} : ddt::NormArgs{};
+}
+
+ddtree_status q8_status(const ddtree_q8_cache* c) {
+    if (!c || !c->k_pages || !c->v_pages || !c->k_scales || !c->v_scales || !c->page_table ||
+        c->k_pages == c->v_pages || c->k_scales == c->v_scales)
+        return DDTREE_ERR_INVALID_ARG;
+    if (!dtype16(c->dtype) || c->num_pages <= 0 || c->page_size <= 0 || c->block <= 0 || c->Hkv <= 0 ||
+        c->D <= 0 || c->max_pages <= 0 || c->table_stride < c->max_pages ||
+        (int64_t)c->max_pages * c->page_size > (1 << 30))
+        return DDTREE_ERR_INVALID_ARG;
+    for (const int64_t st : {c->page_stride, c->head_stride, c->slot_stride})
+        if (st < 0 || st % 16) return DDTREE_ERR_INVALID_ARG;
+    if ((c->num_pages > 1 && c->page_stride < c->D) || (c->Hkv > 1 && c->head_stride < c->D) ||
+        (c->page_size > 1 && c->slot_stride < c->D))
+        return DDTREE_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)c->k_pages, (const void*)c->v_pages, (const void*)c->k_scales,
+                          (const void*)c->v_scales})
+        if (!aligned(p, 16)) return DDTREE_ERR_INVALID_ARG;
+    if (!aligned(c->page_table, 4)) return DDTREE_ERR_INVALID_ARG;
+    if ((c->D != 64 && c->D != 128) || c->page_size < 8 || (c->page_size & (c->page_size - 1)) ||
+        c->block < 8 || (c->block & (c->block - 1)) || c->block > c->page_size ||
+        c->block > DDTREE_MAX_Q8_BLOCK)
+        return DDTREE_ERR_UNSUPPORTED;
+    return DDTREE_OK;
+}
+ddt::Q8Args q8_arg(const ddtree_q8_cache* c) {
+    return {(uint8_t*)c->k_pages, (uint8_t*)c->v_pages, c->k_scales, c->v_scales, c->dtype,
+            c->num_pages, c->page_size, c->block, c->Hkv, c->D, c->page_stride, c->head_stride,
+            c->slot_stride, c->page_table, c->max_pages, c->table_stride};
+}
+// Rows of a call over an 8-bit cache: 16-byte accesses, one row a KV head.
+bool q8_rows_ok(const ddtree_rows* r, const ddtree_q8_cache* c, bool out) {
+    return rows_ok(r, c->dtype, c->D, out) && rows16(r) && r->heads == c->Hkv;
+}
+
+}  // namespace
+
+ddtree_status ddtree_norm_rope(const ddtree_rows* q, const ddtree_rows* q_out,
+                               const ddtree_rows* k, const ddtree_rows* k_out, int dtype, int T,
+                               int D, const int32_t* pos, const ddtree_head_norm* norm,
+                               const ddtree_rotary* rot, void* stream) try {
+    if ((dtype != DDTREE_FP32 && !dtype16(dtype)) || T < 0 || D < 1) return DDTREE_ERR_INVALID_ARG;
+    if (D > DDTREE_MAX_ROPE_D) return DDTREE_ERR_UNSUPPORTED;
+    if (T == 0) return DDTREE_OK;
+    if (!pos || !aligned(pos, 4) || !norm || !norm_ok(norm) || !pair_ok(q, q_out, dtype, D) ||
+        (k || k_out ? !pair_ok(k, k_out, dtype, D) : false) || (rot && !rotary_ok(rot, D)) ||
+        (k && !apart(q, q_out, k, k_out)))
+        return DDTREE_ERR_INVALID_ARG;
+    if ((int64_t)q->heads + (k ? k->heads : 0) > 65535) return DDTREE_ERR_UNSUPPORTED;
+    ddt::NormRopeArgs a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(k_out), dtype, T, D, pos,
+                        rot ? rot->turns : nullptr, rot ? rot->rot_dim : 0, rot && rot->interleaved,
+                        rot ? rot->scale : 1.f, norm_arg(norm)};
+    return launched(ddt::launch_norm_rope(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
+}
+
+ddtree_status ddtree_append_q8(const ddtree_rows* k, const ddtree_rows* v, int T,
+                               const int32_t* first, const int32_t* at, int B,
+                               const ddtree_q8_cache* cache, const ddtree_rotary* rot,
+                               const ddtree_head_norm* norm, const ddtree_rows* q,
+                               const ddtree_rows* q_out, void* stream) try {
+    if (ddtree_status st = q8_status(cache)) return st;
+    const int dt = cache->dtype, D = cache->D;
+    if (T < 0 || B <= 0) return DDTREE_ERR_INVALID_ARG;
+    if (T == 0) return DDTREE_OK;
+    if (!first || !at || !aligned4({first, at}) || !q8_rows_ok(k, cache, false) ||
+        !q8_rows_ok(v, cache, false) || !norm_ok(norm) || (rot && !rotary_ok(rot, D)) ||
+        (q || q_out ? !(pair_ok(q, q_out, dt, D) && rows16(q) && rows16(q_out)) : false) ||
+        (q && !(apart(q, q_out, k, nullptr) && apart(q, q_out, v, nullptr))))
+        return DDTREE_ERR_INVALID_ARG;
+    if ((rot && rot->rot_dim % 16) || 2 * (int64_t)cache->Hkv + (q ? q->heads : 0) > 65535)
+        return DDTREE_ERR_UNSUPPORTED;
+    ddt::AppendQ8Args a{rows_arg(q), rows_arg(q_out), rows_arg(k), rows_arg(v), T, B, first, at,
+                        q8_arg(cache), rot ? rot->turns : nullptr, rot ? rot->rot_dim : 0,
+                        rot && rot->interleaved, rot ? rot->scale : 1.f, norm_arg(norm), error_word()};
+    return launched(ddt::launch_append_q8(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
+}
+
+ddtree_status ddtree_commit_q8(const ddtree_q8_cache* cache, const ddtree_rows* k_tree,
+                               const ddtree_rows* v_tree, const int32_t* accept_len,
+                               const int32_t* accepted_nodes, const int32_t* prefix_len,
+                               int32_t* new_len, int B, int L, int N, void* stream) try {
+    if (ddtree_status st = q8_status(cache)) return st;
+    if (!accept_len || !accepted_nodes || !prefix_len || B <= 0 || B > 65535 || L <= 0 || N < 0)
+        return DDTREE_ERR_INVALID_ARG;
+    if (!q8_rows_ok(k_tree, cache, false) || !q8_rows_ok(v_tree, cache, false) ||
+        !aligned4({accept_len, accepted_nodes, prefix_len, new_len}) ||
+        (new_len && (new_len == prefix_len || new_len == accept_len || new_len == accepted_nodes)))
+        return DDTREE_ERR_INVALID_ARG;
+    if (L > DDTREE_MAX_L || N > DDTREE_MAX_N || cache->Hkv > 65535) return DDTREE_ERR_UNSUPPORTED;
+    ddt::CommitQ8Args a{q8_arg(cache), rows_arg(k_tree), rows_arg(v_tree), accept_len,
+                        accepted_nodes, prefix_len, new_len, B, L, N, error_word()};
+    return launched(ddt::launch_commit_q8(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
+}
+
+ddtree_status ddtree_read_q8(const ddtree_q8_cache* cache, const int32_t* first,
+                             const int32_t* at, int B, const ddtree_rows* k_out,
+                             const ddtree_rows* v_out, int T, void* stream) try {
+    if (ddtree_status st = q8_status(cache)) return st;
+    if (T < 0 || B <= 0) return DDTREE_ERR_INVALID_ARG;
+    if (T == 0) return DDTREE_OK;
+    if (!first || !at || !aligned4({first, at}) || !q8_rows_ok(k_out, cache, true) ||
+        !q8_rows_ok(v_out, cache, true) || k_out->data == v_out->data)
+        return DDTREE_ERR_INVALID_ARG;
+    if (cache->Hkv > 65535) return DDTREE_ERR_UNSUPPORTED;
+    ddt::ReadQ8Args a{q8_arg(cache), first, at, rows_arg(k_out), rows_arg(v_out), B, T, error_word()};
+    return launched(ddt::launch_read_q8(a, (cudaStream_t)stream));
+} catch (...) {
+    return ddt::caught();
+}
+
+ddtree_status ddtree_tree_attn_q8(const ddtree_rows* q, const ddtree_q8_cache* cache,
+                                  const ddtree_rows* k_tree, const ddtree_rows* v_tree,
+                                  const int32_t* prefix_len, const int32_t* n_nodes,
+                                  const uint32_t* anc_mask, int B, int N, float scale, void* out,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream) try {
+    if (ddtree_status st = q8_status(cache)) return st;
+    const int dt = cache->dtype, D = cache->D, Hkv = cache->Hkv;
+    if (!prefix_len || !n_nodes || !anc_mask || !out || B <= 0 || N < 0 || !(scale > 0.f) ||
+        !std::isfinite(scale))
+        return DDTREE_ERR_INVALID_ARG;
+    if (!rows_ok(q, dt, D, true) || !rows16(q) || !q8_rows_ok(k_tree, cache, true) ||
+        !q8_rows_ok(v_tree, cache, true) || q->heads % Hkv || out == q->data ||
+        out == k_tree->data || out == v_tree->data || !aligned(out, 16) ||
+        !aligned4({prefix_len, n_nodes, anc_mask, lse}))
+        return DDTREE_ERR_INVALID_ARG;
+    if (N > DDTREE_MAX_N || q->heads / Hkv > 128 || (int64_t)B * (N + 1) > INT32_MAX)
+        return DDTREE_ERR_UNSUPPORTED;
+    const size_t need = ddt::q8_attn_workspace_bytes(B, N, q->heads, Hkv, D,
+                                                     (int64_t)cache->max_pages * cache->page_size);
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+        return DDTREE_ERR_INVALID_ARG;
+    ddt::Q8AttnArgs a{rows_arg(q), rows_arg(k_tree), rows_arg(v_tree), q8_arg(cache),
+                      prefix_len, n_nodes, anc_mask, B, N, scale, out, lse, workspace,
+                      error_word()};
+    return launched(ddt::launch_tree_attn_q8(a, (cudaStream_t)stream));
 } catch (...) {
     return ddt::caught();
 }

@@ -165,6 +165,86 @@ struct PagedAttnArgs {
 size_t paged_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t cache_cap);
 cudaError_t launch_tree_attn_paged(const PagedAttnArgs& a, cudaStream_t s);
 
+// ---- 8-bit paged cache ---------------------------------------------------------
+// Codes placed as in PagedArgs (strides in bytes), a scale byte for each block of
+// positions of a page and head.
+struct Q8Args {
+    uint8_t *k, *v, *k_scales, *v_scales;
+    int dtype;  // of the tokens
+    int num_pages, page_size, block, Hkv, D;
+    int64_t page_stride, head_stride, slot_stride;
+    const int32_t* table;
+    int max_pages;
+    int64_t table_stride;
+};
+// Norm of a head; null weights count as ones.  on: whether there is one.
+struct NormArgs {
+    const float *q_weight, *k_weight;
+    float eps;
+    bool on;
+};
+
+struct NormRopeArgs {
+    RowsArg q, q_out, k, k_out;
+    int dtype, T, D;
+    const int32_t* pos;
+    const uint64_t* turns;
+    int rot;  // 0: no rotation
+    bool interleaved;
+    float scale;
+    NormArgs norm;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
+
+struct AppendQ8Args {
+    RowsArg q, q_out, k, v;
+    int T, B;
+    const int32_t *first, *at;
+    Q8Args cache;
+    const uint64_t* turns;
+    int rot;  // 0: no rotation
+    bool interleaved;
+    float scale;
+    NormArgs norm;
+    uint32_t* err;
+};
+cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t s);
+
+struct CommitQ8Args {
+    Q8Args cache;
+    RowsArg k_tree, v_tree;
+    const int32_t *accept_len, *accepted_nodes, *prefix_len;
+    int32_t* new_len;
+    int B, L, N;
+    uint32_t* err;
+};
+cudaError_t launch_commit_q8(const CommitQ8Args& a, cudaStream_t s);
+
+struct ReadQ8Args {
+    Q8Args cache;
+    const int32_t *first, *at;
+    RowsArg k_out, v_out;
+    int B, T;
+    uint32_t* err;
+};
+cudaError_t launch_read_q8(const ReadQ8Args& a, cudaStream_t s);
+
+struct Q8AttnArgs {
+    RowsArg q, k_tree, v_tree;
+    Q8Args cache;
+    const int32_t* prefix_len;
+    const int32_t* n_nodes;
+    const uint32_t* anc_mask;
+    int B, N;
+    float scale;
+    void* out;
+    float* lse;
+    void* ws;
+    uint32_t* err;
+};
+size_t q8_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int64_t cache_cap);
+cudaError_t launch_tree_attn_q8(const Q8AttnArgs& a, cudaStream_t s);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ---- shared by the entry points (api.cu) --------------------------------------

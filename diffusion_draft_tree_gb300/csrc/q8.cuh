@@ -1,0 +1,89 @@
+// q8.cuh -- the 8-bit cache's format: e4m3 codes under a power of two for each block of
+// positions of a page and head, and where a run's blocks lie.
+//
+// A code c stands for c * 2^e.  The exponent of a block is the least e at which its
+// largest element is at most 448 * 2^e (448 = 1.75 * 2^8 is the largest code), so that its
+// significand is found by a power of two alone: x * 2^-e is exact, the one rounding is to
+// the code, and c * 2^e is exact in bf16 always and in fp16 from e = -15 (the smallest
+// code's step is then fp16's own, 2^-24) to 7 (448 * 2^7 = 57344).  bf16 stops at 7 too:
+// its codes are widened by a product with 2^(120 + e), which has to be a bf16 number.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace ddt {
+
+namespace {
+
+constexpr int kQ8Most = 7;
+__host__ __device__ constexpr int q8_least(bool f16) { return f16 ? -15 : -96; }
+
+DDT_DEV float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+// The exponent of a block whose largest element is amax >= 0.
+DDT_DEV int q8_exponent(float amax, int least) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, least), kQ8Most);
+}
+DDT_DEV int q8_from_byte(uint32_t x, int least) { return min(max((int)x - 127, least), kQ8Most); }
+
+// Two elements as codes, lo in the low byte: to the nearest, ties to even, at most 448.
+DDT_DEV uint32_t q8_pack2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+DDT_DEV uint32_t q8_pack4(float a, float b, float c, float d) {
+    return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
+}
+// The value of one code (0x7F as 480).
+DDT_DEV float q8_value(uint32_t c) {
+    const uint32_t sign = (c & 0x80u) << 24, rest = (c & 0x7fu) << 20;
+    return __uint_as_float(sign | rest) * 0x1p120f;  // (exponent bias 127 - 7)
+}
+
+// A run's tokens first[b] .. first[b + 1] - 1 become positions at[b] .. of sequence b.  Whether
+// it is one that no call may carry out: outside the T tokens or the table's positions.
+DDT_DEV bool run_bad(int f, int n, int p, int T, int64_t cap) {
+    return n != 0 && (f < 0 || n < 0 || (int64_t)f + n > T || p < 0 || (int64_t)p + n > cap);
+}
+// One block of a run: positions [p0, p0 + S) of the sequence, of which [lo, hi) are the run's.
+struct RunBlock {
+    int b, lo, hi, p0;
+    int token;  // of position lo
+    bool ok;    // there is such a block, and its run is not a bad one
+};
+// Runs cover their blocks by slots: sequence b has slots first[b] / S + 2 b and up, two more
+// than its tokens fill, as n tokens touch at most (n - 2) / S + 2 blocks.  The slots'
+// starts are known without adding up the runs before, so a CTA finds its own by halving.
+DDT_DEV RunBlock run_block(const int32_t* first, const int32_t* at, int B, int T, int S, int64_t cap,
+                           int64_t slot) {
+    int lo = 0, hi = B - 1;  // the last sequence whose slots start at or before this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)(first[mid] / S) + 2 * (int64_t)mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    RunBlock x{};
+    x.b = lo;
+    const int f = first[lo], n = first[lo + 1] - f, p = at[lo];
+    const int64_t j = slot - ((int64_t)(f / S) + 2 * (int64_t)lo);
+    if (j < 0 || n == 0 || run_bad(f, n, p, T, cap)) return x;
+    x.p0 = (int)min((int64_t)(p / S * S) + j * S, (int64_t)INT32_MAX - S);
+    x.lo = max(x.p0, p);
+    x.hi = min(x.p0 + S, p + n);
+    x.ok = x.lo < x.hi;
+    x.token = f + (x.lo - p);
+    return x;
+}
+// Records a bad run; every run has a slot of its own number.
+DDT_DEV void check_run(const int32_t* first, const int32_t* at, int B, int T, int64_t cap, int64_t slot,
+                       uint32_t* err, uint32_t code) {
+    if (slot < B && run_bad(first[slot], first[slot + 1] - first[slot], at[slot], T, cap)) record_error(err, code);
+}
+inline int64_t run_slots(int B, int T, int S) { return (int64_t)T / S + 2 * (int64_t)B; }
+
+}  // namespace
+
+}  // namespace ddt

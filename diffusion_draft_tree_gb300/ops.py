@@ -25,7 +25,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libddtree.so")
 
 BF16, FP32, FP16 = 0, 1, 2
-OP_TOPK, OP_TREE_ATTN, OP_ACCEPT, OP_TREE_ATTN_PAGED = 0, 2, 3, 4
+OP_TOPK, OP_TREE_ATTN, OP_ACCEPT, OP_TREE_ATTN_PAGED, OP_TREE_ATTN_Q8 = 0, 2, 3, 4, 5
 MAX_K, MAX_L, MAX_N = 32, 16, 1024
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error",
@@ -35,6 +35,8 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error
 # Structs of include/ddtree.h, packed with the platform's own alignment.
 _pack_cache = struct.Struct("@PPiiiiiqqqPiq").pack    # ddtree_paged_cache
 _pack_rotary = struct.Struct("@Piif4x").pack          # ddtree_rotary
+_pack_norm = struct.Struct("@PPf4x").pack             # ddtree_head_norm
+_pack_q8 = struct.Struct("@PPPPiiiiiiqqqPi4xq").pack  # ddtree_q8_cache
 
 
 class DDTreeError(RuntimeError):
@@ -79,6 +81,12 @@ def _load() -> ctypes.CDLL:
     lib.ddtree_tree_attn_paged.argtypes = [rows, cache, rows, rows, P, P, P, i32, i32, f32, P, P,
                                            P, sz, P]
     lib.ddtree_commit_paged.argtypes = [cache, rows, rows, P, P, P, P, i32, i32, i32, P]
+    q8 = norm = P
+    lib.ddtree_norm_rope.argtypes = [rows, rows, rows, rows, i32, i32, i32, P, norm, rotary, P]
+    lib.ddtree_append_q8.argtypes = [rows, rows, i32, P, P, i32, q8, rotary, norm, rows, rows, P]
+    lib.ddtree_commit_q8.argtypes = [q8, rows, rows, P, P, P, P, i32, i32, i32, P]
+    lib.ddtree_read_q8.argtypes = [q8, P, P, i32, rows, rows, i32, P]
+    lib.ddtree_tree_attn_q8.argtypes = lib.ddtree_tree_attn_paged.argtypes
     lib.ddtree_device_check.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.ddtree_selftest_wait.argtypes = [ctypes.c_uint32, P]
     lib.ddtree_last_cuda_error.argtypes = []
@@ -89,7 +97,8 @@ def _load() -> ctypes.CDLL:
               "ddtree_accept", "ddtree_accept_path", "ddtree_commit", "ddtree_topk_noalloc",
               "ddtree_device_check", "ddtree_selftest_wait", "ddtree_rope_frequencies",
               "ddtree_rope_turns", "ddtree_rope", "ddtree_append_paged",
-              "ddtree_tree_attn_paged", "ddtree_commit_paged"):
+              "ddtree_tree_attn_paged", "ddtree_commit_paged", "ddtree_norm_rope",
+              "ddtree_append_q8", "ddtree_commit_q8", "ddtree_read_q8", "ddtree_tree_attn_q8"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -107,7 +116,8 @@ if getattr(_ddtree, "built_for", None) != _build.abi_key():
 EXPORTED = ("ddtree_workspace_size", "ddtree_topk", "ddtree_build", "ddtree_build_heap",
             "ddtree_tree_attn", "ddtree_accept", "ddtree_device_check", "ddtree_last_cuda_error",
             "ddtree_status_str", "ddtree_rope", "ddtree_append_paged", "ddtree_tree_attn_paged",
-            "ddtree_commit_paged")
+            "ddtree_commit_paged", "ddtree_norm_rope", "ddtree_append_q8", "ddtree_commit_q8",
+            "ddtree_read_q8", "ddtree_tree_attn_q8")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -512,3 +522,185 @@ def ddtree_commit_paged(cache: PagedCache, k_tree, v_tree, accept_len, accepted_
                               cache.v_pages)
     if st:
         raise DDTreeError("ddtree_commit_paged", st)
+
+
+# --------------------------------------------------------------------------
+# the round over an 8-bit paged cache, and the norm of queries and keys
+# --------------------------------------------------------------------------
+
+class HeadNorm:
+    """The norm of every head before its rotation, x / sqrt(mean x^2 + eps) * weight:
+    the weights of queries and keys, [D] of any floating type (None: ones), taken
+    once, in 32 bits.  `offset` is added to them (models that keep weight - 1)."""
+
+    def __init__(self, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, offset: float = 0.0):
+        if not eps > 0:
+            raise ValueError(f"eps must be positive, got {eps}")
+        self.eps, self._index, self.D = float(eps), -1, -1
+        held = []
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                held.append(None)
+                continue
+            if w.dim() != 1 or not w.is_floating_point():
+                raise ValueError(f"{name} must be a floating [D] tensor")
+            at = _index(w)
+            if self._index not in (-1, at) or self.D not in (-1, w.shape[0]):
+                raise ValueError("q_weight and k_weight must agree in size and device")
+            self._index, self.D = at, w.shape[0]
+            held.append((w.detach().float() + offset).contiguous())
+        self.q_weight, self.k_weight = held
+        self._c = (_pack_norm(*(0 if w is None else w.data_ptr() for w in held), self.eps),
+                   self._index, self.D)
+
+
+class QuantCache:
+    """A paged KV cache in 8 bits: k_pages and v_pages float8_e4m3fn codes
+    [num_pages][Hkv][page_size][D] (views with equal strides), k_scales and v_scales
+    uint8 [num_pages][Hkv][page_size // block], a byte x for each block of positions:
+    a code c stands for c * 2^(x - 127) (include/ddtree.h, ddtree_q8_cache), and
+    page_table int32 [B][max_pages].  dtype (bfloat16 or float16) is that of the tokens.
+    Holds the tensors, copies nothing."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                 v_scales: torch.Tensor, page_table: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
+        index = _index(k_pages)
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        if k_pages.dim() != 4 or k_pages.dtype != torch.float8_e4m3fn:
+            raise ValueError("k_pages must be a float8_e4m3fn [num_pages][Hkv][page_size][D] tensor")
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or \
+                v_pages.stride() != k_pages.stride() or v_pages.get_device() != index:
+            raise ValueError("v_pages must match k_pages in shape, type, strides and device")
+        if k_pages.stride(3) != 1 and k_pages.shape[3] > 1:
+            raise ValueError("a page's rows must be contiguous")
+        if 0 in k_pages.shape or 0 in page_table.shape:
+            raise ValueError("a paged cache needs at least one page, head, slot and table entry")
+        self.num_pages, self.Hkv, self.page_size, self.D = k_pages.shape
+        blocks = k_scales.shape[-1] if k_scales.dim() == 3 else 0
+        if blocks == 0 or self.page_size % blocks:
+            raise ValueError("k_scales must be [num_pages][Hkv][page_size // block]")
+        for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if s.dtype != torch.uint8 or s.shape != (self.num_pages, self.Hkv, blocks) or \
+                    not s.is_contiguous() or s.get_device() != index:
+                raise ValueError(f"{name} must be a contiguous uint8 tensor "
+                                 f"{[self.num_pages, self.Hkv, blocks]} on the pages' device")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                page_table.get_device() != index or \
+                (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+            raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows, on the "
+                             "pages' device")
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.k_scales, self.v_scales, self.block = k_scales, v_scales, self.page_size // blocks
+        self.B, self.max_pages = page_table.shape
+        self.dtype, self.device, self._index = dtype, k_pages.device, index
+        st = [s if n > 1 else self.D for n, s in zip(k_pages.shape, k_pages.stride())]
+        self._c = _pack_q8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                           v_scales.data_ptr(), _CODES[dtype], self.num_pages, self.page_size,
+                           self.block, self.Hkv, self.D, *st[:3], page_table.data_ptr(),
+                           self.max_pages, page_table.stride(0) if self.B > 1 else self.max_pages)
+
+    @classmethod
+    def empty(cls, num_pages: int, Hkv: int, page_size: int, D: int, page_table: torch.Tensor,
+              block: int = 32, dtype: torch.dtype = torch.bfloat16) -> "QuantCache":
+        """New pages of zeros on the table's device."""
+        if block < 1 or page_size % block:
+            raise ValueError(f"block must divide page_size, got {block} and {page_size}")
+        dev = page_table.device
+        pages = [torch.zeros(num_pages, Hkv, page_size, D, dtype=torch.uint8, device=dev)
+                 .view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.full((num_pages, Hkv, page_size // block), 127, dtype=torch.uint8, device=dev)
+                  for _ in range(2)]
+        return cls(*pages, *scales, page_table, dtype)
+
+
+_NO_NORM = (None, -1, -1)
+
+
+def ddtree_norm_rope(q, k, pos, norm: HeadNorm, rotary: Optional[Rotary] = None, q_out=None,
+                     k_out=None, stream=None):
+    """Norms every head of q and, unless it is None, k and rotates them for pos, as
+    ddtree_rope takes them; in place where no output is given.  A token at a negative
+    position is copied as it is."""
+    turns, where = (None, None) if rotary is None else (rotary._c, rotary._index)
+    st = _ddtree.norm_rope(q, k, pos, *norm._c, turns, where, q_out, k_out,
+                           _raw("ddtree_norm_rope", stream, _index(q)))
+    if st:
+        raise DDTreeError("ddtree_norm_rope", st)
+
+
+def norm_rope(q, k, pos, norm: HeadNorm, rotary: Optional[Rotary] = None, stream=None):
+    """ddtree_norm_rope into new tensors: (q, k); k may be None."""
+    made = _empty(stream, *[(x.shape, x.dtype, x.device) for x in (q, k) if x is not None])
+    q_out, k_out = made[0], made[1] if len(made) > 1 else None
+    ddtree_norm_rope(q, k, pos, norm, rotary, q_out, k_out, stream)
+    return q_out, k_out
+
+
+def ddtree_append_q8(k, v, first, at, cache: QuantCache, rotary: Optional[Rotary] = None,
+                     norm: Optional[HeadNorm] = None, q=None, q_out=None, stream=None):
+    """Quantises runs of tokens into the cache: tokens first[b] .. first[b + 1] - 1 (first int32
+    [B + 1]) become positions at[b].. (int32 [B]) of sequence b, k normed and rotated on the
+    way if a norm and a rotary are given, and their queries q likewise, in place unless
+    q_out is given."""
+    turns, where = (None, None) if rotary is None else (rotary._c, rotary._index)
+    st = _ddtree.append_q8(cache._c, cache._index, cache.B, k, v, first, at, turns, where,
+                           *(_NO_NORM if norm is None else norm._c), q, q_out,
+                           _raw("ddtree_append_q8", stream, cache._index), cache.k_pages,
+                           cache.v_pages, cache.k_scales, cache.v_scales)
+    if st:
+        raise DDTreeError("ddtree_append_q8", st)
+
+
+def ddtree_commit_q8(cache: QuantCache, k_tree, v_tree, accept_len, accepted_nodes, prefix_len,
+                     new_len=None, stream=None):
+    """ddtree_commit_paged into an 8-bit cache."""
+    st = _ddtree.commit_q8(cache._c, cache._index, cache.B, k_tree, v_tree, accept_len,
+                           accepted_nodes, prefix_len, new_len,
+                           _raw("ddtree_commit_q8", stream, cache._index), cache.k_pages,
+                           cache.v_pages, cache.k_scales, cache.v_scales)
+    if st:
+        raise DDTreeError("ddtree_commit_q8", st)
+
+
+def ddtree_read_q8(cache: QuantCache, first, at, k_out, v_out, stream=None):
+    """Reads runs of positions back in the tokens' type: position at[b] + i of sequence b
+    becomes row first[b] + i of k_out and v_out ([tokens][Hkv][D])."""
+    st = _ddtree.read_q8(cache._c, cache._index, cache.B, first, at, k_out, v_out,
+                         _raw("ddtree_read_q8", stream, cache._index))
+    if st:
+        raise DDTreeError("ddtree_read_q8", st)
+
+
+def q8_attn_workspace(q, cache: QuantCache) -> torch.Tensor:
+    """A workspace for ddtree_tree_attn_q8 of q's sizes over the cache."""
+    B, R, Hq, D = q.shape
+    with torch.cuda.device(cache._index):
+        n = workspace_size(OP_TREE_ATTN_Q8, B=B, N=R - 1, Hq=Hq, Hkv=cache.Hkv, D=D,
+                           cache_cap=cache.max_pages * cache.page_size)
+    return alloc_workspace(n, cache.device)
+
+
+def ddtree_tree_attn_q8(q, cache: QuantCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask, out,
+                        lse=None, scale=None, workspace=None, stream=None):
+    """ddtree_tree_attn_paged over an 8-bit cache; q, k_tree, v_tree and out of its dtype."""
+    st = _ddtree.tree_attn_q8(cache._c, cache._index, cache.B, q, k_tree, v_tree, prefix_len,
+                              n_nodes, anc_mask, out, lse, scale, workspace,
+                              _raw("ddtree_tree_attn_q8", stream, cache._index))
+    if st:
+        raise DDTreeError("ddtree_tree_attn_q8", st)
+
+
+def tree_attn_q8(q, cache: QuantCache, k_tree, v_tree, prefix_len, n_nodes, anc_mask, scale=None,
+                 want_lse=True, workspace=None, stream=None):
+    B, R, Hq, _ = q.shape
+    specs = [(q.shape, q.dtype, q.device), ((B, R, Hq), torch.float32, q.device)]
+    made = _empty(stream, *specs[:2 if want_lse else 1])
+    out, lse = made[0], made[1] if want_lse else None
+    if workspace is None:  # (its zeros have to be on the call's stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = q8_attn_workspace(q, cache)
+    ddtree_tree_attn_q8(q, cache, k_tree, v_tree, prefix_len, n_nodes, anc_mask, out, lse, scale,
+                        workspace, stream)
+    return out, lse

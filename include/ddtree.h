@@ -60,7 +60,7 @@ typedef enum {
     DDTREE_ERR_DEVICE = 4       /* a kernel recorded bad device-side data or a timeout */
 } ddtree_status;
 
-/* DDTREE_FP16 is taken by the paged-cache calls and ddtree_rope only. */
+/* DDTREE_FP16 is taken by the paged-cache calls, ddtree_rope and ddtree_norm_rope only. */
 typedef enum { DDTREE_BF16 = 0, DDTREE_FP32 = 1, DDTREE_FP16 = 2 } ddtree_dtype;
 
 /* Operation ids for ddtree_workspace_size. */
@@ -68,21 +68,23 @@ typedef enum {
     DDTREE_OP_TOPK = 0,
     DDTREE_OP_TREE_ATTN = 2,
     DDTREE_OP_ACCEPT = 3,
-    DDTREE_OP_TREE_ATTN_PAGED = 4
+    DDTREE_OP_TREE_ATTN_PAGED = 4,
+    DDTREE_OP_TREE_ATTN_Q8 = 5
 } ddtree_op;
 
 /* Upper limits of this implementation. */
 #define DDTREE_MAX_K 32
 #define DDTREE_MAX_L 16
 #define DDTREE_MAX_N 1024
-#define DDTREE_MAX_ROPE_D 512 /* head dimension of ddtree_rope / ddtree_append_paged */
+#define DDTREE_MAX_ROPE_D 512 /* head dimension of ddtree_rope / _norm_rope / _append_paged */
+#define DDTREE_MAX_Q8_BLOCK 64 /* positions that share a scale of an 8-bit cache */
 
 /* Bytes of workspace that `op` needs for the given sizes (0 if it needs none,
  * or on an invalid combination).  Arguments an op does not use are ignored:
  *   TOPK:      rows = B*L, V, K, dtype
  *   TREE_ATTN: B, N, Hq, Hkv, D, cache_cap
  *   ACCEPT:    B, N, V, dtype
- *   TREE_ATTN_PAGED: B, N, Hq, Hkv, D, cache_cap = max_pages * page_size */
+ *   TREE_ATTN_PAGED, TREE_ATTN_Q8: B, N, Hq, Hkv, D, cache_cap = max_pages * page_size */
 size_t ddtree_workspace_size(ddtree_op op, int B, int L, int N, int V, int K, int dtype, int Hq,
                              int Hkv, int D, int64_t cache_cap);
 
@@ -436,11 +438,118 @@ ddtree_status ddtree_commit_paged(const ddtree_paged_cache* cache, const ddtree_
                                   const int32_t* accepted_nodes, const int32_t* prefix_len,
                                   int32_t* new_len, int B, int L, int N, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The round over an 8-BIT paged cache, half the bytes of a 16-bit one, and the
+ * norm of queries and keys that some target models put before the rotation:
+ *
+ *   ddtree_norm_rope     norm and rotation of the tree's queries and keys
+ *   ddtree_append_q8     prompts, or one token a sequence, quantised into the pages,
+ *                        queries and keys normed and rotated on the way
+ *   ddtree_tree_attn_q8  step 3 over the pages
+ *   ddtree_commit_q8     the accepted path, quantised into the pages
+ *   ddtree_read_q8       a sequence's keys and values back in 16 bits
+ *
+ * The tree's own keys and values, queries and outputs stay in 16 bits. */
+
+/* The norm of a head of D elements: y = x / sqrt(mean x^2 + eps) * weight.  A NULL
+ * weight counts as ones.  (Where a model adds one to its weights, so do these.) */
+typedef struct {
+    const float *q_weight, *k_weight; /* DEVICE [D] */
+    float eps;                        /* > 0 */
+} ddtree_head_norm;
+
+/* ddtree_rope with the norm of every head before the rotation, in one pass: the
+ * same tensors, types, alignment rules and limits.  rot may be NULL: the norm
+ * alone.  Norm, rotation and their sums are formed in 32 bits and rounded once.  A
+ * token at a negative position is copied as it is. */
+ddtree_status ddtree_norm_rope(const ddtree_rows* q, const ddtree_rows* q_out,
+                               const ddtree_rows* k, const ddtree_rows* k_out, int dtype, int T,
+                               int D, const int32_t* pos, const ddtree_head_norm* norm,
+                               const ddtree_rotary* rot, void* stream);
+
+/* A paged cache of e4m3 codes.  A code c in a block of `block` consecutive positions of
+ * a page and KV head stands for c * 2^(x - 127), x the block's byte in k_scales or
+ * v_scales.  A power of two as scale makes every value exact in the tokens' 16-bit
+ * type, and moves a block to a larger scale by an exponent.  Rows and positions are
+ * placed as in a ddtree_paged_cache, strides in bytes and multiples of 16; the block of
+ * slot s of page g and head h is byte g * Hkv * n + h * n + s / block, n = page_size / block.
+ * Scales: the writers choose x - 127 as the least e at which the block's largest
+ * element is at most 448 * 2^e, from -96 (bf16 tokens) or -15 (fp16) to 7; elements beyond
+ * 448 * 2^7 become that.  A byte outside this range counts as the range's nearer end.
+ * Codes 0x7F and 0xFF, which no writer makes of finite elements, count as 480 and -480.
+ * D in {64, 128}; page_size a power of two of at least 8; block a power of two, 8 to
+ * min(page_size, DDTREE_MAX_Q8_BLOCK); max_pages * page_size at most 2^30. */
+typedef struct {
+    void *k_pages, *v_pages;          /* DEVICE, 16-byte aligned */
+    uint8_t *k_scales, *v_scales;     /* DEVICE [num_pages][Hkv][page_size / block], 16-byte aligned */
+    int32_t dtype;                    /* of the tokens: DDTREE_BF16 or DDTREE_FP16 */
+    int32_t num_pages, page_size, block, Hkv, D;
+    int64_t page_stride, head_stride, slot_stride;
+    const int32_t* page_table; /* DEVICE [B][table_stride] */
+    int32_t max_pages;         /* entries of a sequence, <= table_stride */
+    int64_t table_stride;
+} ddtree_q8_cache;
+
+/* Appends runs of tokens to an 8-bit cache: tokens first[b] .. first[b + 1] - 1 become
+ * positions at[b], at[b] + 1, ... of sequence b.
+ *   k, v       in, cache->Hkv heads each, T tokens, of the cache's dtype and D.
+ *   first      int32 [B + 1], ascending, within 0..T (first[0] need not be 0, and tokens
+ *              outside all runs, the padding of a fixed shape, are not looked at).
+ *   at         int32 [B].
+ *   rot, norm  the rotation (for the token's position) and norm of keys and queries,
+ *              either NULL to leave it out; rot_dim a multiple of 16.
+ *   q, q_out   the tokens' queries, normed and rotated in 16 bits, as in ddtree_rope
+ *              (q_out is q's own tensor or overlaps no input); both NULL to leave them
+ *              out.  Rows of tokens outside all runs stay as they are.
+ * A block of the cache that a run enters in its middle holds earlier positions: its
+ * scale becomes the larger of what it was and what the new elements need, and if it
+ * grows the earlier codes move to it, rounded once more where they fall below its
+ * normal numbers.  A block entered at its first position takes the scale of its new elements;
+ * codes behind a run's end are left as they are.  Elements are quantised from 32 bits, to
+ * the nearest, ties to even.
+ * A run whose tokens lie outside 0..T or whose positions lie outside the table is
+ * left out, queries too, and recorded; so is the part of a run whose page lies outside
+ * the pool (its queries are still written).  The pages written belong to one sequence
+ * alone.  The caller's lengths are not changed.  T = 0 does nothing.  Every pointer
+ * 16-byte aligned, strides of rows multiples of 8 elements.  No workspace. */
+ddtree_status ddtree_append_q8(const ddtree_rows* k, const ddtree_rows* v, int T,
+                               const int32_t* first, const int32_t* at, int B,
+                               const ddtree_q8_cache* cache, const ddtree_rotary* rot,
+                               const ddtree_head_norm* norm, const ddtree_rows* q,
+                               const ddtree_rows* q_out, void* stream);
+
+/* ddtree_commit_paged into an 8-bit cache: the same arguments and refusals (a path that
+ * does not fit leaves its sequence unchanged), the rows quantised as ddtree_append_q8
+ * does it. */
+ddtree_status ddtree_commit_q8(const ddtree_q8_cache* cache, const ddtree_rows* k_tree,
+                               const ddtree_rows* v_tree, const int32_t* accept_len,
+                               const int32_t* accepted_nodes, const int32_t* prefix_len,
+                               int32_t* new_len, int B, int L, int N, void* stream);
+
+/* Reads runs of positions back in 16 bits: position at[b] + i of sequence b becomes row
+ * first[b] + i of k_out and v_out (out, T tokens, cache->Hkv heads of its dtype and D;
+ * neither overlaps the other or the cache), for rows first[b] .. first[b + 1] - 1; first and
+ * at as in ddtree_append_q8.  Rows outside all runs, of a run outside the table (recorded)
+ * or of a page outside the pool (recorded) stay as they are.  No workspace. */
+ddtree_status ddtree_read_q8(const ddtree_q8_cache* cache, const int32_t* first,
+                             const int32_t* at, int B, const ddtree_rows* k_out,
+                             const ddtree_rows* v_out, int T, void* stream);
+
+/* ddtree_tree_attn_paged with the prefix in an 8-bit cache: the same formula over the
+ * values that its codes stand for, the same tree inputs, outputs, sizes and padding
+ * rules.  q, k_tree, v_tree and out are of the cache's dtype.
+ * Workspace: ddtree_workspace_size(DDTREE_OP_TREE_ATTN_Q8, ...). */
+ddtree_status ddtree_tree_attn_q8(const ddtree_rows* q, const ddtree_q8_cache* cache,
+                                  const ddtree_rows* k_tree, const ddtree_rows* v_tree,
+                                  const int32_t* prefix_len, const int32_t* n_nodes,
+                                  const uint32_t* anc_mask, int B, int N, float scale, void* out,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns DDTREE_OK, DDTREE_ERR_DEVICE (and the recorded code in
  * *detail when non-null: which kernel and what was wrong), or DDTREE_ERR_CUDA.
  * Code: high byte = kernel (1 top-K, 2 build, 3 tree attention, 4 accept,
- * 5 commit, 6 append, 15 ddtree_selftest_wait), low byte = reason (1 bad prefix
+ * 5 commit, 6 append, 7 read, 15 ddtree_selftest_wait), low byte = reason (1 bad prefix
  * length, 2 bad node count, 3 bad tree or path, 4 a bounded wait timed out, 5
  * bad input, 6 internal plan, 7 a page number outside the pool). */
 ddtree_status ddtree_device_check(void* stream, uint32_t* detail);
