@@ -38,7 +38,8 @@
 // tile holds up to floor(128 / G) nodes) and cut a sequence's tiles by its own
 // length rather than by the table's capacity.  kLeftBf16 / kLeftFp16 are those for
 // many units with two warps more, for a few rows that whole pairs of tiles leave
-// over (left_rows).
+// over (left_rows).  kQ8Bf16 / kQ8Fp16 read an 8-bit cache, with four warps more that widen
+// its tiles (widen_tile).
 #pragma once
 
 #include <mutex>
@@ -49,6 +50,7 @@
 #include <type_traits>
 #include <map>
 
+#include "q8.cuh"
 #include "tree_attn_common.cuh"
 
 #include "../../include/ddtree.h"
@@ -108,10 +110,24 @@ struct Cfg {
 
 // Where the prefix lives, and the 16-bit type of everything; LEFT: with two warps for
 // the rows that the query tiles leave over.
-constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4;
-constexpr bool is_left(int mode) { return mode >= kLeftBf16; }
-constexpr bool is_f16(int mode) { return mode == kPagedFp16 || mode == kLeftFp16; }
-constexpr int threads_of(int mode) { return kThreads + (is_left(mode) ? 64 : 0); }
+constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4, kQ8Bf16 = 5, kQ8Fp16 = 6;
+constexpr bool is_left(int mode) { return mode == kLeftBf16 || mode == kLeftFp16; }
+constexpr bool is_q8(int mode) { return mode >= kQ8Bf16; }
+constexpr bool is_f16(int mode) { return mode == kPagedFp16 || mode == kLeftFp16 || mode == kQ8Fp16; }
+constexpr int kWideners = 4;  // warps that widen an 8-bit cache's tiles
+constexpr int threads_of(int mode) { return kThreads + (is_left(mode) ? 64 : is_q8(mode) ? 32 * kWideners : 0); }
+// Tiles of codes (K's or V's) that wait to be widened: RAW of them behind the K and V
+// stages, and a lone query tile leaves room for two more where the second one would be.
+template <int D>
+struct RawCfg {
+    static constexpr int BYTES = BN * D;
+    static constexpr int SLOTS = D == 128 ? 2 : 6;
+    static constexpr int MORE = D == 128 ? 2 : 0;
+    static_assert(MORE * BYTES <= Cfg<D>::QT_BYTES, "room of the second query tile");
+    static_assert(SLOTS * BYTES >= 3 * BM * 8, "(m, l) rows of both groups and the second halves");
+};
+template <int D, int MODE>
+constexpr int smem_of() { return Cfg<D>::SMEM + (is_q8(MODE) ? RawCfg<D>::SLOTS * RawCfg<D>::BYTES : 0); }
 constexpr int kLeftRows = 8;  // rows left over, at most: the narrow side of mma.sync
 
 struct Params {
@@ -147,6 +163,13 @@ struct PagedParams : Params {
     float* part_left;        // global merge: [B*Hkv][smax][kLeftRows][D + 4] O, m, l
     unsigned int* tickets_left;  // ... [B*Hkv]
 };
+
+struct Q8Params : PagedParams {
+    const uint8_t *k_scales, *v_scales;
+    int block_log2, per_page_log2;  // log2 of positions a scale, of scales a page and head
+};
+template <int MODE>
+using ParamsOf = std::conditional_t<MODE == kDense, Params, std::conditional_t<is_q8(MODE), Q8Params, PagedParams>>;
 
 // Named barrier over the 256 softmax threads (both query tiles).
 DDT_DEV void softmax_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -546,6 +569,67 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
     }
 }
 
+// The tiles of an 8-bit cache, widened for the tensor core.  tcgen05 takes both factors of a
+// product in one 16-bit type or both in 8 bits; queries and softmax weights in 8 bits
+// would need two or three such parts each (a weight 2^-18 of its row's largest would
+// be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
+// turn codes into the tokens' type between the copy and the tensor core: the kernel's
+// other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
+//
+// A pair of codes becomes a pair of elements by moving each code's exponent and
+// significand bits to the type's places and its sign bit to the top -- a number 2^-8
+// (fp16) or 2^-120 (bf16) of the code's, subnormal codes included -- and one packed
+// product with the block's scale and that power: 5 instructions a pair.
+template <bool F16>
+DDT_DEV uint32_t widen2(uint32_t codes, uint32_t sel, uint32_t mult) {
+    const uint32_t t = __byte_perm(codes, 0u, sel);  // the two codes at bytes 1 and 3
+    uint32_t r = (F16 ? (t >> 1) & 0x3f803f80u : (t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+    if constexpr (F16) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
+    else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
+    return r;
+}
+// That power of two for a scale byte, as the type's bits.
+template <bool F16>
+DDT_DEV uint32_t widen_factor(uint32_t byte) {
+    const int e = q8_from_byte(byte, q8_least(F16));
+    return F16 ? (uint32_t)(23 + e) << 10 : (uint32_t)(247 + e) << 7;
+}
+// Widens a tile of codes [128 keys][D] into [D / 64] swizzled slabs, keys by `mult` (two
+// equal halves a word); thread i of 32 kWideners.  The threads of a second slab store
+// their halves the other way round: 8 lanes then store to 8 different 16-byte banks.
+template <int D, bool F16>
+DDT_DEV void widen_tile(const uint8_t* raw, const uint16_t* mult, uint8_t* tile, int i) {
+    constexpr int CH = D / 16;                        // 16-byte chunks of a row
+    constexpr int STEP = 32 * kWideners / CH;         // rows of a pass
+    const int c = i % CH, r0 = i / CH;
+    const int slab = c >> 2, flip = slab & 1;
+    constexpr int BATCH = 4;
+#pragma unroll 1
+    for (int p0 = 0; p0 < BN / STEP; p0 += BATCH) {
+        uint4 w[BATCH];
+        uint32_t m[BATCH];
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p) {
+            const int r = r0 + (p0 + p) * STEP;
+            w[p] = *(const uint4*)(raw + r * D + c * 16);
+            m[p] = (uint32_t)mult[r] * 0x10001u;
+        }
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p) {
+            const int r = r0 + (p0 + p) * STEP;
+            uint4 y[2];
+            y[0] = make_uint4(widen2<F16>(w[p].x, 0x1404u, m[p]), widen2<F16>(w[p].x, 0x3424u, m[p]),
+                              widen2<F16>(w[p].y, 0x1404u, m[p]), widen2<F16>(w[p].y, 0x3424u, m[p]));
+            y[1] = make_uint4(widen2<F16>(w[p].z, 0x1404u, m[p]), widen2<F16>(w[p].z, 0x3424u, m[p]),
+                              widen2<F16>(w[p].w, 0x1404u, m[p]), widen2<F16>(w[p].w, 0x3424u, m[p]));
+            uint8_t* to = tile + slab * kHalfBytes;
+            const int first = (c & 3) * 2;
+            *(uint4*)(to + swz(r, first + flip)) = flip ? y[1] : y[0];
+            *(uint4*)(to + swz(r, first + 1 - flip)) = flip ? y[0] : y[1];
+        }
+    }
+}
+
 // One CTA = one (sequence b, KV head g, pair of 128-row query tiles, KV split).
 // Warp 0: TMA producer.  Warp 1: TMEM owner and MMA issuer.  Warps 2-5: softmax
 // of query tile 0; warps 6-9: softmax of query tile 1.  Per KV tile j the
@@ -561,9 +645,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_vc,
                  const __grid_constant__ CUtensorMap tm_kt,
                  const __grid_constant__ CUtensorMap tm_vt,
-                 const std::conditional_t<MODE == kDense, Params, PagedParams> p) {
+                 const ParamsOf<MODE> p) {
     using C = Cfg<D>;
-    constexpr bool PAGED = MODE != kDense, F16 = is_f16(MODE), LEFT = is_left(MODE);
+    constexpr bool PAGED = MODE != kDense, F16 = is_f16(MODE), LEFT = is_left(MODE), Q8 = is_q8(MODE);
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
@@ -572,8 +656,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ bool s_last, s_ok;
-    __shared__ float2 s_ml[PAGED ? 2 * BM : 1];  // paged cluster merge: (m, l) of the rows
-    __shared__ float2 s_ml1[BM];  // lone tile: (m, l) of the second group's key halves
+    __shared__ float2 s_ml_own[PAGED && !Q8 ? 2 * BM : 1];  // paged cluster merge: (m, l) of the rows
+    __shared__ float2 s_ml1_own[Q8 ? 1 : BM];  // lone tile: (m, l) of the second group's key halves
+    using Raw = RawCfg<D>;
+    constexpr int NR = Q8 ? Raw::SLOTS + Raw::MORE : 1;
+    __shared__ __align__(8) uint64_t bar_rfull[NR], bar_rempty[NR];  // tiles of codes
+    __shared__ uint16_t s_mult[Q8 ? NR : 1][Q8 ? BN : 1];            // ... their keys' factors
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one number a warp
@@ -582,11 +670,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (tid == 0) {
         mbar_init(&bar_q, 1);
         constexpr int readers = LEFT ? 3 : 1;  // the tensor core, and two warps for the rows left over
+        constexpr int writers = Q8 ? kWideners : 1;
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar_kfull[s], 1);
+            mbar_init(&bar_kfull[s], writers);
             mbar_init(&bar_kempty[s], readers);
-            mbar_init(&bar_vfull[s], 1);
+            mbar_init(&bar_vfull[s], writers);
             mbar_init(&bar_vempty[s], readers);
+        }
+        for (int s = 0; Q8 && s < NR; ++s) {
+            mbar_init(&bar_rfull[s], 1);
+            mbar_init(&bar_rempty[s], kWideners);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&bar_sfull[k][0], 1);
@@ -778,6 +871,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint8_t* sq = base;                          // two query tiles
     uint8_t* sk = sq + 2 * C::QT_BYTES;          // NS stages of K
     uint8_t* sv = sk + NS * C::KV_BYTES;         // NS stages of V
+    uint8_t* sr = sv + NS * C::KV_BYTES;         // (8-bit cache) tiles of codes
+    const int raws = Raw::SLOTS + (dual ? Raw::MORE : 0);
+    auto raw_at = [&](int s) { return s < Raw::SLOTS ? sr + s * Raw::BYTES : sq + C::QT_BYTES + (s - Raw::SLOTS) * Raw::BYTES; };
+    // (every tile of codes is widened when these are written)
+    float2* s_ml = Q8 ? reinterpret_cast<float2*>(sr) : s_ml_own;
+    float2* s_ml1 = Q8 ? reinterpret_cast<float2*>(sr) + 2 * BM : s_ml1_own;
 
     auto fail = [&]() {
         record_error(p.err, ERR_ATTN | ERR_WAIT_TIMEOUT);
@@ -826,6 +925,79 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return num_pages;
         };
         int ids = checked(ids_of(0), 0), next_ids = ids_of(1);
+        if constexpr (Q8) {
+            // Codes of the prefix tiles, K of tile i and then V of tile i - 1, each a slot of
+            // the ring, with their keys' factors.  Scales come with the page numbers, 32
+            // boxes at a time (lane l the up to 16 bytes of box 32 k + l), a batch ahead of
+            // their use: page numbers two ahead.
+            const int per_box_log2 = max(0, 31 - __clz(box) - p.block_log2), per_box = 1 << per_box_log2;
+            auto scales_of = [&](int page, int k, const uint8_t* from) {
+                uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                if (page == num_pages) return y;
+                const int slot = (t_begin * BN + (k * 32 + lane) * box) & (ps - 1);
+                const uint8_t* at = from + ((((int64_t)page * p.Hkv + g) << p.per_page_log2) + (slot >> p.block_log2));
+                if (per_box == 1) y.x = __ldg(at);
+                else if (per_box == 2) y.x = __ldg((const uint16_t*)at);
+                else if (per_box == 4) y.x = __ldg((const uint32_t*)at);
+                else if (per_box == 8) *(uint2*)&y = __ldg((const uint2*)at);
+                else y = __ldg((const uint4*)at);
+                return y;
+            };
+            int id1 = checked(next_ids, 1);
+            next_ids = ids_of(2);
+            uint4 k0 = scales_of(ids, 0, p.k_scales), v0 = scales_of(ids, 0, p.v_scales);
+            uint4 k1 = scales_of(id1, 1, p.k_scales), v1 = scales_of(id1, 1, p.v_scales);
+            int c = 0, ring = 0, turn = 0;
+            bool ok = true;
+            for (int i = 0; ok && i <= nprefix; ++i) {
+                const int ids_v = ids;  // the batch of tile i - 1
+                const uint4 v_now = v0;
+                if (i > 0 && (i * nb & 31) == 0) {
+                    const int k = i * nb / 32;
+                    ids = id1, k0 = k1, v0 = v1;
+                    id1 = checked(next_ids, k + 1);
+                    next_ids = ids_of(k + 2);
+                    k1 = scales_of(id1, k + 1, p.k_scales), v1 = scales_of(id1, k + 1, p.v_scales);
+                }
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int j = i - v;
+                    if (j < 0 || j >= nprefix) continue;
+                    ok = mbar_wait_warp(&bar_rempty[ring], turn ^ 1, &s_abort);
+                    if (!ok) break;
+                    const int mine = v ? ids_v : ids;
+                    const uint4 y = v ? v_now : k0;
+                    // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
+                    const int src = (j * nb + 4 * lane / box) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
+                    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
+                    if (per_box > 4) {
+                        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
+                                       w3 = __shfl_sync(0xffffffffu, y.w, src);
+                        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
+                    }
+                    const uint32_t m = widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
+                    *(uint2*)&s_mult[ring][4 * lane] = make_uint2(m, m);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
+                    __syncwarp();
+                    const uint32_t to = smem_u32(raw_at(ring));
+                    const int key0 = (t_begin + j) * BN;
+#pragma unroll 4
+                    for (int x = 0; x < nb; ++x) {
+                        const int page = __shfl_sync(0xffffffffu, mine, (j * nb + x) & 31);
+                        tma_load_4d_warp(lead, to + x * box * D, v ? &tm_vc : &tm_kc, &bar_rfull[ring], 0,
+                                         (key0 + x * box) & (ps - 1), g, page);
+                    }
+                    ++c;
+                    if (++ring == raws) ring = 0, turn ^= 1;
+                }
+            }
+            if (!ok) fail();
+            // (where a wait gave up, no copy may land in memory given back)
+            mbar_wait(&bar_q, 0, nullptr, 100000000ull);
+            for (int x = max(0, c - raws); x < c; ++x)
+                mbar_wait(&bar_rfull[x % raws], (x / raws) & 1, nullptr, 100000000ull);
+        } else {
         int issued[2] = {0, 0};  // tiles of K, of V
         for (int i = 0; i <= nt; ++i) {
             const int ids_v = ids;  // the batch of tile i - 1
@@ -882,6 +1054,57 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int v = 0; v < 2; ++v)
             for (int j = max(0, issued[v] - NS); j < issued[v]; ++j)
                 mbar_wait(v ? &bar_vfull[j % NS] : &bar_kfull[j % NS], (j / NS) & 1, nullptr, 100000000ull);
+        }
+    } else if (Q8 && warp >= 10) {
+        // ================= 8-bit cache: codes to 16-bit tiles =====================
+        // In the ring's order.  A tree tile is 16-bit already: the first of these warps
+        // has it copied in its turn.
+        if constexpr (Q8) {
+            const uint32_t lead = elect_one();
+            const int wi = warp - 10;
+            int ring = 0, turn = 0, issued[2] = {0, 0};
+            bool ok = true;
+            for (int i = 0; ok && i <= nt; ++i) {
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int j = i - v, s = j % NS;
+                    if (j < 0 || j >= nt) continue;
+                    uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
+                    uint8_t* to = (v ? sv : sk) + s * C::KV_BYTES;
+                    const bool codes = j < nprefix;
+                    if (codes) ok = mbar_wait_warp(&bar_rfull[ring], turn, &s_abort);
+                    ok = ok && mbar_wait_warp(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
+                    if (!ok) break;
+                    if (codes) {
+                        widen_tile<D, F16>(raw_at(ring), s_mult[ring], to, wi * 32 + lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(full);
+                            mbar_arrive(&bar_rempty[ring]);
+                        }
+                        if (++ring == raws) ring = 0, turn ^= 1;
+                    } else if (wi == 0) {
+                        if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
+                        __syncwarp();
+                        const int a0 = (tree_first + j - nprefix) * BN;
+#pragma unroll
+                        for (int h = 0; h < C::NH; ++h)
+                            tma_load_3d_warp(lead, smem_u32(to) + h * kHalfBytes, v ? &tm_vt : &tm_kt, full, 64 * h, g,
+                                             b * R + a0);
+                        if (v) issued[1] = j + 1;
+                        else issued[0] = j + 1;
+                    } else if (lane == 0) {
+                        mbar_arrive(full);
+                    }
+                }
+            }
+            if (!ok) fail();
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                for (int j = max(nprefix, issued[v] - NS); j < issued[v]; ++j)
+                    mbar_wait(v ? &bar_vfull[j % NS] : &bar_kfull[j % NS], (j / NS) & 1, nullptr, 100000000ull);
+        }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
         // The whole warp runs the loop and one lane issues: per key tile j and query
@@ -1198,7 +1421,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tmem_st_wait();
             l += sum;
-            if (k == 0 && quarter * 32 + 32 > lim_t) {  // (the warp as a whole)
+            // (the widened rows of an 8-bit cache are numbers, whatever their codes)
+            if (k == 0 && quarter * 32 + 32 > lim_t && (!Q8 || is_tree)) {  // (the warp as a whole)
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
                 if (!mbar_wait_warp(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
@@ -1448,7 +1672,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const bool row_valid = mine && u <= n && r < rows_used;
             fence_proxy_async_smem();
             cluster_sync();
-            if (warp >= 2 && mine && !idle && s_ok) {
+            const bool rows_warp = warp >= 2 && (!Q8 || warp < 10);
+            if (rows_warp && mine && !idle && s_ok) {
                 tc_fence_after();
                 const uint32_t tm_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + tile * D;
                 float2 ml = s_ml[row2];
@@ -1493,7 +1718,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tc_fence_before();
             }
             cluster_sync();
-            if (warp >= 2 && (tile == 0 || tile1) && u < R && r < rows_used) {
+            if (rows_warp && (tile == 0 || tile1) && u < R && r < rows_used) {
                 // (four splits at a time, those past the last with weight 0)
                 const float2* ml = reinterpret_cast<const float2*>(base + S * slot) + row2;
                 float M = -INFINITY, Ls = 0.f, w[kMaxSplits], ls[kMaxSplits];
@@ -1825,14 +2050,14 @@ constexpr int kLoneTiles = 80;
 struct ManyPlan : Plan {
     int left;
 };
-ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms) {
+ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms, bool take_along = true) {
     ManyPlan pl{};
     (Plan&)pl = plan_base(N, Hq, Hkv);
     const int G = Hq / Hkv, left = (N + 1 - (pl.mtiles - 1) * (BM / G)) * G;
     if (plan_units(pl, B, Hkv) < sms) return pl;  // few units (smax = 0)
     const long along = (long)B * Hkv * (pl.mpairs - 1);  // units if the pairs take them
     const bool short_wave = pl.mpairs == 2 && along * 10 < sms * 7L && t.prefix + t.tree <= kLoneTiles;
-    if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
+    if (take_along && pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
         --pl.mtiles;
         --pl.mpairs;
         pl.left = left;
@@ -1876,8 +2101,8 @@ int active_clusters(int dev, int size) {
     if (!known) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)size);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+        cfg.blockDim = dim3(threads_of(MODE));
+        cfg.dynamicSmemBytes = smem_of<D, MODE>();
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
         at.val.clusterDim.x = (unsigned)size;
@@ -1903,7 +2128,7 @@ cudaError_t prepare_kernel(int dev) {
     static cudaError_t attr_err[64];
     std::call_once(once[dev & 63], [&] {
         cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, MODE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D, MODE>());
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(tree_attn_kernel<D, MODE>,
                                      cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

@@ -139,6 +139,21 @@ bool page_map(CUtensorMap* m, const PagedArgs& c, const void* pages, int rows, b
     return make_map(m, pages, d, f16);
 }
 
+// Pages of an 8-bit cache: boxes of a head's whole rows, not swizzled.
+template <int D>
+bool code_map(CUtensorMap* m, const Q8Args& c, const void* pages, int rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    auto stride = [](int64_t bytes, int size) { return size > 1 ? (cuuint64_t)bytes : (cuuint64_t)D; };
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {stride(c.slot_stride, c.page_size), stride(c.head_stride, c.Hkv),
+                                   stride(c.page_stride, c.num_pages)};
+    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)std::min(c.page_size, rows), 1, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pages), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 // The kernel for few query rows (tree_attn_rows.cu): whether it takes a shape,

@@ -1,5 +1,5 @@
 // tree_attn_paged.cuh -- launch of the tree-attention kernel (tree_attn.cuh) over a
-// paged cache.
+// paged cache, 16-bit (PagedAttnArgs) or 8-bit (Q8AttnArgs).
 #pragma once
 #include "tree_attn.cuh"
 
@@ -7,8 +7,17 @@ namespace ddt {
 
 namespace {
 
-template <int D, int MODE>
-cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
+template <int D>
+bool cache_map(CUtensorMap* m, const PagedArgs& c, const void* pages, bool f16) {
+    return page_map<D>(m, c, pages, BN, f16);
+}
+template <int D>
+bool cache_map(CUtensorMap* m, const Q8Args& c, const void* pages, bool) {
+    return code_map<D>(m, c, pages, BN);
+}
+
+template <int D, int MODE, typename Args>
+cudaError_t launch_mode(const Args& a, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (const cudaError_t e = prepare_kernel<D, MODE>(dev)) return e;
@@ -17,7 +26,7 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     const int G = Hq / Hkv, R = a.N + 1;
     const Tiles t = max_tiles(a.N, cap);
     const int sms = num_sms();
-    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms);
+    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms, !is_q8(MODE));
     PagedPlan pl{};
     if (many.smax) {
         (Plan&)pl = many;
@@ -33,9 +42,9 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     CUtensorMap mq, mkc, mvc, mkt, mvt;
     if (!tree_map<D>(&mq, a.q, tokens, G, pl.npt, f16) || !tree_map<D>(&mkt, a.k_tree, tokens, 1, BN, f16) ||
         !tree_map<D>(&mvt, a.v_tree, tokens, 1, BN, f16) ||
-        !page_map<D>(&mkc, a.cache, a.cache.k, BN, f16) || !page_map<D>(&mvc, a.cache, a.cache.v, BN, f16))
+        !cache_map<D>(&mkc, a.cache, a.cache.k, f16) || !cache_map<D>(&mvc, a.cache, a.cache.v, f16))
         return cudaErrorInvalidValue;
-    PagedParams p{};
+    ParamsOf<MODE> p{};
     p.prefix_len = a.prefix_len;
     p.n_nodes = a.n_nodes;
     p.anc_mask = a.anc_mask;
@@ -71,10 +80,16 @@ cudaError_t launch_mode(const PagedAttnArgs& a, cudaStream_t s) {
     for (p.ps_log2 = 0; (1 << p.ps_log2) < ps;) ++p.ps_log2;
     p.npt = pl.npt;
     p.single = pl.single;
+    if constexpr (is_q8(MODE)) {
+        p.k_scales = a.cache.k_scales;
+        p.v_scales = a.cache.v_scales;
+        for (p.block_log2 = 0; (1 << p.block_log2) < a.cache.block;) ++p.block_log2;
+        p.per_page_log2 = p.ps_log2 - p.block_log2;
+    }
     const long grid = plan_units(pl, a.B, Hkv) * pl.smax;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     return launch_pdl_cluster(tree_attn_kernel<D, MODE>, dim3((unsigned)grid), dim3(threads_of(MODE)),
-                              (size_t)Cfg<D>::SMEM, s,
+                              (size_t)smem_of<D, MODE>(), s,
                               pl.merge == kMergeCluster ? (unsigned)pl.smax : 1u, mq, mkc, mvc,
                               mkt, mvt, p);
 }
