@@ -139,9 +139,10 @@ bool page_map(CUtensorMap* m, const PagedArgs& c, const void* pages, int rows, b
     return make_map(m, pages, d, f16);
 }
 
-// Pages of an 8-bit cache: boxes of a head's whole rows, not swizzled.
+// Pages of an 8-bit cache: boxes of a head's whole rows, swizzled over the row's length or not
+// at all.
 template <int D>
-bool code_map(CUtensorMap* m, const Q8Args& c, const void* pages, int rows) {
+bool code_map(CUtensorMap* m, const Q8Args& c, const void* pages, int rows, bool swizzled = false) {
     auto fn = encode_fn();
     if (!fn) return false;
     auto stride = [](int64_t bytes, int size) { return size > 1 ? (cuuint64_t)bytes : (cuuint64_t)D; };
@@ -150,7 +151,8 @@ bool code_map(CUtensorMap* m, const Q8Args& c, const void* pages, int rows) {
                                    stride(c.page_stride, c.num_pages)};
     const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)std::min(c.page_size, rows), 1, 1}, estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pages), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -161,5 +163,8 @@ bool code_map(CUtensorMap* m, const Q8Args& c, const void* pages, int rows) {
 bool few_rows(int B, int N, int Hq, int Hkv, int64_t cache_cap);
 size_t few_rows_workspace_bytes(int N, int Hq, int Hkv, int D);
 cudaError_t launch_tree_attn_rows(const PagedAttnArgs& a, cudaStream_t s);
+// ... over an 8-bit cache (tree_attn_q8_rows.cu), in a workspace of the same size.
+bool q8_few_rows(int B, int N, int Hq, int Hkv, int64_t cache_cap);
+cudaError_t launch_tree_attn_q8_rows(const Q8AttnArgs& a, cudaStream_t s);
 
 }  // namespace ddt
