@@ -9,6 +9,8 @@
 // its codes are widened by a product with 2^(120 + e), which has to be a bf16 number.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -35,13 +37,46 @@ DDT_DEV uint32_t q8_pack2(float lo, float hi) {
     return r;
 }
 DDT_DEV uint32_t q8_pack4(float a, float b, float c, float d) {
-    return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
+    return __byte_perm(q8_pack2(a, b), q8_pack2(c, d), 0x5410);
 }
-// The value of one code (0x7F as 480).
-DDT_DEV float q8_value(uint32_t c) {
-    const uint32_t sign = (c & 0x80u) << 24, rest = (c & 0x7fu) << 20;
-    return __uint_as_float(sign | rest) * 0x1p120f;  // (exponent bias 127 - 7)
+// Four codes moved to a scale 2^-shift as large: rounded once more where they fall below
+// the normal codes.
+DDT_DEV uint32_t q8_moved(uint32_t w, float factor) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = w >> (8 * i);
+        v[i] = __uint_as_float((c & 0x80u) << 24 | (c & 0x7fu) << 20) * 0x1p120f * factor;
+    }
+    return q8_pack4(v[0], v[1], v[2], v[3]);
 }
+// Codes as elements of the tokens' type.  Each code's exponent and significand bits move to the
+// type's places and its sign bit to the top, which is a number 2^-8 (fp16) or 2^-120
+// (bf16) of the code's, subnormal codes included (and 0x7F as 480); one packed product with
+// the block's scale and that power gives the value, exactly.  (bf16's product takes and
+// gives subnormal numbers as they are.)
+//
+// What that product takes for a block's scale byte, as the type's bits.
+template <bool F16>
+DDT_DEV uint32_t widen_factor(uint32_t byte) {
+    const int e = q8_from_byte(byte, q8_least(F16));
+    return F16 ? (uint32_t)(23 + e) << 10 : (uint32_t)(247 + e) << 7;
+}
+// The codes at bytes 1 and 3 of a word (bytes 0 and 2 hold none or others) as a pair.
+template <bool F16>
+DDT_DEV uint32_t widen_odd(uint32_t t, uint32_t factors) {
+    uint32_t r = (F16 ? (t >> 1) & 0x3f803f80u : (t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+    if constexpr (F16) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(factors));
+    else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(factors));
+    return r;
+}
+template <bool F16>
+DDT_DEV uint32_t widen_even(uint32_t t, uint32_t factors) { return widen_odd<F16>(t << 8, factors); }
+// Codes 0, 1 and codes 2, 3 of a word as pairs in their order.
+template <bool F16>
+DDT_DEV uint32_t widen_lo(uint32_t t, uint32_t factors) { return widen_odd<F16>(__byte_perm(t, 0u, 0x1404), factors); }
+template <bool F16>
+DDT_DEV uint32_t widen_hi(uint32_t t, uint32_t factors) { return widen_odd<F16>(__byte_perm(t, 0u, 0x3424), factors); }
 
 // A run's tokens first[b] .. first[b + 1] - 1 become positions at[b] .. of sequence b.  Whether
 // it is one that no call may carry out: outside the T tokens or the table's positions.
@@ -57,20 +92,21 @@ struct RunBlock {
 // Runs cover their blocks by slots: sequence b has slots first[b] / S + 2 b and up, two more
 // than its tokens fill, as n tokens touch at most (n - 2) / S + 2 blocks.  The slots'
 // starts are known without adding up the runs before, so a CTA finds its own by halving.
-DDT_DEV RunBlock run_block(const int32_t* first, const int32_t* at, int B, int T, int S, int64_t cap,
+DDT_DEV RunBlock run_block(const int32_t* first, const int32_t* at, int B, int T, int block_log2, int64_t cap,
                            int64_t slot) {
+    const int S = 1 << block_log2;
     int lo = 0, hi = B - 1;  // the last sequence whose slots start at or before this one
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)(first[mid] / S) + 2 * (int64_t)mid <= slot) lo = mid;
+        if ((int64_t)(first[mid] >> block_log2) + 2 * (int64_t)mid <= slot) lo = mid;
         else hi = mid - 1;
     }
     RunBlock x{};
     x.b = lo;
     const int f = first[lo], n = first[lo + 1] - f, p = at[lo];
-    const int64_t j = slot - ((int64_t)(f / S) + 2 * (int64_t)lo);
+    const int64_t j = slot - ((int64_t)(f >> block_log2) + 2 * (int64_t)lo);
     if (j < 0 || n == 0 || run_bad(f, n, p, T, cap)) return x;
-    x.p0 = (int)min((int64_t)(p / S * S) + j * S, (int64_t)INT32_MAX - S);
+    x.p0 = (int)min((int64_t)(p & -S) + j * S, (int64_t)INT32_MAX - S);
     x.lo = max(x.p0, p);
     x.hi = min(x.p0 + S, p + n);
     x.ok = x.lo < x.hi;

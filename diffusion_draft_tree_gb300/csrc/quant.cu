@@ -1,9 +1,15 @@
 // quant.cu -- the 8-bit cache's writers (ddtree_append_q8, ddtree_commit_q8) and its
 // reader (ddtree_read_q8); q8.cuh has the format.
 //
-// Writers.  A CTA takes one block of the cache that a run touches, for one head of the
-// keys or values (or of the queries, which only pass through): its rows in 32 bits in
-// shared memory, normed and turned, their largest element, the exponent, the codes.
+// Writers.  HBM-bound: rows are read once and stay in registers from their load to their
+// codes.  A CTA takes one block of the cache that a run touches (run_block) and some of the
+// heads of its tokens: queries, keys, values.  It fills the block's positions' cosine and
+// sine table in shared memory once for all of them; a head's rows are then loaded, normed
+// and turned in 32 bits -- D / 16 lanes a row, two vectors of 8 elements a lane, as in
+// norm_rope.cu -- their largest element found, and rounded to codes under its power of
+// two.  A head is one warp's where its rows fit four passes of a warp (a decoding step's
+// single row, 16 rows of D = 128), so that warps go on without each other, and the
+// CTA's otherwise, which then meets once a head.
 #include "q8.cuh"
 #include "rotary.cuh"
 
@@ -11,169 +17,343 @@ namespace ddt {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxBlock = DDTREE_MAX_Q8_BLOCK, kMaxD = 128;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kPasses = 4;  // rows of a lane, at most
+constexpr int kFill = 16;   // CTAs per SM that fill the GPU
 
 struct WriteParams {
     RowsArg q, q_out, k, v;
     Q8Args cache;
-    const int32_t *first, *at;                              // append
+    const int32_t *first, *at;                                // append
     const int32_t *accept_len, *accepted_nodes, *prefix_len;  // commit
     int32_t* new_len;
     const uint64_t* turns;
     NormArgs norm;
     float scale;
-    int T, B, rot, L, N, slots;
-    bool interleaved;
+    int T, B, rot, L, N;
+    int slots;  // commit: blocks that a path may touch
+    int heads, chunk;  // of a token: queries, keys and values; ... that a CTA takes
+    int page_log2, block_log2;
     uint32_t* err;
 };
 
-template <typename T, bool COMMIT>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteParams p) {
-    __shared__ float s_x[kMaxBlock][kMaxD];
-    __shared__ float s_max[kThreads / 32];
+// PAIRED: pairs (2j, 2j + 1), else (j, j + rot/2).
+template <typename T, int D, bool PAIRED, bool COMMIT>
+__global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constant__ WriteParams p) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes a row, rows of a warp's pass
+    using Vt = Vec<T, 8>;
+    // cos and sin of row r's pair 8 u + e, at [r][e / 4][u][e % 4]
+    extern __shared__ __align__(16) float s_cos[];
+    __shared__ float s_max[2][kWarps];
     __shared__ int s_node[DDTREE_MAX_L + 1];
     __shared__ int s_bad;
     const Q8Args& c = p.cache;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = c.block, D = c.D;
-    const int64_t cap = (int64_t)c.max_pages * c.page_size;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = c.block;
+    const int64_t cap = (int64_t)c.max_pages << p.page_log2;
     pdl_wait();
-    RunBlock x;
+    RunBlock x{};
     if constexpr (COMMIT) {
+        // Every CTA of a sequence checks its whole path and its pages, so that all reach
+        // the same verdict.
         x.b = blockIdx.x / p.slots;
-        const int j = blockIdx.x % p.slots;
+        const int j = blockIdx.x - x.b * p.slots;
         const int P = p.prefix_len[x.b], a = p.accept_len[x.b];
-        if (tid == 0) s_bad = 0;
-        __syncthreads();
-        if (a < 0 || a > p.L || P < 0 || (int64_t)P + a + 1 > cap) {
-            if (tid == 0) s_bad = ERR_BAD_PREFIX_LEN;
-        } else if (tid <= a) {
-            const int node = tid ? p.accepted_nodes[(int64_t)x.b * p.L + tid - 1] : 0;
-            const int page = c.table[x.b * c.table_stride + (P + tid) / c.page_size];
-            s_node[tid] = node;
-            if (tid && (node < 1 || node > p.N)) atomicMax(&s_bad, (int)ERR_BAD_TREE);
-            else if (page < 0 || page >= c.num_pages) atomicMax(&s_bad, (int)ERR_BAD_PAGE);
+        if (tid < 32) {
+            uint32_t bad = 0;
+            if (a < 0 || a > p.L || P < 0 || (int64_t)P + a + 1 > cap) {
+                bad = ERR_BAD_PREFIX_LEN;
+            } else if (tid <= a) {
+                const int node = tid ? p.accepted_nodes[(int64_t)x.b * p.L + tid - 1] : 0;
+                const int page = c.table[x.b * c.table_stride + ((P + tid) >> p.page_log2)];
+                s_node[tid] = node;
+                if (tid && (node < 1 || node > p.N)) bad = ERR_BAD_TREE;
+                else if (page < 0 || page >= c.num_pages) bad = ERR_BAD_PAGE;
+            }
+            bad = __reduce_max_sync(0xffffffffu, bad);
+            if (tid == 0) {
+                s_bad = (int)bad;
+                if (j == 0 && blockIdx.y == 0) {
+                    if (bad) record_error(p.err, ERR_COMMIT | bad);
+                    if (p.new_len) p.new_len[x.b] = bad ? P : P + a + 1;
+                }
+            }
         }
         __syncthreads();
-        if (j == 0 && blockIdx.y == 0 && tid == 0) {
-            if (s_bad) record_error(p.err, ERR_COMMIT | (uint32_t)s_bad);
-            if (p.new_len) p.new_len[x.b] = s_bad ? P : P + a + 1;
-        }
         if (s_bad) return;
-        x.p0 = P / S * S + j * S;
+        x.p0 = (P & -S) + j * S;
         x.lo = max(x.p0, P);
         x.hi = min(x.p0 + S, P + a + 1);
         x.token = x.lo - P;  // (of the path)
         if (x.lo >= x.hi) return;
     } else {
-        x = run_block(p.first, p.at, p.B, p.T, S, cap, blockIdx.x);
+        x = run_block(p.first, p.at, p.B, p.T, p.block_log2, cap, blockIdx.x);
         if (tid == 0 && blockIdx.y == 0)
             check_run(p.first, p.at, p.B, p.T, cap, blockIdx.x, p.err, ERR_APPEND | ERR_BAD_INPUT);
         if (!x.ok) return;
     }
-    const int h = blockIdx.y, hk = h - p.q.heads, hv = hk - c.Hkv;
-    const bool is_q = hk < 0, is_v = hv >= 0;
-    const int head = is_q ? h : (is_v ? hv : hk);
-    const RowsArg& in = is_q ? p.q : (is_v ? p.v : p.k);
-    const int page = c.table[x.b * c.table_stride + x.p0 / c.page_size];
+    const int page = c.table[x.b * c.table_stride + (x.p0 >> p.page_log2)];
     const bool there = page >= 0 && page < c.num_pages;
-    if (!there && !is_q) {
-        if (tid == 0) record_error(p.err, ERR_APPEND | ERR_BAD_PAGE);
-        return;
+    const int rows = x.hi - x.lo, slot0 = x.p0 & (c.page_size - 1), least = q8_least(c.dtype == 2);
+    const int h_first = blockIdx.y * p.chunk;
+    int h_last = min(p.heads, h_first + p.chunk);
+    if (!there) {
+        if (tid == 0 && h_last > p.q.heads) record_error(p.err, ERR_APPEND | ERR_BAD_PAGE);
+        h_last = min(h_last, p.q.heads);  // (queries go on)
     }
-    const int rows = x.hi - x.lo;
-    const bool norm = !is_v && p.norm.on;
-    const float* w = is_q ? p.norm.q_weight : p.norm.k_weight;
-    float most = 0.f;
-    for (int r = warp; r < rows; r += kThreads / 32) {
-        const int64_t token = COMMIT ? (int64_t)x.b * (p.N + 1) + s_node[x.token + r] : x.token + r;
-        const T* row = (const T*)in.data + token * in.ts + head * in.hs;
-        float* y = s_x[r];
-        float sum = 0.f;
-        for (int i = lane; i < D; i += 32) {
-            y[i] = to_f(row[i]);
-            sum = fmaf(y[i], y[i], sum);
+
+    // ---- the block's table, if a head here is turned ---------------------------
+    const int pairs = p.rot / 2, ru = p.rot / 16;
+    float* s_sin = s_cos + S * pairs;
+    if (!COMMIT && pairs && h_first < p.q.heads + c.Hkv) {
+        for (int j = tid; j < rows * pairs; j += kThreads) {
+            const int r = j / pairs, f = j - r * pairs;
+            const float2 cs = cos_sin((uint64_t)(uint32_t)(x.lo + r) * p.turns[f]);
+            const int at = r * pairs + (((f & 7) >> 2) * ru + (f >> 3)) * 4 + (f & 3);
+            s_cos[at] = cs.x * p.scale;
+            s_sin[at] = cs.y * p.scale;
         }
+        __syncthreads();
+    }
+
+    // ---- the heads ----------------------------------------------------------------
+    const int l = lane & (LPR - 1), u = l;  // the lane's two vectors of a row
+    const bool in_rot = u < ru;
+    const int e0 = in_rot ? (PAIRED ? 16 * u : 8 * u) : p.rot + 16 * (u - ru);
+    const int e1 = in_rot && !PAIRED ? e0 + pairs : e0 + 8;
+    const bool whole = rows > kPasses * RPW;  // a head is the CTA's
+    const int r_first = (whole ? warp * RPW : 0) + lane / LPR, r_step = whole ? kWarps * RPW : RPW;
+    int turn = 0;
+    for (int h = h_first + (whole ? 0 : warp); h < h_last; h += whole ? 1 : kWarps) {
+        const int hk = h - p.q.heads, hv = hk - c.Hkv;
+        const bool is_q = hk < 0, is_v = hv >= 0;
+        const int head = is_q ? h : (is_v ? hv : hk);
+        const RowsArg& in = is_q ? p.q : (is_v ? p.v : p.k);
+        Vt ra[kPasses], rb[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = r_first + i * r_step;
+            if (r < rows) {
+                const int64_t token = COMMIT ? (int64_t)x.b * (p.N + 1) + s_node[x.token + r] : x.token + r;
+                const T* row = (const T*)in.data + token * in.ts + head * in.hs;
+                ra[i] = *(const Vt*)(row + e0);
+                rb[i] = *(const Vt*)(row + e1);
+            }
+        }
+        uint8_t *scale = nullptr, *codes = nullptr;
+        int old = least;
+        if (!is_q) {
+            scale = (is_v ? c.v_scales : c.k_scales) +
+                    ((((int64_t)page * c.Hkv + head) << (p.page_log2 - p.block_log2)) + (slot0 >> p.block_log2));
+            codes = (is_v ? c.v : c.k) + page * c.page_stride + head * c.head_stride + slot0 * c.slot_stride;
+            if (x.lo > x.p0) old = q8_from_byte(*scale, least);
+        }
+        float y[kPasses][2][8], most = 0.f;  // the elements at e0 and at e1
+        const bool norm = !COMMIT && !is_v && p.norm.on, turned_head = !COMMIT && !is_v && in_rot;
+        float w[2][8];
         if (norm) {
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float f = rsqrtf(sum / D + p.norm.eps);
-            for (int i = lane; i < D; i += 32) y[i] = y[i] * f * (w ? w[i] : 1.f);
-        }
-        __syncwarp();
-        if (!is_v)
-            for (int j = lane; j < p.rot / 2; j += 32) {
-                const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + p.rot / 2;
-                const float2 cs = cos_sin((uint64_t)(uint32_t)(x.lo + r) * p.turns[j]);
-                const float2 z = turned(y[a], y[b], cs.x * p.scale, cs.y * p.scale);
-                y[a] = z.x;
-                y[b] = z.y;
+            const float* from = is_q ? p.norm.q_weight : p.norm.k_weight;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[0][e] = from ? __ldg(&from[e0 + e]) : 1.f;
+                w[1][e] = from ? __ldg(&from[e1 + e]) : 1.f;
             }
-        __syncwarp();
-        for (int i = lane; i < D; i += 32) {
-            most = fmaxf(most, fabsf(y[i]));
-            if (is_q) ((T*)p.q_out.data + token * p.q_out.ts + head * p.q_out.hs)[i] = from_f<T>(y[i]);
         }
-    }
-    if (is_q) return;
-    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    if (lane == 0) s_max[warp] = most;
-    __syncthreads();
-    most = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    const int slot0 = x.p0 % c.page_size, least = q8_least(c.dtype == 2);
-    uint8_t* scale = (is_v ? c.v_scales : c.k_scales) +
-                     ((int64_t)page * c.Hkv + head) * (c.page_size / S) + slot0 / S;
-    uint8_t* codes = (is_v ? c.v : c.k) + page * c.page_stride + head * c.head_stride;
-    int e = q8_exponent(most, least);
-    if (x.lo > x.p0) {
-        const int old = q8_from_byte(*scale, least);
-        e = max(e, old);
-        if (e > old)
-            for (int i = tid; i < (x.lo - x.p0) * D; i += kThreads) {
-                uint8_t* at = codes + (slot0 + i / D) * c.slot_stride + i % D;
-                *at = (uint8_t)q8_pack2(q8_value(*at) * pow2(old - e), 0.f);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = r_first + i * r_step;
+            if (whole || i * RPW < rows) {  // (the warp as a whole)
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 a = unpack2<T>(reinterpret_cast<const uint32_t*>(ra[i].e)[e]);
+                    const float2 b = unpack2<T>(reinterpret_cast<const uint32_t*>(rb[i].e)[e]);
+                    y[i][0][2 * e] = a.x, y[i][0][2 * e + 1] = a.y;
+                    y[i][1][2 * e] = b.x, y[i][1][2 * e + 1] = b.y;
+                }
+                if (norm) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum = fmaf(y[i][e >> 3][e & 7], y[i][e >> 3][e & 7], sum);
+#pragma unroll
+                    for (int d = LPR / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    const float f = rsqrtf(fmaf(sum, 1.f / D, p.norm.eps));
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[i][e >> 3][e & 7] *= f * w[e >> 3][e & 7];
+                }
+                if (turned_head && r < rows) {
+                    const float* tc = s_cos + r * pairs + u * 4;
+                    const float* ts = s_sin + r * pairs + u * 4;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const float4 cc = *(const float4*)&tc[g * ru * 4], ss = *(const float4*)&ts[g * ru * 4];
+                        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float& a = PAIRED ? y[i][g][2 * e] : y[i][0][4 * g + e];
+                            float& b = PAIRED ? y[i][g][2 * e + 1] : y[i][1][4 * g + e];
+                            const float2 z = turned(a, b, cv[e], sv[e]);
+                            a = z.x, b = z.y;
+                        }
+                    }
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(y[i][e >> 3][e & 7]));
+                }
             }
+        }
+        if (is_q) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = r_first + i * r_step;
+                if (r < rows) {
+                    T* row = (T*)p.q_out.data + (int64_t)(x.token + r) * p.q_out.ts + head * p.q_out.hs;
+                    Vt a, b;
+                    pack_vec<T, 8>(y[i][0], a);
+                    pack_vec<T, 8>(y[i][1], b);
+                    *(Vt*)(row + e0) = a;
+                    *(Vt*)(row + e1) = b;
+                }
+            }
+            continue;
+        }
+        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (not negative)
+        if (whole) {
+            if (lane == 0) s_max[turn][warp] = most;
+            __syncthreads();  // (and every thread has read the old scale)
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_max[turn][i]);
+            turn ^= 1;
+        } else {
+            __syncwarp();
+        }
+        const int e = max(q8_exponent(most, least), old);
+        if (x.lo > x.p0 && e > old) {  // the block's earlier codes move to its new scale
+            const float f = pow2(old - e);
+            const int n = (x.lo - x.p0) * LPR, step = whole ? kThreads : 32;
+            for (int i = whole ? tid : lane; i < n; i += step) {
+                uint4* to = (uint4*)(codes + (i / LPR) * c.slot_stride + (i & (LPR - 1)) * 16);
+                const uint4 v = *to;
+                *to = make_uint4(q8_moved(v.x, f), q8_moved(v.y, f), q8_moved(v.z, f), q8_moved(v.w, f));
+            }
+        }
+        const float f = pow2(-e);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = r_first + i * r_step;
+            if (r < rows) {
+                uint8_t* row = codes + (x.lo - x.p0 + r) * c.slot_stride;
+                uint32_t g[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    g[k] = q8_pack4(y[i][k >> 1][4 * (k & 1)] * f, y[i][k >> 1][4 * (k & 1) + 1] * f,
+                                    y[i][k >> 1][4 * (k & 1) + 2] * f, y[i][k >> 1][4 * (k & 1) + 3] * f);
+                if constexpr (PAIRED) {
+                    *(uint4*)(row + e0) = make_uint4(g[0], g[1], g[2], g[3]);
+                } else {
+                    *(uint2*)(row + e0) = make_uint2(g[0], g[1]);
+                    *(uint2*)(row + e1) = make_uint2(g[2], g[3]);
+                }
+            }
+        }
+        if ((whole ? tid : lane) == 0) *scale = (uint8_t)(e + 127);
     }
-    const float f = pow2(-e);
-    for (int i = tid; i < rows * D; i += kThreads)
-        codes[(slot0 + x.lo - x.p0 + i / D) * c.slot_stride + i % D] = (uint8_t)q8_pack2(s_x[i / D][i % D] * f, 0.f);
-    __syncthreads();  // (every thread has read the old scale)
-    if (tid == 0) *scale = (uint8_t)(e + 127);
+    pdl_trigger();
 }
 
 struct ReadParams {
     Q8Args cache;
     const int32_t *first, *at;
     RowsArg k_out, v_out;
-    int B, T;
+    int B, T, chunk;
+    int page_log2, block_log2;
     uint32_t* err;
 };
 
-template <typename T>
+// Reader.  HBM-bound: a CTA takes one block of the cache that a run touches, for some of its
+// (half, head)s; a thread takes 16 codes at a time, several in flight, and stores the 16
+// elements that they are.
+constexpr int kInFlight = 4;
+
+template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
+    constexpr int CH = D / 16;  // 16-byte chunks of a row of codes
     const Q8Args& c = p.cache;
-    const int S = c.block, D = c.D, head = blockIdx.y, half = blockIdx.z;
+    const int64_t cap = (int64_t)c.max_pages << p.page_log2;
     pdl_wait();
-    const int64_t cap = (int64_t)c.max_pages * c.page_size;
-    const RunBlock x = run_block(p.first, p.at, p.B, p.T, S, cap, blockIdx.x);
-    if (threadIdx.x == 0 && head == 0 && half == 0)
+    const RunBlock x = run_block(p.first, p.at, p.B, p.T, p.block_log2, cap, blockIdx.x);
+    if (threadIdx.x == 0 && blockIdx.y == 0)
         check_run(p.first, p.at, p.B, p.T, cap, blockIdx.x, p.err, ERR_READ | ERR_BAD_INPUT);
     if (!x.ok) return;
-    const int page = c.table[x.b * c.table_stride + x.p0 / c.page_size];
+    const int page = c.table[x.b * c.table_stride + (x.p0 >> p.page_log2)];
     if (page < 0 || page >= c.num_pages) {
         if (threadIdx.x == 0) record_error(p.err, ERR_READ | ERR_BAD_PAGE);
         return;
     }
-    const int slot0 = x.p0 % c.page_size;
-    const uint8_t* scales = half ? c.v_scales : c.k_scales;
-    const float f = pow2(q8_from_byte(scales[((int64_t)page * c.Hkv + head) * (c.page_size / S) + slot0 / S],
-                                      q8_least(c.dtype == 2)));
-    const uint8_t* codes = (half ? c.v : c.k) + page * c.page_stride + head * c.head_stride;
-    const RowsArg& out = half ? p.v_out : p.k_out;
-    for (int i = threadIdx.x; i < (x.hi - x.lo) * D; i += kThreads) {
-        const int r = i / D, d = i % D;
-        const float y = q8_value(codes[(slot0 + x.lo - x.p0 + r) * c.slot_stride + d]) * f;
-        ((T*)out.data + (int64_t)(x.token + r) * out.ts + head * out.hs)[d] = from_f<T>(y);
+    const int slot0 = x.p0 & (c.page_size - 1), r_lo = x.lo - x.p0, r_hi = x.hi - x.p0;
+    const int t_first = blockIdx.y * p.chunk, t_last = min(2 * c.Hkv, t_first + p.chunk);
+    // items: (half, head), slot of the block, chunk of the row
+    const int items = ((t_last - t_first) << p.block_log2) * CH;
+    for (int i0 = threadIdx.x; i0 < items; i0 += kInFlight * kThreads) {
+        uint4 w[kInFlight];
+        uint32_t f[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int i = i0 + k * kThreads, r = i / CH & (c.block - 1), t = t_first + ((i / CH) >> p.block_log2);
+            if (i < items && r >= r_lo && r < r_hi) {
+                const bool is_v = t >= c.Hkv;
+                const int head = is_v ? t - c.Hkv : t;
+                const uint8_t* row = (is_v ? c.v : c.k) + page * c.page_stride + head * c.head_stride +
+                                     (slot0 + r) * c.slot_stride;
+                w[k] = ld_stream_v4(row + (i & (CH - 1)) * 16);
+                f[k] = __ldg((is_v ? c.v_scales : c.k_scales) +
+                             ((((int64_t)page * c.Hkv + head) << (p.page_log2 - p.block_log2)) + (slot0 >> p.block_log2)));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int i = i0 + k * kThreads, r = i / CH & (c.block - 1), t = t_first + ((i / CH) >> p.block_log2);
+            if (i < items && r >= r_lo && r < r_hi) {
+                const bool is_v = t >= c.Hkv;
+                const RowsArg& out = is_v ? p.v_out : p.k_out;
+                uint16_t* row = (uint16_t*)out.data + (int64_t)(x.token + r - r_lo) * out.ts +
+                                (is_v ? t - c.Hkv : t) * out.hs + (i & (CH - 1)) * 16;
+                const uint32_t m = widen_factor<F16>(f[k]) * 0x10001u;
+                *(uint4*)row = make_uint4(widen_lo<F16>(w[k].x, m), widen_hi<F16>(w[k].x, m),
+                                          widen_lo<F16>(w[k].y, m), widen_hi<F16>(w[k].y, m));
+                *(uint4*)(row + 8) = make_uint4(widen_lo<F16>(w[k].z, m), widen_hi<F16>(w[k].z, m),
+                                                widen_lo<F16>(w[k].w, m), widen_hi<F16>(w[k].w, m));
+            }
+        }
     }
+    pdl_trigger();
+}
+
+int log2_of(int x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+// Heads of a CTA: as many as leave kFill CTAs an SM, at least `least` of them.
+int heads_of(int heads, int64_t slots, int least) {
+    const int64_t fill = (int64_t)num_sms() * kFill, cuts = std::max<int64_t>(1, (fill + slots - 1) / slots);
+    return (int)std::max<int64_t>(std::min(least, heads), (heads + cuts - 1) / cuts);
+}
+
+template <typename T, int D, bool PAIRED, bool COMMIT>
+cudaError_t launch_write(WriteParams& p, int64_t blocks, cudaStream_t s) {
+    p.page_log2 = log2_of(p.cache.page_size);
+    p.block_log2 = log2_of(p.cache.block);
+    p.heads = p.q.heads + 2 * p.cache.Hkv;
+    p.chunk = heads_of(p.heads, blocks, kWarps);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)((p.heads + p.chunk - 1) / p.chunk));
+    return launch_pdl(write_kernel<T, D, PAIRED, COMMIT>, grid, dim3(kThreads),
+                      (size_t)p.cache.block * p.rot * sizeof(float), s, p);
+}
+template <typename T, int D>
+cudaError_t launch_append(WriteParams& p, int64_t blocks, bool paired, cudaStream_t s) {
+    return paired ? launch_write<T, D, true, false>(p, blocks, s) : launch_write<T, D, false, false>(p, blocks, s);
 }
 
 }  // namespace
@@ -182,12 +362,14 @@ cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t s) {
     WriteParams p{};
     p.q = a.q, p.q_out = a.q_out, p.k = a.k, p.v = a.v, p.cache = a.cache;
     p.first = a.first, p.at = a.at, p.turns = a.turns, p.norm = a.norm, p.scale = a.scale;
-    p.T = a.T, p.B = a.B, p.rot = a.rot, p.interleaved = a.interleaved, p.err = a.err;
-    const int64_t slots = run_slots(a.B, a.T, a.cache.block);
-    if (slots > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)slots, (unsigned)(a.q.heads + 2 * a.cache.Hkv));
-    return a.cache.dtype == 2 ? launch_pdl(write_kernel<__half, false>, grid, dim3(kThreads), 0, s, p)
-                              : launch_pdl(write_kernel<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, p);
+    p.T = a.T, p.B = a.B, p.rot = a.rot, p.err = a.err;
+    const int64_t blocks = run_slots(a.B, a.T, a.cache.block);
+    const bool f16 = a.cache.dtype == 2;
+    if (a.cache.D == 128)
+        return f16 ? launch_append<__half, 128>(p, blocks, a.interleaved, s)
+                   : launch_append<__nv_bfloat16, 128>(p, blocks, a.interleaved, s);
+    return f16 ? launch_append<__half, 64>(p, blocks, a.interleaved, s)
+               : launch_append<__nv_bfloat16, 64>(p, blocks, a.interleaved, s);
 }
 
 cudaError_t launch_commit_q8(const CommitQ8Args& a, cudaStream_t s) {
@@ -195,19 +377,34 @@ cudaError_t launch_commit_q8(const CommitQ8Args& a, cudaStream_t s) {
     p.k = a.k_tree, p.v = a.v_tree, p.cache = a.cache;
     p.accept_len = a.accept_len, p.accepted_nodes = a.accepted_nodes, p.prefix_len = a.prefix_len;
     p.new_len = a.new_len, p.B = a.B, p.L = a.L, p.N = a.N, p.err = a.err;
-    p.slots = (a.L + 1 - 2 + a.cache.block) / a.cache.block + 1;  // blocks that L + 1 positions touch
-    const dim3 grid((unsigned)(a.B * p.slots), (unsigned)(2 * a.cache.Hkv));
-    return a.cache.dtype == 2 ? launch_pdl(write_kernel<__half, true>, grid, dim3(kThreads), 0, s, p)
-                              : launch_pdl(write_kernel<__nv_bfloat16, true>, grid, dim3(kThreads), 0, s, p);
+    p.slots = (a.L - 1 + a.cache.block) / a.cache.block + 1;  // blocks that L + 1 positions touch
+    const int64_t blocks = (int64_t)a.B * p.slots;
+    const bool f16 = a.cache.dtype == 2;
+    if (a.cache.D == 128)
+        return f16 ? launch_write<__half, 128, true, true>(p, blocks, s)
+                   : launch_write<__nv_bfloat16, 128, true, true>(p, blocks, s);
+    return f16 ? launch_write<__half, 64, true, true>(p, blocks, s)
+               : launch_write<__nv_bfloat16, 64, true, true>(p, blocks, s);
 }
 
 cudaError_t launch_read_q8(const ReadQ8Args& a, cudaStream_t s) {
-    ReadParams p{a.cache, a.first, a.at, a.k_out, a.v_out, a.B, a.T, a.err};
-    const int64_t slots = run_slots(a.B, a.T, a.cache.block);
-    if (slots > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)slots, (unsigned)a.cache.Hkv, 2);
-    return a.cache.dtype == 2 ? launch_pdl(read_kernel<__half>, grid, dim3(kThreads), 0, s, p)
-                              : launch_pdl(read_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, p);
+    ReadParams p{};
+    p.cache = a.cache, p.first = a.first, p.at = a.at, p.k_out = a.k_out, p.v_out = a.v_out;
+    p.B = a.B, p.T = a.T, p.err = a.err;
+    p.page_log2 = log2_of(a.cache.page_size);
+    p.block_log2 = log2_of(a.cache.block);
+    const int64_t blocks = run_slots(a.B, a.T, a.cache.block);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    // (at least one round of a CTA's threads)
+    const int tasks = 2 * a.cache.Hkv, one = a.cache.block * a.cache.D / 16;
+    p.chunk = heads_of(tasks, blocks, std::max(1, kThreads / one));
+    const dim3 grid((unsigned)blocks, (unsigned)((tasks + p.chunk - 1) / p.chunk));
+    const bool f16 = a.cache.dtype == 2;
+    if (a.cache.D == 128)
+        return f16 ? launch_pdl(read_kernel<true, 128>, grid, dim3(kThreads), 0, s, p)
+                   : launch_pdl(read_kernel<false, 128>, grid, dim3(kThreads), 0, s, p);
+    return f16 ? launch_pdl(read_kernel<true, 64>, grid, dim3(kThreads), 0, s, p)
+               : launch_pdl(read_kernel<false, 64>, grid, dim3(kThreads), 0, s, p);
 }
 
 }  // namespace ddt

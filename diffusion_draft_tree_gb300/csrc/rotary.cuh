@@ -37,6 +37,19 @@ struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 
+// Elements in 32 bits into a vector, rounded once.
+template <typename T, int V>
+DDT_DEV void pack_vec(const float (&y)[V], Vec<T, V>& v) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(v.e);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v.e[e] = from_f<T>(y[e]);
+    }
+}
+
 // Turns the V pairs of two vectors: pairs (a.e[i], b.e[i]), or PAIRED neighbours,
 // a's before b's.  In 32 bits, one rounding each.
 DDT_DEV float2 turned(float a, float b, float c, float s) {

@@ -575,25 +575,6 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
 // turn codes into the tokens' type between the copy and the tensor core: the kernel's
 // other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
-//
-// A pair of codes becomes a pair of elements by moving each code's exponent and
-// significand bits to the type's places and its sign bit to the top -- a number 2^-8
-// (fp16) or 2^-120 (bf16) of the code's, subnormal codes included -- and one packed
-// product with the block's scale and that power: 5 instructions a pair.
-template <bool F16>
-DDT_DEV uint32_t widen2(uint32_t codes, uint32_t sel, uint32_t mult) {
-    const uint32_t t = __byte_perm(codes, 0u, sel);  // the two codes at bytes 1 and 3
-    uint32_t r = (F16 ? (t >> 1) & 0x3f803f80u : (t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
-    if constexpr (F16) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
-    else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
-    return r;
-}
-// That power of two for a scale byte, as the type's bits.
-template <bool F16>
-DDT_DEV uint32_t widen_factor(uint32_t byte) {
-    const int e = q8_from_byte(byte, q8_least(F16));
-    return F16 ? (uint32_t)(23 + e) << 10 : (uint32_t)(247 + e) << 7;
-}
 // Widens a tile of codes [128 keys][D] into [D / 64] swizzled slabs, keys by `mult` (two
 // equal halves a word); thread i of 32 kWideners.  The threads of a second slab store
 // their halves the other way round: 8 lanes then store to 8 different 16-byte banks.
@@ -618,10 +599,10 @@ DDT_DEV void widen_tile(const uint8_t* raw, const uint16_t* mult, uint8_t* tile,
         for (int p = 0; p < BATCH; ++p) {
             const int r = r0 + (p0 + p) * STEP;
             uint4 y[2];
-            y[0] = make_uint4(widen2<F16>(w[p].x, 0x1404u, m[p]), widen2<F16>(w[p].x, 0x3424u, m[p]),
-                              widen2<F16>(w[p].y, 0x1404u, m[p]), widen2<F16>(w[p].y, 0x3424u, m[p]));
-            y[1] = make_uint4(widen2<F16>(w[p].z, 0x1404u, m[p]), widen2<F16>(w[p].z, 0x3424u, m[p]),
-                              widen2<F16>(w[p].w, 0x1404u, m[p]), widen2<F16>(w[p].w, 0x3424u, m[p]));
+            y[0] = make_uint4(widen_lo<F16>(w[p].x, m[p]), widen_hi<F16>(w[p].x, m[p]),
+                              widen_lo<F16>(w[p].y, m[p]), widen_hi<F16>(w[p].y, m[p]));
+            y[1] = make_uint4(widen_lo<F16>(w[p].z, m[p]), widen_hi<F16>(w[p].z, m[p]),
+                              widen_lo<F16>(w[p].w, m[p]), widen_hi<F16>(w[p].w, m[p]));
             uint8_t* to = tile + slab * kHalfBytes;
             const int first = (c & 3) * 2;
             *(uint4*)(to + swz(r, first + flip)) = flip ? y[1] : y[0];

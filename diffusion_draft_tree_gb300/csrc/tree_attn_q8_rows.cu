@@ -38,22 +38,6 @@ struct ParamsQ : ParamsR {
     int block_log2, per_page_log2;  // log2 of positions a scale, of scales a page and head
 };
 
-// Four codes of a word as two pairs of the type: bytes 0 and 2, bytes 1 and 3.
-template <bool F16>
-DDT_DEV uint32_t widen_odd(uint32_t t, uint32_t mult) {
-    uint32_t r = (F16 ? (t >> 1) & 0x3f803f80u : (t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
-    if constexpr (F16) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
-    else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(mult));
-    return r;
-}
-template <bool F16>
-DDT_DEV uint32_t widen_even(uint32_t t, uint32_t mult) { return widen_odd<F16>(t << 8, mult); }
-// What takes the bits of such a pair to the values of a block's scale byte.
-template <bool F16>
-DDT_DEV uint32_t factor_of(uint32_t byte) {
-    const int e = q8_from_byte(byte, q8_least(F16));
-    return F16 ? (uint32_t)(23 + e) << 10 : (uint32_t)(247 + e) << 7;
-}
 // 16-byte chunk c of row r of a tile of codes, swizzled by its row's length.
 template <int D>
 DDT_DEV uint32_t swz8(int r, int c) {
@@ -197,7 +181,7 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
                                        w3 = __shfl_sync(0xffffffffu, y.w, src);
                         word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
                     }
-                    const uint32_t m = factor_of<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
+                    const uint32_t m = widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
                     *(uint2*)&s_mult[s][v][4 * lane] = make_uint2(m, m);
                 }
             }
