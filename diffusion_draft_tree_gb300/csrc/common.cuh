@@ -165,6 +165,20 @@ DDT_DEV float2 fadd2(float2 a, float2 b) {
     return r;
 }
 
+// ... on two neighbours of an array: x *= s, and x += a * b.
+DDT_DEV void mul2(float& x0, float& x1, float s0, float s1) {
+    asm("{\n\t.reg .b64 X, S;\n\tmov.b64 X, {%0, %1};\n\tmov.b64 S, {%2, %3};\n\t"
+        "mul.rn.f32x2 X, X, S;\n\tmov.b64 {%0, %1}, X;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(s0), "f"(s1));
+}
+DDT_DEV void fma2(float& x0, float& x1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 X, A, B;\n\tmov.b64 X, {%0, %1};\n\tmov.b64 A, {%2, %3};\n\tmov.b64 B, {%4, %5};\n\t"
+        "fma.rn.f32x2 X, A, B, X;\n\tmov.b64 {%0, %1}, X;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // K-th largest (with multiplicity) of one uint32 per lane, K in [1, 32];
 // warp-collective.  Small K: remove the maximum K-1 times (one reduction, one
 // ballot each); larger K: a bitonic sort.

@@ -7,9 +7,12 @@
 // sine table in shared memory once for all of them; a head's rows are then loaded, normed
 // and turned in 32 bits -- D / 16 lanes a row, two vectors of 8 elements a lane, as in
 // norm_rope.cu -- their largest element found, and rounded to codes under its power of
-// two.  A head is one warp's where its rows fit four passes of a warp (a decoding step's
-// single row, 16 rows of D = 128), so that warps go on without each other, and the
-// CTA's otherwise, which then meets once a head.
+// two, the next head's loads in flight meanwhile.  A head is one warp's where its rows fit
+// the passes that a whole block takes the CTA (a decoding step's single row always does),
+// so that warps go on without each other, and the CTA's otherwise, which then meets
+// once a head.
+#include <type_traits>
+
 #include "q8.cuh"
 #include "rotary.cuh"
 
@@ -17,8 +20,7 @@ namespace ddt {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kPasses = 4;  // rows of a lane, at most
+constexpr int kThreads = 128;  // of the reader; the writers' CTAs have as many or twice
 constexpr int kFill = 16;   // CTAs per SM that fill the GPU
 
 struct WriteParams {
@@ -37,9 +39,10 @@ struct WriteParams {
     uint32_t* err;
 };
 
-// PAIRED: pairs (2j, 2j + 1), else (j, j + rot/2).
-template <typename T, int D, bool PAIRED, bool COMMIT>
-__global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constant__ WriteParams p) {
+// PAIRED: pairs (2j, 2j + 1), else (j, j + rot/2).  kPasses: rows of a lane where a whole
+// block is the CTA's, of kWarps warps.
+template <typename T, int D, int kWarps, int kPasses, bool PAIRED, bool COMMIT>
+__global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps) write_kernel(const __grid_constant__ WriteParams p) {
     constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes a row, rows of a warp's pass
     using Vt = Vec<T, 8>;
     // cos and sin of row r's pair 8 u + e, at [r][e / 4][u][e % 4]
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constan
     const int pairs = p.rot / 2, ru = p.rot / 16;
     float* s_sin = s_cos + S * pairs;
     if (!COMMIT && pairs && h_first < p.q.heads + c.Hkv) {
-        for (int j = tid; j < rows * pairs; j += kThreads) {
+        for (int j = tid; j < rows * pairs; j += (32 * kWarps)) {
             const int r = j / pairs, f = j - r * pairs;
             const float2 cs = cos_sin((uint64_t)(uint32_t)(x.lo + r) * p.turns[f]);
             const int at = r * pairs + (((f & 7) >> 2) * ru + (f >> 3)) * 4 + (f & 3);
@@ -115,148 +118,157 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constan
         __syncthreads();
     }
 
-    // ---- the heads ----------------------------------------------------------------
-    const int l = lane & (LPR - 1), u = l;  // the lane's two vectors of a row
+    // ---- the heads: of a kind (queries, keys, values) one after another ------------
+    const int u = lane & (LPR - 1);  // the lane's two vectors of a row
     const bool in_rot = u < ru;
     const int e0 = in_rot ? (PAIRED ? 16 * u : 8 * u) : p.rot + 16 * (u - ru);
     const int e1 = in_rot && !PAIRED ? e0 + pairs : e0 + 8;
     const bool whole = rows > kPasses * RPW;  // a head is the CTA's
     const int r_first = (whole ? warp * RPW : 0) + lane / LPR, r_step = whole ? kWarps * RPW : RPW;
-    int turn = 0;
-    for (int h = h_first + (whole ? 0 : warp); h < h_last; h += whole ? 1 : kWarps) {
-        const int hk = h - p.q.heads, hv = hk - c.Hkv;
-        const bool is_q = hk < 0, is_v = hv >= 0;
-        const int head = is_q ? h : (is_v ? hv : hk);
-        const RowsArg& in = is_q ? p.q : (is_v ? p.v : p.k);
-        Vt ra[kPasses], rb[kPasses];
+    const int h_step = whole ? 1 : kWarps, h_off = whole ? 0 : warp;
+    int64_t token[kPasses];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int r = r_first + i * r_step;
-            if (r < rows) {
-                const int64_t token = COMMIT ? (int64_t)x.b * (p.N + 1) + s_node[x.token + r] : x.token + r;
-                const T* row = (const T*)in.data + token * in.ts + head * in.hs;
-                ra[i] = *(const Vt*)(row + e0);
-                rb[i] = *(const Vt*)(row + e1);
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = min(r_first + i * r_step, rows - 1);  // (a lane without a row repeats the last)
+        token[i] = COMMIT ? (int64_t)x.b * (p.N + 1) + s_node[x.token + r] : x.token + r;
+    }
+    int turn = 0;
+    auto heads = [&](auto kind_, const RowsArg& in, int before, const float* weight) {
+        constexpr int kind = decltype(kind_)::value;  // 0 queries, 1 keys, 2 values
+        constexpr bool may_turn = !COMMIT && kind != 2;
+        const int to = min(h_last - before, in.heads);
+        int h = max(h_first - before, 0);
+        h += h_off;
+        if (h >= to) return;
+        struct Rows {
+            Vt a[kPasses], b[kPasses];
+        };
+        const T* src[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) src[i] = (const T*)in.data + token[i] * in.ts + h * in.hs;
+        const int64_t src_step = h_step * in.hs;
+        auto load = [&](Rows& v) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                v.a[i] = *(const Vt*)(src[i] + e0);
+                v.b[i] = *(const Vt*)(src[i] + e1);
+                src[i] += src_step;
             }
-        }
-        uint8_t *scale = nullptr, *codes = nullptr;
-        int old = least;
-        if (!is_q) {
-            scale = (is_v ? c.v_scales : c.k_scales) +
-                    ((((int64_t)page * c.Hkv + head) << (p.page_log2 - p.block_log2)) + (slot0 >> p.block_log2));
-            codes = (is_v ? c.v : c.k) + page * c.page_stride + head * c.head_stride + slot0 * c.slot_stride;
-            if (x.lo > x.p0) old = q8_from_byte(*scale, least);
-        }
-        float y[kPasses][2][8], most = 0.f;  // the elements at e0 and at e1
-        const bool norm = !COMMIT && !is_v && p.norm.on, turned_head = !COMMIT && !is_v && in_rot;
+        };
+        Rows ahead;
+        load(ahead);
+        const bool norm = may_turn && p.norm.on;
         float w[2][8];
         if (norm) {
-            const float* from = is_q ? p.norm.q_weight : p.norm.k_weight;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                w[0][e] = from ? __ldg(&from[e0 + e]) : 1.f;
-                w[1][e] = from ? __ldg(&from[e1 + e]) : 1.f;
+                w[0][e] = weight ? __ldg(&weight[place_of_pair<8, PAIRED>(e0, e1, e, false)]) : 1.f;
+                w[1][e] = weight ? __ldg(&weight[place_of_pair<8, PAIRED>(e0, e1, e, true)]) : 1.f;
             }
         }
+        for (; h < to; h += h_step) {
+            Rows v = ahead;
+            if (h + h_step < to) load(ahead);
+            uint8_t *scale = nullptr, *codes = nullptr;
+            int old = least;
+            if constexpr (kind > 0) {
+                scale = (kind == 2 ? c.v_scales : c.k_scales) +
+                        ((((int64_t)page * c.Hkv + h) << (p.page_log2 - p.block_log2)) + (slot0 >> p.block_log2));
+                codes = (kind == 2 ? c.v : c.k) + page * c.page_stride + h * c.head_stride + slot0 * c.slot_stride;
+                if (x.lo > x.p0) old = q8_from_byte(*scale, least);
+            }
+            float ya[kPasses][8], yb[kPasses][8], most = 0.f;  // first and second elements of pairs
+            float root[kPasses];  // the norm's factor, which may come last: a rotation is linear
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int r = r_first + i * r_step;
-            if (whole || i * RPW < rows) {  // (the warp as a whole)
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 a = unpack2<T>(reinterpret_cast<const uint32_t*>(ra[i].e)[e]);
-                    const float2 b = unpack2<T>(reinterpret_cast<const uint32_t*>(rb[i].e)[e]);
-                    y[i][0][2 * e] = a.x, y[i][0][2 * e + 1] = a.y;
-                    y[i][1][2 * e] = b.x, y[i][1][2 * e + 1] = b.y;
-                }
+            for (int i = 0; i < kPasses; ++i) {
+                unpack_pairs<T, 8, PAIRED>(v.a[i], v.b[i], ya[i], yb[i]);
+                root[i] = 1.f;
                 if (norm) {
+                    float s0 = 0.f, s1 = 0.f;
+                    add_squares<8>(ya[i], s0, s1);
+                    add_squares<8>(yb[i], s0, s1);
+                    s0 += s1;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) sum = fmaf(y[i][e >> 3][e & 7], y[i][e >> 3][e & 7], sum);
-#pragma unroll
-                    for (int d = LPR / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    const float f = rsqrtf(fmaf(sum, 1.f / D, p.norm.eps));
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[i][e >> 3][e & 7] *= f * w[e >> 3][e & 7];
+                    for (int d = LPR / 2; d; d >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, d);
+                    root[i] = rsqrtf(fmaf(s0, 1.f / D, p.norm.eps));
+                    scale_vec<8>(ya[i], w[0]);
+                    scale_vec<8>(yb[i], w[1]);
                 }
-                if (turned_head && r < rows) {
-                    const float* tc = s_cos + r * pairs + u * 4;
-                    const float* ts = s_sin + r * pairs + u * 4;
+                if (may_turn && in_rot) {
+                    const int at = min(r_first + i * r_step, rows - 1) * pairs + u * 4;
+                    float cv[8], sv[8];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        const float4 cc = *(const float4*)&tc[g * ru * 4], ss = *(const float4*)&ts[g * ru * 4];
-                        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+                        const float4 cc = *(const float4*)&s_cos[at + g * ru * 4], ss = *(const float4*)&s_sin[at + g * ru * 4];
+                        cv[4 * g] = cc.x, cv[4 * g + 1] = cc.y, cv[4 * g + 2] = cc.z, cv[4 * g + 3] = cc.w;
+                        sv[4 * g] = ss.x, sv[4 * g + 1] = ss.y, sv[4 * g + 2] = ss.z, sv[4 * g + 3] = ss.w;
+                    }
+                    turn_vec<8>(ya[i], yb[i], cv, sv);
+                }
+                if constexpr (kind > 0) {
+                    float m = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float& a = PAIRED ? y[i][g][2 * e] : y[i][0][4 * g + e];
-                            float& b = PAIRED ? y[i][g][2 * e + 1] : y[i][1][4 * g + e];
-                            const float2 z = turned(a, b, cv[e], sv[e]);
-                            a = z.x, b = z.y;
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(ya[i][e]), fabsf(yb[i][e])));
+                    most = fmaxf(most, m * root[i]);
+                }
+            }
+            if constexpr (kind == 0) {
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i)
+                    if (r_first + i * r_step < rows) {
+                        T* row = (T*)p.q_out.data + token[i] * p.q_out.ts + h * p.q_out.hs;
+                        Vt a, b;
+                        scale_by<8>(ya[i], root[i]);
+                        scale_by<8>(yb[i], root[i]);
+                        pack_pairs<T, 8, PAIRED>(ya[i], yb[i], a, b);
+                        *(Vt*)(row + e0) = a;
+                        *(Vt*)(row + e1) = b;
+                    }
+            } else {
+                most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (not negative)
+                if (whole) {
+                    if (lane == 0) s_max[turn][warp] = most;
+                    __syncthreads();  // (and every thread has read the old scale)
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_max[turn][i]);
+                    turn ^= 1;
+                }
+                const int e = max(q8_exponent(most, least), old);
+                if (x.lo > x.p0 && e > old) {  // the block's earlier codes move to its new scale
+                    const float f = pow2(old - e);
+                    const int n = (x.lo - x.p0) * LPR, step = whole ? 32 * kWarps : 32;
+                    for (int i = whole ? tid : lane; i < n; i += step) {
+                        uint4* to_ = (uint4*)(codes + (i / LPR) * c.slot_stride + (i & (LPR - 1)) * 16);
+                        const uint4 m = *to_;
+                        *to_ = make_uint4(q8_moved(m.x, f), q8_moved(m.y, f), q8_moved(m.z, f), q8_moved(m.w, f));
+                    }
+                }
+                const float f = pow2(-e);
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int r = r_first + i * r_step;
+                    if (r < rows) {
+                        uint8_t* row = codes + (x.lo - x.p0 + r) * c.slot_stride;
+                        float(&a)[8] = ya[i], (&b)[8] = yb[i];
+                        scale_by<8>(a, root[i] * f);  // (f is a power of two: one rounding)
+                        scale_by<8>(b, root[i] * f);
+                        if constexpr (PAIRED) {
+                            *(uint4*)(row + e0) = make_uint4(q8_pack4(a[0], b[0], a[1], b[1]), q8_pack4(a[2], b[2], a[3], b[3]),
+                                                             q8_pack4(a[4], b[4], a[5], b[5]), q8_pack4(a[6], b[6], a[7], b[7]));
+                        } else {
+                            *(uint2*)(row + e0) = make_uint2(q8_pack4(a[0], a[1], a[2], a[3]), q8_pack4(a[4], a[5], a[6], a[7]));
+                            *(uint2*)(row + e1) = make_uint2(q8_pack4(b[0], b[1], b[2], b[3]), q8_pack4(b[4], b[5], b[6], b[7]));
                         }
                     }
                 }
-                if (r < rows) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(y[i][e >> 3][e & 7]));
-                }
+                __syncwarp();  // (the warp's lanes have read the old scale)
+                if ((whole ? tid : lane) == 0) *scale = (uint8_t)(e + 127);
             }
         }
-        if (is_q) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int r = r_first + i * r_step;
-                if (r < rows) {
-                    T* row = (T*)p.q_out.data + (int64_t)(x.token + r) * p.q_out.ts + head * p.q_out.hs;
-                    Vt a, b;
-                    pack_vec<T, 8>(y[i][0], a);
-                    pack_vec<T, 8>(y[i][1], b);
-                    *(Vt*)(row + e0) = a;
-                    *(Vt*)(row + e1) = b;
-                }
-            }
-            continue;
-        }
-        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (not negative)
-        if (whole) {
-            if (lane == 0) s_max[turn][warp] = most;
-            __syncthreads();  // (and every thread has read the old scale)
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s_max[turn][i]);
-            turn ^= 1;
-        } else {
-            __syncwarp();
-        }
-        const int e = max(q8_exponent(most, least), old);
-        if (x.lo > x.p0 && e > old) {  // the block's earlier codes move to its new scale
-            const float f = pow2(old - e);
-            const int n = (x.lo - x.p0) * LPR, step = whole ? kThreads : 32;
-            for (int i = whole ? tid : lane; i < n; i += step) {
-                uint4* to = (uint4*)(codes + (i / LPR) * c.slot_stride + (i & (LPR - 1)) * 16);
-                const uint4 v = *to;
-                *to = make_uint4(q8_moved(v.x, f), q8_moved(v.y, f), q8_moved(v.z, f), q8_moved(v.w, f));
-            }
-        }
-        const float f = pow2(-e);
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int r = r_first + i * r_step;
-            if (r < rows) {
-                uint8_t* row = codes + (x.lo - x.p0 + r) * c.slot_stride;
-                uint32_t g[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    g[k] = q8_pack4(y[i][k >> 1][4 * (k & 1)] * f, y[i][k >> 1][4 * (k & 1) + 1] * f,
-                                    y[i][k >> 1][4 * (k & 1) + 2] * f, y[i][k >> 1][4 * (k & 1) + 3] * f);
-                if constexpr (PAIRED) {
-                    *(uint4*)(row + e0) = make_uint4(g[0], g[1], g[2], g[3]);
-                } else {
-                    *(uint2*)(row + e0) = make_uint2(g[0], g[1]);
-                    *(uint2*)(row + e1) = make_uint2(g[2], g[3]);
-                }
-            }
-        }
-        if ((whole ? tid : lane) == 0) *scale = (uint8_t)(e + 127);
-    }
+    };
+    if constexpr (!COMMIT) heads(std::integral_constant<int, 0>{}, p.q, 0, p.norm.q_weight);
+    heads(std::integral_constant<int, 1>{}, p.k, p.q.heads, p.norm.k_weight);
+    heads(std::integral_constant<int, 2>{}, p.v, p.q.heads + c.Hkv, nullptr);
     pdl_trigger();
 }
 
@@ -340,16 +352,28 @@ int heads_of(int heads, int64_t slots, int least) {
     return (int)std::max<int64_t>(std::min(least, heads), (heads + cuts - 1) / cuts);
 }
 
-template <typename T, int D, bool PAIRED, bool COMMIT>
-cudaError_t launch_write(WriteParams& p, int64_t blocks, cudaStream_t s) {
+template <typename T, int D, int WARPS, int PASSES, bool PAIRED, bool COMMIT>
+cudaError_t launch_passes(WriteParams& p, int64_t blocks, cudaStream_t s) {
     p.page_log2 = log2_of(p.cache.page_size);
     p.block_log2 = log2_of(p.cache.block);
     p.heads = p.q.heads + 2 * p.cache.Hkv;
-    p.chunk = heads_of(p.heads, blocks, kWarps);
+    p.chunk = heads_of(p.heads, blocks, WARPS);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)((p.heads + p.chunk - 1) / p.chunk));
-    return launch_pdl(write_kernel<T, D, PAIRED, COMMIT>, grid, dim3(kThreads),
+    return launch_pdl(write_kernel<T, D, WARPS, PASSES, PAIRED, COMMIT>, grid, dim3(32 * WARPS),
                       (size_t)p.cache.block * p.rot * sizeof(float), s, p);
+}
+// The fewest registers that hold a block's rows: one row a lane, two, or two of twice the
+// lanes (64 rows of D = 128; four a lane spilled).
+template <typename T, int D, bool PAIRED, bool COMMIT>
+cudaError_t launch_write(WriteParams& p, int64_t blocks, cudaStream_t s) {
+    constexpr int rows = 4 * 32 / (D / 16);  // of a pass of four warps
+    static_assert(DDTREE_MAX_Q8_BLOCK <= 4 * rows, "two passes of eight warps");
+    if constexpr (DDTREE_MAX_Q8_BLOCK > 2 * rows)
+        if (p.cache.block > 2 * rows) return launch_passes<T, D, 8, 2, PAIRED, COMMIT>(p, blocks, s);
+    if constexpr (DDTREE_MAX_Q8_BLOCK > rows)
+        if (p.cache.block > rows) return launch_passes<T, D, 4, 2, PAIRED, COMMIT>(p, blocks, s);
+    return launch_passes<T, D, 4, 1, PAIRED, COMMIT>(p, blocks, s);
 }
 template <typename T, int D>
 cudaError_t launch_append(WriteParams& p, int64_t blocks, bool paired, cudaStream_t s) {

@@ -37,16 +37,108 @@ struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 
-// Elements in 32 bits into a vector, rounded once.
-template <typename T, int V>
-DDT_DEV void pack_vec(const float (&y)[V], Vec<T, V>& v) {
+template <int V>
+struct alignas(V >= 4 ? 16 : 4 * V) VecF {  // V floats, 16 bytes an access
+    float e[V];
+};
+
+// A lane's share of a head in 32 bits: the first and the second elements of V pairs, whose
+// places are two vectors -- one each, or PAIRED neighbours, the first vector's before
+// the second's -- so that two pairs are worked on by an instruction, however they lie.
+//
+// Where the first (second) element of pair e is, in a head whose vectors are at e0 and e1.
+template <int V, bool PAIRED>
+DDT_DEV int place_of_pair(int e0, int e1, int e, bool second) {
+    if constexpr (!PAIRED) return (second ? e1 : e0) + e;
+    const int i = 2 * e + (second ? 1 : 0);
+    return i < V ? e0 + i : e1 + i - V;
+}
+template <typename T, int V, bool PAIRED>
+DDT_DEV void unpack_pairs(const Vec<T, V>& va, const Vec<T, V>& vb, float (&a)[V], float (&b)[V]) {
     if constexpr (sizeof(T) == 2 && V > 1) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(v.e);
+        const uint32_t* wa = reinterpret_cast<const uint32_t*>(va.e);
+        const uint32_t* wb = reinterpret_cast<const uint32_t*>(vb.e);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) w[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 x = unpack2<T>(wa[i]), y = unpack2<T>(wb[i]);
+            if constexpr (PAIRED) {
+                a[i] = x.x, b[i] = x.y;
+                a[V / 2 + i] = y.x, b[V / 2 + i] = y.y;
+            } else {
+                a[2 * i] = x.x, a[2 * i + 1] = x.y;
+                b[2 * i] = y.x, b[2 * i + 1] = y.y;
+            }
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v.e[e] = from_f<T>(y[e]);
+        for (int e = 0; e < V; ++e) {
+            a[e] = to_f(PAIRED ? (2 * e < V ? va.e[2 * e % V] : vb.e[2 * e % V]) : va.e[e]);
+            b[e] = to_f(PAIRED ? (2 * e + 1 < V ? va.e[(2 * e + 1) % V] : vb.e[(2 * e + 1) % V]) : vb.e[e]);
+        }
+    }
+}
+template <typename T, int V, bool PAIRED>
+DDT_DEV void pack_pairs(const float (&a)[V], const float (&b)[V], Vec<T, V>& va, Vec<T, V>& vb) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t* wa = reinterpret_cast<uint32_t*>(va.e);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(vb.e);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            wa[i] = PAIRED ? pack2<T>(a[i], b[i]) : pack2<T>(a[2 * i], a[2 * i + 1]);
+            wb[i] = PAIRED ? pack2<T>(a[V / 2 + i], b[V / 2 + i]) : pack2<T>(b[2 * i], b[2 * i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            (PAIRED ? (2 * e < V ? va.e[2 * e % V] : vb.e[2 * e % V]) : va.e[e]) = from_f<T>(a[e]);
+            (PAIRED ? (2 * e + 1 < V ? va.e[(2 * e + 1) % V] : vb.e[(2 * e + 1) % V]) : vb.e[e]) = from_f<T>(b[e]);
+        }
+    }
+}
+template <int V>
+DDT_DEV void scale_vec(float (&y)[V], const float (&s)[V]) {
+    if constexpr (V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) mul2(y[i], y[i + 1], s[i], s[i + 1]);
+    } else {
+        y[0] *= s[0];
+    }
+}
+template <int V>
+DDT_DEV void scale_by(float (&y)[V], float s) {
+    if constexpr (V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) mul2(y[i], y[i + 1], s, s);
+    } else {
+        y[0] *= s;
+    }
+}
+// Sums of squares, even and odd elements apart.
+template <int V>
+DDT_DEV void add_squares(const float (&y)[V], float& s0, float& s1) {
+    if constexpr (V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) fma2(s0, s1, y[i], y[i + 1], y[i], y[i + 1]);
+    } else {
+        s0 = fmaf(y[0], y[0], s0);
+    }
+}
+template <int V>
+DDT_DEV void turn_vec(float (&a)[V], float (&b)[V], const float (&c)[V], const float (&s)[V]) {
+    if constexpr (V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float x0 = a[i], x1 = a[i + 1];
+            float t0 = b[i], t1 = b[i + 1];
+            mul2(t0, t1, s[i], s[i + 1]);
+            a[i] = fmaf(x0, c[i], -t0), a[i + 1] = fmaf(x1, c[i + 1], -t1);
+            mul2(b[i], b[i + 1], c[i], c[i + 1]);
+            fma2(b[i], b[i + 1], x0, x1, s[i], s[i + 1]);
+        }
+    } else {
+        const float x = a[0];
+        a[0] = fmaf(x, c[0], -(b[0] * s[0]));
+        b[0] = fmaf(x, s[0], b[0] * c[0]);
     }
 }
 
