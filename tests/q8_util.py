@@ -25,7 +25,7 @@ def grid64(x):
 
 
 def codes64(pages):
-    """Codes as numbers (0x7F as 480), in 64 bits."""
+    """Codes as numbers (0x7F, which is none, as 480), in 64 bits."""
     c = pages.view(torch.uint8).int()
     e, m = (c >> 3) & 15, c & 7
     size = torch.where(e > 0, (8 + m) * torch.exp2((e - 10).double()), m * 2.0 ** -9)
@@ -61,7 +61,8 @@ def pool(gen, lens, Hkv, D, page, block, dtype, spare=2, width=None, slots_first
         x = torch.randn(total, Hkv, nb, block, D, generator=gen)
         x *= torch.exp2(spread * torch.randn(total, Hkv, nb, 1, 1, generator=gen))
         e = exponent64(x.abs().amax((3, 4)).double(), dtype)
-        c = (x * torch.exp2(-e.float())[..., None, None]).view(total, Hkv, page, D).to(E4M3).view(torch.uint8)
+        c = (x * torch.exp2(-e.float())[..., None, None]).clamp(-448, 448)  # (as the writers do)
+        c = c.view(total, Hkv, page, D).to(E4M3).view(torch.uint8)
         c = torch.where(live[:, None, :, None], c, torch.full_like(c, 0x7F))
         s = torch.where(owned[:, None, None], torch.full_like(e, 255), e + 127).to(torch.uint8)
         if slots_first:
