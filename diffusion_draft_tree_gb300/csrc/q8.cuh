@@ -52,9 +52,11 @@ DDT_DEV uint32_t q8_moved(uint32_t w, float factor) {
 }
 // Codes as elements of the tokens' type.  Each code's exponent and significand bits move to the
 // type's places and its sign bit to the top, which is a number 2^-8 (fp16) or 2^-120
-// (bf16) of the code's, subnormal codes included (and 0x7F as 480); one packed product with
-// the block's scale and that power gives the value, exactly.  (bf16's product takes and
-// gives subnormal numbers as they are.)
+// (bf16) of the code's, subnormal codes included; one packed product with the block's scale
+// and that power gives the value, exactly.  (bf16's product takes and gives subnormal
+// numbers as they are.)  Four instructions a pair: a byte permute puts a code under a
+// byte of its sign bit eight times, a shift brings both to their places, a mask
+// takes the sign bits between them away.
 //
 // What that product takes for a block's scale byte, as the type's bits.
 template <bool F16>
@@ -62,21 +64,25 @@ DDT_DEV uint32_t widen_factor(uint32_t byte) {
     const int e = q8_from_byte(byte, q8_least(F16));
     return F16 ? (uint32_t)(23 + e) << 10 : (uint32_t)(247 + e) << 7;
 }
-// The codes at bytes 1 and 3 of a word (bytes 0 and 2 hold none or others) as a pair.
-template <bool F16>
-DDT_DEV uint32_t widen_odd(uint32_t t, uint32_t factors) {
-    uint32_t r = (F16 ? (t >> 1) & 0x3f803f80u : (t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+// Two codes of a word, by a permutation that gives (code, its sign, code, its sign).
+template <bool F16, uint32_t SEL>
+DDT_DEV uint32_t widen(uint32_t w, uint32_t factors) {
+    uint32_t t;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w), "n"(SEL));
+    uint32_t r = F16 ? (t << 7) & 0xbf80bf80u : (t << 4) & 0x87f087f0u;
     if constexpr (F16) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(factors));
     else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(factors));
     return r;
 }
+// Codes 0, 1 and codes 2, 3 of a word; codes 0, 2 and 1, 3.
 template <bool F16>
-DDT_DEV uint32_t widen_even(uint32_t t, uint32_t factors) { return widen_odd<F16>(t << 8, factors); }
-// Codes 0, 1 and codes 2, 3 of a word as pairs in their order.
+DDT_DEV uint32_t widen_lo(uint32_t w, uint32_t factors) { return widen<F16, 0x9180>(w, factors); }
 template <bool F16>
-DDT_DEV uint32_t widen_lo(uint32_t t, uint32_t factors) { return widen_odd<F16>(__byte_perm(t, 0u, 0x1404), factors); }
+DDT_DEV uint32_t widen_hi(uint32_t w, uint32_t factors) { return widen<F16, 0xb3a2>(w, factors); }
 template <bool F16>
-DDT_DEV uint32_t widen_hi(uint32_t t, uint32_t factors) { return widen_odd<F16>(__byte_perm(t, 0u, 0x3424), factors); }
+DDT_DEV uint32_t widen_even(uint32_t w, uint32_t factors) { return widen<F16, 0xa280>(w, factors); }
+template <bool F16>
+DDT_DEV uint32_t widen_odd(uint32_t w, uint32_t factors) { return widen<F16, 0xb391>(w, factors); }
 
 // A run's tokens first[b] .. first[b + 1] - 1 become positions at[b] .. of sequence b.  Whether
 // it is one that no call may carry out: outside the T tokens or the table's positions.

@@ -29,10 +29,6 @@ DDT_DEV void mbar_arrive(uint64_t* bar) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}"
                  ::"r"(smem_u32(bar)) : "memory");
 }
-DDT_DEV void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}"
-                 ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
 DDT_DEV void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile(
         "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
@@ -100,6 +96,13 @@ DDT_DEV void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
 }
 
+// Registers of a thread of this group of four warps, which all come here: given back, or
+// taken from what other groups of the CTA gave back.
+template <int N>
+DDT_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+DDT_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor core operand reads).
 DDT_DEV void fence_proxy_async_smem() {
@@ -156,19 +159,6 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, int a_mn, int b_m
                : idesc_bf16_f32(M, N, a_mn, b_mn);
 }
 
-// ... for kind::f8f6f4 with e4m3 A/B, both K-major, and fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// Descriptor of a K-major tile of rows of `ROWB` bytes (128 or 64), swizzled over them: layout 2
-// or 4, eight rows a stride.
-template <int ROWB>
-DDT_DEV uint64_t smem_desc_rows(uint32_t saddr) {
-    static_assert(ROWB == 128 || ROWB == 64, "a row is a swizzle's width");
-    const uint64_t d = smem_desc_sw128(saddr, 16, 8 * ROWB);
-    return ROWB == 128 ? d : (d & ~(7ull << 61)) | 4ull << 61;
-}
-
 // Products, commits and copies are issued by a whole warp that keeps together, in
 // the one lane whose `lead` is set (elect_one), without a branch: the compiler
 // then keeps descriptors and addresses, equal in all lanes, in the uniform
@@ -188,17 +178,6 @@ DDT_DEV void mma_ss_warp(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_
         "setp.ne.b32 q, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
-}
-// ... of e4m3 operands.
-DDT_DEV void mma_ss_e4m3_warp(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                              uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }

@@ -113,10 +113,14 @@ struct Cfg {
 constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4, kQ8Bf16 = 5, kQ8Fp16 = 6;
 constexpr bool is_left(int mode) { return mode == kLeftBf16 || mode == kLeftFp16; }
 constexpr bool is_q8(int mode) { return mode >= kQ8Bf16; }
-constexpr bool is_split(int mode) { return mode == kQ8Bf16; }  // scores from 8-bit products (split_row)
 constexpr bool is_f16(int mode) { return mode == kPagedFp16 || mode == kLeftFp16 || mode == kQ8Fp16; }
 constexpr int kWideners = 4;  // warps that widen an 8-bit cache's tiles
-constexpr int threads_of(int mode) { return kThreads + (is_left(mode) ? 64 : is_q8(mode) ? 32 * kWideners : 0); }
+constexpr int threads_of(int mode) { return is_q8(mode) ? 512 : kThreads + (is_left(mode) ? 64 : 0); }
+// The first softmax warp.  Over an 8-bit cache registers move between groups of four warps: a
+// scheduler's four warps would have 128 each, of which the softmax takes 148.
+constexpr int softmax_warp(int mode) { return is_q8(mode) ? 4 : 2; }
+constexpr int kSoftmaxRegs = 128, kOtherRegs = 128;
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "of a scheduler's 512 a lane");
 // Tiles of codes (K's or V's) that wait to be widened: RAW of them behind the K and V
 // stages, and a lone query tile leaves room for two more where the second one would be.
 template <int D>
@@ -125,8 +129,6 @@ struct RawCfg {
     static constexpr int SLOTS = D == 128 ? 2 : 6;
     static constexpr int MORE = D == 128 ? 2 : 0;
     static_assert(MORE * BYTES <= Cfg<D>::QT_BYTES, "room of the second query tile");
-    static constexpr int PART = BN * D;  // bytes of a part of a tile in two e4m3 parts
-    static_assert(2 * PART == Cfg<D>::QT_BYTES && 2 * PART == Cfg<D>::KV_BYTES, "two parts take 16 bits");
     static_assert(SLOTS * BYTES >= 3 * BM * 8, "(m, l) rows of both groups and the second halves");
 };
 template <int D, int MODE>
@@ -168,8 +170,6 @@ struct PagedParams : Params {
 };
 
 struct Q8Params : PagedParams {
-    const uint16_t* k_tree;  // the tree's keys, in rows
-    int64_t kt_ts, kt_hs;
     const uint8_t *k_scales, *v_scales;
     int block_log2, per_page_log2;  // log2 of positions a scale, of scales a page and head
 };
@@ -580,8 +580,8 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
 // turn codes into the tokens' type between the copy and the tensor core: the kernel's
 // other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
-// Widens a tile of codes [128 keys][D] into [D / 64] swizzled slabs, eight keys by a
-// factor of `mult`; thread i of 32 kWideners.  The threads of a second slab store
+// Widens a tile of codes [128 keys][D] into [D / 64] swizzled slabs, eight keys by a factor
+// of `mult`; thread i of 32 kWideners.  The threads of a second slab store
 // their halves the other way round: 8 lanes then store to 8 different 16-byte banks.
 template <int D, bool F16>
 DDT_DEV void widen_tile(const uint8_t* raw, const uint16_t* mult, uint8_t* tile, int i) {
@@ -616,58 +616,6 @@ DDT_DEV void widen_tile(const uint8_t* raw, const uint16_t* mult, uint8_t* tile,
     }
 }
 
-// Scores from 8-bit products.  A bf16 number is a sum of two e4m3 numbers: it has 8
-// significant bits and a sign, e4m3 4, and what rounding to the first leaves is at most
-// 2^-5 of it.  So Q, and the tree's K, become two parts under a power of two each -- their
-// largest element is 224 to 448 then, and what is lost is below 2^-18 of that, where e4m3
-// ends -- and Q K^T is Q_hi C + Q_lo C with the codes C as they came from the cache, for the
-// tensor core's time of one 16-bit product: K is not widened at all (its tile is half as
-// long in shared memory, where a widened one passes twice), and its blocks' scales go
-// onto the scores, eight keys at a time.  fp16's 11 bits would take three parts; there K is
-// widened like V.
-//
-// The exponent of a row or group of rows with largest element amax.
-DDT_DEV int split_exponent(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    return min(max((int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0), -96), 120);
-}
-// Two elements, times f, as codes of both parts: the first's in the low half.
-DDT_DEV uint32_t split2(uint32_t w, float f) {
-    const float x = bf16lo(w) * f, y = bf16hi(w) * f;
-    const uint32_t hi = q8_pack2(x, y);
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi));
-    float hx, hy;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-        : "=f"(hx), "=f"(hy)
-        : "r"(h));
-    return hi | q8_pack2(x - hx, y - hy) << 16;
-}
-// 16 elements (two vectors) as a 16-byte chunk of either part.
-DDT_DEV void split16(const uint4& a, const uint4& b, float f, uint4& hi, uint4& lo) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = split2(w[i], f);
-    hi = make_uint4(__byte_perm(s[0], s[1], 0x5410), __byte_perm(s[2], s[3], 0x5410), __byte_perm(s[4], s[5], 0x5410),
-                    __byte_perm(s[6], s[7], 0x5410));
-    lo = make_uint4(__byte_perm(s[0], s[1], 0x7632), __byte_perm(s[2], s[3], 0x7632), __byte_perm(s[4], s[5], 0x7632),
-                    __byte_perm(s[6], s[7], 0x7632));
-}
-DDT_DEV float largest16(const uint4& a, const uint4& b) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-    return m;
-}
-// 16-byte chunk c of row r of a tile of codes, swizzled by its row's length.
-template <int D>
-DDT_DEV uint32_t swz_codes(int r, int c) {
-    return D == 128 ? swz(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
-constexpr int kScaleRing = 8;  // key tiles whose scales are kept: K stages and 2 at least
-
 // One CTA = one (sequence b, KV head g, pair of 128-row query tiles, KV split).
 // Warp 0: TMA producer.  Warp 1: TMEM owner and MMA issuer.  Warps 2-5: softmax
 // of query tile 0; warps 6-9: softmax of query tile 1.  Per KV tile j the
@@ -685,7 +633,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_vt,
                  const ParamsOf<MODE> p) {
     using C = Cfg<D>;
-    constexpr bool PAGED = MODE != kDense, F16 = is_f16(MODE), LEFT = is_left(MODE), Q8 = is_q8(MODE), SPLIT = is_split(MODE);
+    constexpr bool PAGED = MODE != kDense, F16 = is_f16(MODE), LEFT = is_left(MODE), Q8 = is_q8(MODE);
+    constexpr int SW = softmax_warp(MODE);
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_q, bar_kfull[NS], bar_kempty[NS], bar_vfull[NS],
@@ -700,16 +649,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     constexpr int NR = Q8 ? Raw::SLOTS + Raw::MORE : 1;
     __shared__ __align__(8) uint64_t bar_rfull[NR], bar_rempty[NR];  // tiles of codes
     __shared__ uint16_t s_mult[Q8 ? NR : 1][Q8 ? BN / 8 : 1];        // ... factors of eight keys each
-    // SPLIT: scales of eight keys each, by key tile; exponent of a query row's
-    __shared__ __align__(16) float s_kscale[SPLIT ? kScaleRing : 1][BN / 8];
-    __shared__ int8_t s_qexp[SPLIT ? 2 * BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one number a warp
 
     // ---- set-up that reads no global memory (overlaps the previous kernel) -------
     if (tid == 0) {
-        mbar_init(&bar_q, SPLIT ? kWideners : 1);
+        mbar_init(&bar_q, 1);
         constexpr int readers = LEFT ? 3 : 1;  // the tensor core, and two warps for the rows left over
         constexpr int writers = Q8 ? kWideners : 1;
         for (int s = 0; s < NS; ++s) {
@@ -924,7 +870,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         s_abort = 1;
     };
 
-    if (idle) {
+    if constexpr (Q8) {
+        if (warp >= SW && warp < SW + 8) reg_inc<kSoftmaxRegs>();
+        else reg_dec<kOtherRegs>();
+    }
+    if (idle || (Q8 && (warp == 2 || warp == 3))) {
     } else if (warp == 0) {
         // =========================== TMA producer ===========================
         // The warp keeps together and one lane issues: a lane that polled a barrier for
@@ -932,9 +882,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // warp of its scheduler (long_context_70b over pages 3.2 -> 4.1 ms) and made
         // the copies of 16-row pages the slowest part of the kernel.
         const uint32_t lead = elect_one();
-        if (!SPLIT && lane == 0) mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
+        if (lane == 0) mbar_arrive_expect_tx(&bar_q, (has1 ? 2 : 1) * C::NH * rows_used * 128);
         __syncwarp();
-        for (int h = 0; !SPLIT && h < C::NH; ++h) {
+        for (int h = 0; h < C::NH; ++h) {
             tma_load_3d_warp(lead, smem_u32(sq) + h * kHalfBytes, &tm_q, &bar_q, 64 * h, g * G, b * R + u00);
             if (has1)
                 tma_load_3d_warp(lead, smem_u32(sq) + C::QT_BYTES + h * kHalfBytes, &tm_q, &bar_q, 64 * h,
@@ -988,7 +938,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_ids = ids_of(2);
             uint4 k0 = scales_of(ids, 0, p.k_scales), v0 = scales_of(ids, 0, p.v_scales);
             uint4 k1 = scales_of(id1, 1, p.k_scales), v1 = scales_of(id1, 1, p.v_scales);
-            int c = 0, ring = 0, turn = 0, issued_k = 0;
+            int c = 0, ring = 0, turn = 0;
             bool ok = true;
             for (int i = 0; ok && i <= nprefix; ++i) {
                 const int ids_v = ids;  // the batch of tile i - 1
@@ -1004,12 +954,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int v = 0; v < 2; ++v) {
                     const int j = i - v;
                     if (j < 0 || j >= nprefix) continue;
-                    const bool straight = SPLIT && v == 0;  // K's codes go where the tensor core reads them
-                    const int st = j % NS;
-                    ok = straight ? mbar_wait_warp(&bar_kempty[st], ((j / NS) & 1) ^ 1, &s_abort)
-                                  : mbar_wait_warp(&bar_rempty[ring], turn ^ 1, &s_abort);
+                    ok = mbar_wait_warp(&bar_rempty[ring], turn ^ 1, &s_abort);
                     if (!ok) break;
-                    uint64_t* full = straight ? &bar_kfull[st] : &bar_rfull[ring];
                     const int mine = v ? ids_v : ids;
                     const uint4 y = v ? v_now : k0;
                     // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
@@ -1020,39 +966,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                        w3 = __shfl_sync(0xffffffffu, y.w, src);
                         word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
                     }
-                    const uint32_t scale = (word >> (8 * (byte & 3))) & 0xffu;
-                    if (straight) {
-                        if (!(lane & 1)) s_kscale[j & (kScaleRing - 1)][lane / 2] = pow2(q8_from_byte(scale, q8_least(F16)));
-                    } else {
-                        if (!(lane & 1)) s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>(scale);
-                    }
+                    if (!(lane & 1))
+                        s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
                     __syncwarp();
-                    if (lane == 0) {
-                        if (straight) mbar_arrive_n(full, kWideners - 1);  // (for the warps that fill a tree's)
-                        mbar_arrive_expect_tx(full, Raw::BYTES);
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
                     __syncwarp();
-                    const uint32_t to = straight ? smem_u32(sk) + st * C::KV_BYTES : smem_u32(raw_at(ring));
+                    const uint32_t to = smem_u32(raw_at(ring));
                     const int key0 = (t_begin + j) * BN;
 #pragma unroll 4
                     for (int x = 0; x < nb; ++x) {
                         const int page = __shfl_sync(0xffffffffu, mine, (j * nb + x) & 31);
-                        tma_load_4d_warp(lead, to + x * box * D, v ? &tm_vc : &tm_kc, full, 0,
+                        tma_load_4d_warp(lead, to + x * box * D, v ? &tm_vc : &tm_kc, &bar_rfull[ring], 0,
                                          (key0 + x * box) & (ps - 1), g, page);
                     }
-                    if (straight) {
-                        issued_k = j + 1;
-                    } else {
-                        ++c;
-                        if (++ring == raws) ring = 0, turn ^= 1;
-                    }
+                    ++c;
+                    if (++ring == raws) ring = 0, turn ^= 1;
                 }
             }
             if (!ok) fail();
             // (where a wait gave up, no copy may land in memory given back)
             mbar_wait(&bar_q, 0, nullptr, 100000000ull);
-            for (int j = max(0, issued_k - NS); j < issued_k; ++j)
-                mbar_wait(&bar_kfull[j % NS], (j / NS) & 1, nullptr, 100000000ull);
             for (int x = max(0, c - raws); x < c; ++x)
                 mbar_wait(&bar_rfull[x % raws], (x / raws) & 1, nullptr, 100000000ull);
         } else {
@@ -1113,83 +1046,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int j = max(0, issued[v] - NS); j < issued[v]; ++j)
                 mbar_wait(v ? &bar_vfull[j % NS] : &bar_kfull[j % NS], (j / NS) & 1, nullptr, 100000000ull);
         }
-    } else if (Q8 && warp >= 10) {
+    } else if (Q8 && warp >= SW + 8) {
         // ================= 8-bit cache: codes to 16-bit tiles =====================
         // In the ring's order.  A tree tile is 16-bit already: the first of these warps
         // has it copied in its turn.
         if constexpr (Q8) {
             const uint32_t lead = elect_one();
-            const int wi = warp - 10;
+            const int wi = warp - (SW + 8);
             int ring = 0, turn = 0, issued[2] = {0, 0};
             bool ok = true;
-            constexpr int CH = D / 16, RW = 32 / CH;  // lanes of a row (16 elements each), rows of a warp
-            const int ch = lane % CH;
-            if constexpr (SPLIT) {  // the queries' two parts
-                for (int r0 = wi * RW; r0 < (has1 ? 2 : 1) * BM; r0 += kWideners * RW) {
-                    const int r2 = r0 + lane / CH, r = r2 % BM, u = (r2 < BM ? u00 : u01) + r / G;
-                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b2 = a;
-                    if (r < rows_used && u <= n) {
-                        const uint4* row = (const uint4*)(p.q + ((int64_t)b * R + u) * p.q_ts + (int64_t)(g * G + r % G) * p.q_hs);
-                        a = __ldg(row + 2 * ch), b2 = __ldg(row + 2 * ch + 1);
-                    }
-                    float m = largest16(a, b2);
-#pragma unroll
-                    for (int d = CH / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    const int e = split_exponent(m);
-                    uint4 hi, lo;
-                    split16(a, b2, pow2(-e), hi, lo);
-                    uint8_t* to = sq + (r2 / BM) * C::QT_BYTES + swz_codes<D>(r, ch);
-                    *(uint4*)to = hi;
-                    *(uint4*)(to + Raw::PART) = lo;
-                    if (ch == 0) s_qexp[r2] = (int8_t)e;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_q);
-            }
             for (int i = 0; ok && i <= nt; ++i) {
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     const int j = i - v, s = j % NS;
                     if (j < 0 || j >= nt) continue;
-                    if constexpr (SPLIT) {
-                        if (v == 0) {
-                            if (j < nprefix) continue;  // K's codes are copied straight to their stage
-                            // a tree tile's keys in two parts, eight keys under one power of two
-                            ok = mbar_wait_warp(&bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
-                            if (!ok) break;
-                            const int a0 = (tree_first + j - nprefix) * BN;
-                            for (int g8 = wi; g8 < BN / 8; g8 += kWideners) {
-                                uint4 a[8 / RW], b2[8 / RW];
-                                float m = 0.f;
-#pragma unroll
-                                for (int x = 0; x < 8 / RW; ++x) {
-                                    const int u = a0 + 8 * g8 + x * RW + lane / CH;
-                                    a[x] = b2[x] = make_uint4(0u, 0u, 0u, 0u);
-                                    if (u <= n) {
-                                        const uint4* row = (const uint4*)(p.k_tree + ((int64_t)b * R + u) * p.kt_ts + (int64_t)g * p.kt_hs);
-                                        a[x] = __ldg(row + 2 * ch), b2[x] = __ldg(row + 2 * ch + 1);
-                                    }
-                                    m = fmaxf(m, largest16(a[x], b2[x]));
-                                }
-                                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-                                const int e = split_exponent(m);
-#pragma unroll
-                                for (int x = 0; x < 8 / RW; ++x) {
-                                    uint4 hi, lo;
-                                    split16(a[x], b2[x], pow2(-e), hi, lo);
-                                    uint8_t* to = sk + s * C::KV_BYTES + swz_codes<D>(8 * g8 + x * RW + lane / CH, ch);
-                                    *(uint4*)to = hi;
-                                    *(uint4*)(to + Raw::PART) = lo;
-                                }
-                                if (lane == 0) s_kscale[j & (kScaleRing - 1)][g8] = pow2(e);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bar_kfull[s]);
-                            continue;
-                        }
-                    }
                     uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
                     uint8_t* to = (v ? sv : sk) + s * C::KV_BYTES;
                     const bool codes = j < nprefix;
@@ -1239,10 +1109,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t kd = smem_desc_sw128(smem_u32(sk), 16, 1024);
         const uint64_t vd = smem_desc_sw128(smem_u32(sv), kHalfBytes, 1024);
         const uint32_t k_half = dual ? kHalfRows >> 4 : 0u, q_tile = dual ? 0u : C::QT_BYTES >> 4;
-        // 8-bit products: K-major tiles of D bytes a row
-        const uint32_t idesc_q8 = idesc_e4m3_f32(BM, dual ? BN / 2 : BN);
-        const uint64_t qd8 = smem_desc_rows<D>(smem_u32(sq)), kd8 = smem_desc_rows<D>(smem_u32(sk));
-        const uint32_t k_half8 = dual ? (BN / 2 * D) >> 4 : 0u;
         bool ok = mbar_wait_warp(&bar_q, 0, &s_abort);
 #pragma unroll 1
         for (int j = -ahead; ok && j < nt; ++j) {
@@ -1270,32 +1136,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const int s = jq % NS;
                     if (k == 0) ok = mbar_wait_warp(&bar_kfull[s], (jq / NS) & 1, &s_abort);
                     tc_fence_after();
-                    const uint32_t d0 = s_k + buffer(jq);
-                    if constexpr (SPLIT) {
-                        const uint64_t a0 = qd8 + k * q_tile;
-                        const uint64_t b0 = kd8 + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half8;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < D / 32; ++kk)
-                                mma_ss_e4m3_warp(lead, d0, a0 + ((part * Raw::PART + kk * 32) >> 4), b0 + ((kk * 32) >> 4),
-                                                 idesc_q8, part > 0 || kk > 0);
-                        if (jq >= nprefix) {  // the tree's keys have a second part too
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                                for (int kk = 0; kk < D / 32; ++kk)
-                                    mma_ss_e4m3_warp(lead, d0, a0 + ((part * Raw::PART + kk * 32) >> 4),
-                                                     b0 + ((Raw::PART + kk * 32) >> 4), idesc_q8, 1);
-                        }
-                    } else {
                     const uint64_t a0 = qd + k * q_tile;
                     const uint64_t b0 = kd + (uint32_t)(s * (C::KV_BYTES >> 4)) + k * k_half;
+                    const uint32_t d0 = s_k + buffer(jq);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
                         mma_ss_warp(lead, d0, a0 + off, b0 + off, idesc_qk, kk > 0);
-                    }
                     }
                     mma_commit_warp(lead, &bar_sfull[k][bar_of(jq)]);
                     if (k == 1 || !two) mma_commit_warp(lead, &bar_kempty[s]);
@@ -1332,7 +1179,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else {
         // ==================== softmax / epilogue, one thread per query row ====================
-        const int k = (warp - 2) >> 2;            // query tile of this group
+        const int k = (warp - SW) >> 2;            // query tile of this group
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;         // query row == TMEM lane
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
@@ -1346,17 +1193,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int hh = g * G + r % G;
         const bool row_used = !PAGED || r < rows_used;
         const bool row_valid = work && (u <= n) && row_used;
-        float sl2 = p.scale_log2;
-        if constexpr (SPLIT) {  // (the query row's power of two)
-            if (work && mbar_wait_warp(&bar_q, 0, &s_abort)) sl2 *= pow2(s_qexp[dual ? r : k * BM + r]);
-        }
-        // SPLIT: what raw scores of keys 32 c + 8 i .. + 7 of the group's columns are
-        // multiplied with; not zero, for scores of -inf
-        auto factors = [&](int j, int c, float (&f)[4]) {
-            const float4 x = *(const float4*)&s_kscale[j & (kScaleRing - 1)][(key0 / 32 + c) * 4];
-            f[0] = fmaxf(x.x * sl2, 1e-37f), f[1] = fmaxf(x.y * sl2, 1e-37f);
-            f[2] = fmaxf(x.z * sl2, 1e-37f), f[3] = fmaxf(x.w * sl2, 1e-37f);
-        };
+        const float sl2 = p.scale_log2;
         // ancestor words of this row for the next tree tile, fetched one tile ahead
         uint32_t am[4] = {0u, 0u, 0u, 0u};
         auto fetch_mask = [&](int tt) {
@@ -1440,38 +1277,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // current one is used ----
                 uint32_t qa[32], qb[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto qmax = [&](const uint32_t (&q)[32], int c) {
-                    if constexpr (SPLIT) {
-                        float f[4];
-                        factors(j, c, f);
-#pragma unroll
-                        for (int g8 = 0; g8 < 4; ++g8) {
-                            float m = __uint_as_float(q[8 * g8]);
-#pragma unroll
-                            for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(q[8 * g8 + i]));
-                            mx[g8] = fmaxf(mx[g8], m * f[g8]);
-                        }
-                        return;
-                    }
+                auto qmax = [&](const uint32_t (&q)[32]) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(q[i]));
                 };
                 tmem_ld32(tm_s, qa);
                 tmem_ld_wait(qa);
                 tmem_ld32(tm_s + 32, qb);
-                qmax(qa, 0);
+                qmax(qa);
                 tmem_ld_wait(qb);
                 if (!dual) {
                     tmem_ld32(tm_s + 64, qa);
-                    qmax(qb, 1);
+                    qmax(qb);
                     tmem_ld_wait(qa);
                     tmem_ld32(tm_s + 96, qb);
-                    qmax(qa, 2);
+                    qmax(qa);
                     tmem_ld_wait(qb);
                 }
-                qmax(qb, dual ? 1 : 3);
+                qmax(qb);
                 const float mt_raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float m_new = fmaxf(m_run, SPLIT ? mt_raw : mt_raw * sl2);
+                const float m_new = fmaxf(m_run, mt_raw * sl2);
                 const bool resc = m_new > m_run + kRescaleLog2;
                 const float m_use = resc ? m_new : m_run;
                 const float factor = resc ? fast_exp2(m_run - m_new) : 1.f;
@@ -1492,12 +1317,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 float2 acc = make_float2(0.f, 0.f);
                 auto qexp = [&](const uint32_t (&q)[32], int c) {
                     uint32_t pk[16];
-                    float f[4];
-                    if constexpr (SPLIT) factors(j, c, f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 y = ffma2(make_float2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1])),
-                                               SPLIT ? f[i / 4] : sl2, neg);
+                        const float2 y = ffma2(make_float2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1])), sl2, neg);
                         const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                         pk[i] = pack16<F16>(e.x, e.y);
                         acc = fadd2(acc, e);
@@ -1687,7 +1509,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         } else if (exchange) {
             // (the partial stays in TMEM until the peers' shared memory is idle)
-            if (tid == 64) s_ok = all_ok;
+            if (tid == 32 * SW) s_ok = all_ok;
         } else if (p.merge == kMergeCluster) {
             if (have) {
                 // This split's partial into its own shared memory (Q and K/V stages
@@ -1753,7 +1575,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __threadfence();
             }
             softmax_bar();
-            if (tid == 64) {
+            if (tid == 32 * SW) {
                 // every split takes its ticket, also after a timeout, so that the
                 // counter returns to zero for the next call
                 const bool last = ticket_is_last(&p.tickets[(b * p.Hkv + g) * p.mpairs + mpair],
@@ -1834,14 +1656,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int S = p.smax;
             const uint32_t slot = chunk_slots<D>(S) * kChunk4;
             const uint32_t recv = smem_u32(base), recv_ml = recv + (uint32_t)S * slot;
-            const int k = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, tile = dual ? 0 : k;
+            const int k = (warp - SW) >> 2, r = (warp & 3) * 32 + lane, tile = dual ? 0 : k;
             const int row2 = tile * BM + r;
             const int u = (tile == 0 ? u00 : u01) + r / G, hh = g * G + r % G;
             const bool mine = tile == 0 || has1;
             const bool row_valid = mine && u <= n && r < rows_used;
             fence_proxy_async_smem();
             cluster_sync();
-            const bool rows_warp = warp >= 2 && (!Q8 || warp < 10);
+            const bool rows_warp = warp >= SW && (!Q8 || warp < SW + 8);
             if (rows_warp && mine && !idle && s_ok) {
                 tc_fence_after();
                 const uint32_t tm_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + tile * D;
@@ -1971,7 +1793,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             if (warp >= 2) {
-                const int k = (warp - 2) >> 2;
+                const int k = (warp - SW) >> 2;
                 const int r = (warp & 3) * 32 + lane;
                 const int row2 = k * BM + r;
                 const int u = (k == 0 ? u00 : u01) + r / G;

@@ -7,14 +7,13 @@ namespace ddt {
 
 namespace {
 
-// (an 8-bit cache's V is widened from rows as they are; so is K, unless the tensor core reads it)
-template <int D, int MODE>
-bool cache_map(CUtensorMap* m, const PagedArgs& c, const void* pages, bool) {
-    return page_map<D>(m, c, pages, BN, is_f16(MODE));
+template <int D>
+bool cache_map(CUtensorMap* m, const PagedArgs& c, const void* pages, bool f16) {
+    return page_map<D>(m, c, pages, BN, f16);
 }
-template <int D, int MODE>
-bool cache_map(CUtensorMap* m, const Q8Args& c, const void* pages, bool is_k) {
-    return code_map<D>(m, c, pages, BN, is_k && is_split(MODE));
+template <int D>
+bool cache_map(CUtensorMap* m, const Q8Args& c, const void* pages, bool) {
+    return code_map<D>(m, c, pages, BN);
 }
 
 template <int D, int MODE, typename Args>
@@ -43,7 +42,7 @@ cudaError_t launch_mode(const Args& a, cudaStream_t s) {
     CUtensorMap mq, mkc, mvc, mkt, mvt;
     if (!tree_map<D>(&mq, a.q, tokens, G, pl.npt, f16) || !tree_map<D>(&mkt, a.k_tree, tokens, 1, BN, f16) ||
         !tree_map<D>(&mvt, a.v_tree, tokens, 1, BN, f16) ||
-        !cache_map<D, MODE>(&mkc, a.cache, a.cache.k, true) || !cache_map<D, MODE>(&mvc, a.cache, a.cache.v, false))
+        !cache_map<D>(&mkc, a.cache, a.cache.k, f16) || !cache_map<D>(&mvc, a.cache, a.cache.v, f16))
         return cudaErrorInvalidValue;
     ParamsOf<MODE> p{};
     p.prefix_len = a.prefix_len;
@@ -82,8 +81,6 @@ cudaError_t launch_mode(const Args& a, cudaStream_t s) {
     p.npt = pl.npt;
     p.single = pl.single;
     if constexpr (is_q8(MODE)) {
-        p.k_tree = (const uint16_t*)a.k_tree.data;
-        p.kt_ts = a.k_tree.ts, p.kt_hs = Hkv > 1 ? a.k_tree.hs : D;
         p.k_scales = a.cache.k_scales;
         p.v_scales = a.cache.v_scales;
         for (p.block_log2 = 0; (1 << p.block_log2) < a.cache.block;) ++p.block_log2;
