@@ -22,7 +22,7 @@ BINDING = os.path.join(PKG, "_ddtree.so")
 SOURCES = ["api.cu", "topk.cu", "build.cu", "build_level.cu", "tree_attn.cu", "accept.cu",
            "accept_path.cu", "commit.cu", "rotary.cu", "tree_attn_paged.cu", "tree_attn_left.cu",
            "tree_attn_rows.cu", "norm_rope.cu", "quant.cu", "tree_attn_q8.cu",
-           "tree_attn_q8_rows.cu"]
+           "tree_attn_q8_rows.cu", "tree_attn_q8_left.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

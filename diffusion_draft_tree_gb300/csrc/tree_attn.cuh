@@ -110,16 +110,17 @@ struct Cfg {
 
 // Where the prefix lives, and the 16-bit type of everything; LEFT: with two warps for
 // the rows that the query tiles leave over.
-constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4, kQ8Bf16 = 5, kQ8Fp16 = 6;
-constexpr bool is_left(int mode) { return mode == kLeftBf16 || mode == kLeftFp16; }
+constexpr int kDense = 0, kPagedBf16 = 1, kPagedFp16 = 2, kLeftBf16 = 3, kLeftFp16 = 4, kQ8Bf16 = 5, kQ8Fp16 = 6,
+              kQ8LeftBf16 = 7, kQ8LeftFp16 = 8;
 constexpr bool is_q8(int mode) { return mode >= kQ8Bf16; }
-constexpr bool is_f16(int mode) { return mode == kPagedFp16 || mode == kLeftFp16 || mode == kQ8Fp16; }
+constexpr bool is_left(int mode) { return mode == kLeftBf16 || mode == kLeftFp16 || mode >= kQ8LeftBf16; }
+constexpr bool is_f16(int mode) { return mode > kDense && mode % 2 == 0; }
 constexpr int kWideners = 4;  // warps that widen an 8-bit cache's tiles
 constexpr int threads_of(int mode) { return is_q8(mode) ? 512 : kThreads + (is_left(mode) ? 64 : 0); }
 // The first softmax warp.  Over an 8-bit cache registers move between groups of four warps: a
 // scheduler's four warps would have 128 each, of which the softmax takes 148.
 constexpr int softmax_warp(int mode) { return is_q8(mode) ? 4 : 2; }
-constexpr int kSoftmaxRegs = 128, kOtherRegs = 128;
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "of a scheduler's 512 a lane");
 // Tiles of codes (K's or V's) that wait to be widened: RAW of them behind the K and V
 // stages, and a lone query tile leaves room for two more where the second one would be.
@@ -130,6 +131,7 @@ struct RawCfg {
     static constexpr int MORE = D == 128 ? 2 : 0;
     static_assert(MORE * BYTES <= Cfg<D>::QT_BYTES, "room of the second query tile");
     static_assert(SLOTS * BYTES >= 3 * BM * 8, "(m, l) rows of both groups and the second halves");
+    static_assert(SLOTS * BYTES >= 2 * 8 * (D + 4) * 4, "outputs of the rows left over");
 };
 template <int D, int MODE>
 constexpr int smem_of() { return Cfg<D>::SMEM + (is_q8(MODE) ? RawCfg<D>::SLOTS * RawCfg<D>::BYTES : 0); }
@@ -333,7 +335,7 @@ struct LeftArgs {
     float* part;  // [split][mpair][kLeftRows][D + 4]
     unsigned int* ticket;
     uint64_t *kfull, *kempty, *vfull, *vempty;
-    uint8_t *sk, *sv;
+    uint8_t *sk, *sv, *scratch;  // scratch: (8-bit cache) free once all tiles are there
     volatile int* abort;
     int W, Hq, G, rows, nodes;  // nodes: live ones among them, may be <= 0
     int n, P, t_begin, nprefix, nt, tree_first, split, splits, mpair, mpairs;
@@ -344,11 +346,13 @@ struct LeftArgs {
 // Named barrier over the two warps.
 DDT_DEV void left_bar() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
 
-template <int D, bool F16>
+template <int D, bool F16, bool Q8>
 __device__ __noinline__ void left_rows(const LeftArgs& a) {
     using C = Cfg<D>;
     constexpr int NS = C::NS, NH = C::NH;
-    __shared__ __align__(16) float s_o[2][kLeftRows][D + 4];
+    using Out = float[kLeftRows][D + 4];
+    __shared__ __align__(16) float s_o_own[Q8 ? 1 : 2 * kLeftRows * (D + 4)];
+    Out* s_o = reinterpret_cast<Out*>(Q8 ? reinterpret_cast<float*>(a.scratch) : s_o_own);
     __shared__ float2 s_ml[2][kLeftRows];
     __shared__ int s_state;  // bit w: warp w gave up; bit 2: the last part
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 1, t = threadIdx.x & 63;
@@ -871,10 +875,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
 
     if constexpr (Q8) {
-        if (warp >= SW && warp < SW + 8) reg_inc<kSoftmaxRegs>();
-        else reg_dec<kOtherRegs>();
+        if (warp < SW || warp >= SW + 8) reg_dec<kOtherRegs>();
     }
-    if (idle || (Q8 && (warp == 2 || warp == 3))) {
+    if (idle || (Q8 && !LEFT && (warp == 2 || warp == 3))) {
     } else if (warp == 0) {
         // =========================== TMA producer ===========================
         // The warp keeps together and one lane issues: a lane that polled a barrier for
@@ -1154,7 +1157,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // memory given back; otherwise the last tile's commit says the same)
         mma_commit_warp(lead, &bar_drain);
         mbar_wait(&bar_drain, 0, nullptr, 100000000ull);
-    } else if (LEFT && warp >= 10) {
+    } else if (LEFT && (Q8 ? warp < SW : warp >= 10)) {
         if constexpr (LEFT) {
             const int u = p.mtiles * nodes_per_tile;  // the first node left over
             const size_t unit = (size_t)b * p.Hkv + g, row = ((size_t)b * R + u) * p.Hq + g * G;
@@ -1167,7 +1170,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             a.part = p.part_left + unit * p.smax * p.mpairs * (kLeftRows * (D + 4));
             a.ticket = p.tickets_left + unit;
             a.kfull = bar_kfull, a.kempty = bar_kempty, a.vfull = bar_vfull, a.vempty = bar_vempty;
-            a.sk = sk, a.sv = sv;
+            a.sk = sk, a.sv = sv, a.scratch = Q8 ? sr : nullptr;
             a.abort = &s_abort;
             a.W = p.W, a.Hq = p.Hq, a.G = G, a.rows = p.left, a.nodes = n - u + 1;
             a.n = n, a.P = P, a.t_begin = t_begin, a.nprefix = nprefix, a.nt = nt;
@@ -1175,10 +1178,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             a.mpair = mpair, a.mpairs = p.mpairs;
             a.sl2 = p.scale_log2;
             a.err = p.err;
-            left_rows<D, F16>(a);
+            left_rows<D, F16, Q8>(a);
         }
     } else {
         // ==================== softmax / epilogue, one thread per query row ====================
+        if constexpr (Q8) reg_inc<kSoftmaxRegs>();
         const int k = (warp - SW) >> 2;            // query tile of this group
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;         // query row == TMEM lane
@@ -2041,14 +2045,14 @@ constexpr int kLoneTiles = 80;
 struct ManyPlan : Plan {
     int left;
 };
-ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms, bool take_along = true) {
+ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms) {
     ManyPlan pl{};
     (Plan&)pl = plan_base(N, Hq, Hkv);
     const int G = Hq / Hkv, left = (N + 1 - (pl.mtiles - 1) * (BM / G)) * G;
     if (plan_units(pl, B, Hkv) < sms) return pl;  // few units (smax = 0)
     const long along = (long)B * Hkv * (pl.mpairs - 1);  // units if the pairs take them
     const bool short_wave = pl.mpairs == 2 && along * 10 < sms * 7L && t.prefix + t.tree <= kLoneTiles;
-    if (take_along && pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
+    if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
         --pl.mtiles;
         --pl.mpairs;
         pl.left = left;

@@ -26,7 +26,7 @@ cudaError_t launch_mode(const Args& a, cudaStream_t s) {
     const int G = Hq / Hkv, R = a.N + 1;
     const Tiles t = max_tiles(a.N, cap);
     const int sms = num_sms();
-    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms, !is_q8(MODE));
+    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms);
     PagedPlan pl{};
     if (many.smax) {
         (Plan&)pl = many;
@@ -97,5 +97,6 @@ cudaError_t launch_mode(const Args& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_attn_left(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_tree_attn_q8_left(const Q8AttnArgs& a, cudaStream_t s);
 
 }  // namespace ddt
