@@ -96,13 +96,6 @@ DDT_DEV void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
 }
 
-// Registers of a thread of this group of four warps, which all come here: given back, or
-// taken from what other groups of the CTA gave back.
-template <int N>
-DDT_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-DDT_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor core operand reads).
 DDT_DEV void fence_proxy_async_smem() {

@@ -39,7 +39,7 @@
 // length rather than by the table's capacity.  kLeftBf16 / kLeftFp16 are those for
 // many units with two warps more, for a few rows that whole pairs of tiles leave
 // over (left_rows).  kQ8Bf16 / kQ8Fp16 read an 8-bit cache, with four warps more that widen
-// its tiles (widen_tile).
+// its tiles (widen_codes).
 #pragma once
 
 #include <mutex>
@@ -117,11 +117,9 @@ constexpr bool is_left(int mode) { return mode == kLeftBf16 || mode == kLeftFp16
 constexpr bool is_f16(int mode) { return mode > kDense && mode % 2 == 0; }
 constexpr int kWideners = 4;  // warps that widen an 8-bit cache's tiles
 constexpr int threads_of(int mode) { return is_q8(mode) ? 512 : kThreads + (is_left(mode) ? 64 : 0); }
-// The first softmax warp.  Over an 8-bit cache registers move between groups of four warps: a
-// scheduler's four warps would have 128 each, of which the softmax takes 148.
+// The first softmax warp (over an 8-bit cache the first four warps are the copies', the
+// products', and two for the rows left over).
 constexpr int softmax_warp(int mode) { return is_q8(mode) ? 4 : 2; }
-constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
-static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "of a scheduler's 512 a lane");
 // Tiles of codes (K's or V's) that wait to be widened: RAW of them behind the K and V
 // stages, and a lone query tile leaves room for two more where the second one would be.
 template <int D>
@@ -584,39 +582,44 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
 // turn codes into the tokens' type between the copy and the tensor core: the kernel's
 // other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
-// Widens a tile of codes [128 keys][D] into [D / 64] swizzled slabs, eight keys by a factor
-// of `mult`; thread i of 32 kWideners.  The threads of a second slab store
+// A thread's share of a tile of codes [128 keys][D]: 16 codes of every 16th row (D = 64: 32nd),
+// and the factors of their blocks.
+template <int D>
+struct Codes {
+    static constexpr int CH = D / 16;                 // 16-byte chunks of a row
+    static constexpr int STEP = 32 * kWideners / CH;  // rows between a thread's
+    static constexpr int N = BN / STEP;
+    uint4 w[N];
+    uint32_t m[N];
+};
+// ... from a slot of the ring; thread i of 32 kWideners.
+template <int D>
+DDT_DEV void load_codes(Codes<D>& x, const uint8_t* raw, const uint16_t* mult, int i) {
+    using C = Codes<D>;
+    const int c = i % C::CH, r0 = i / C::CH;
+#pragma unroll
+    for (int p = 0; p < C::N; ++p) {
+        const int r = r0 + p * C::STEP;
+        x.w[p] = *(const uint4*)(raw + r * D + c * 16);
+        x.m[p] = (uint32_t)mult[r >> 3] * 0x10001u;
+    }
+}
+// ... widened into the tile's [D / 64] swizzled slabs.  The threads of a second slab store
 // their halves the other way round: 8 lanes then store to 8 different 16-byte banks.
 template <int D, bool F16>
-DDT_DEV void widen_tile(const uint8_t* raw, const uint16_t* mult, uint8_t* tile, int i) {
-    constexpr int CH = D / 16;                        // 16-byte chunks of a row
-    constexpr int STEP = 32 * kWideners / CH;         // rows of a pass
-    const int c = i % CH, r0 = i / CH;
-    const int slab = c >> 2, flip = slab & 1;
-    constexpr int BATCH = 4;
-#pragma unroll 1
-    for (int p0 = 0; p0 < BN / STEP; p0 += BATCH) {
-        uint4 w[BATCH];
-        uint32_t m[BATCH];
+DDT_DEV void widen_codes(const Codes<D>& x, uint8_t* tile, int i) {
+    using C = Codes<D>;
+    const int c = i % C::CH, r0 = i / C::CH, flip = (c >> 2) & 1, first = (c & 3) * 2;
+    uint8_t* to = tile + (c >> 2) * kHalfBytes;
 #pragma unroll
-        for (int p = 0; p < BATCH; ++p) {
-            const int r = r0 + (p0 + p) * STEP;
-            w[p] = *(const uint4*)(raw + r * D + c * 16);
-            m[p] = (uint32_t)mult[r >> 3] * 0x10001u;
-        }
-#pragma unroll
-        for (int p = 0; p < BATCH; ++p) {
-            const int r = r0 + (p0 + p) * STEP;
-            uint4 y[2];
-            y[0] = make_uint4(widen_lo<F16>(w[p].x, m[p]), widen_hi<F16>(w[p].x, m[p]),
-                              widen_lo<F16>(w[p].y, m[p]), widen_hi<F16>(w[p].y, m[p]));
-            y[1] = make_uint4(widen_lo<F16>(w[p].z, m[p]), widen_hi<F16>(w[p].z, m[p]),
-                              widen_lo<F16>(w[p].w, m[p]), widen_hi<F16>(w[p].w, m[p]));
-            uint8_t* to = tile + slab * kHalfBytes;
-            const int first = (c & 3) * 2;
-            *(uint4*)(to + swz(r, first + flip)) = flip ? y[1] : y[0];
-            *(uint4*)(to + swz(r, first + 1 - flip)) = flip ? y[0] : y[1];
-        }
+    for (int p = 0; p < C::N; ++p) {
+        const int r = r0 + p * C::STEP;
+        const uint4 a = make_uint4(widen_lo<F16>(x.w[p].x, x.m[p]), widen_hi<F16>(x.w[p].x, x.m[p]),
+                                   widen_lo<F16>(x.w[p].y, x.m[p]), widen_hi<F16>(x.w[p].y, x.m[p]));
+        const uint4 b = make_uint4(widen_lo<F16>(x.w[p].z, x.m[p]), widen_hi<F16>(x.w[p].z, x.m[p]),
+                                   widen_lo<F16>(x.w[p].w, x.m[p]), widen_hi<F16>(x.w[p].w, x.m[p]));
+        *(uint4*)(to + swz(r, first + flip)) = flip ? b : a;
+        *(uint4*)(to + swz(r, first + 1 - flip)) = flip ? a : b;
     }
 }
 
@@ -874,9 +877,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         s_abort = 1;
     };
 
-    if constexpr (Q8) {
-        if (warp < SW || warp >= SW + 8) reg_dec<kOtherRegs>();
-    }
     if (idle || (Q8 && !LEFT && (warp == 2 || warp == 3))) {
     } else if (warp == 0) {
         // =========================== TMA producer ===========================
@@ -1066,18 +1066,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     uint64_t* full = v ? &bar_vfull[s] : &bar_kfull[s];
                     uint8_t* to = (v ? sv : sk) + s * C::KV_BYTES;
                     const bool codes = j < nprefix;
-                    if (codes) ok = mbar_wait_warp(&bar_rfull[ring], turn, &s_abort);
-                    ok = ok && mbar_wait_warp(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
+                    Codes<D> x;
+                    if (codes) {  // into registers first: the slot is free then, whatever the stage is
+                        ok = mbar_wait_warp(&bar_rfull[ring], turn, &s_abort);
+                        if (!ok) break;
+                        load_codes<D>(x, raw_at(ring), s_mult[ring], wi * 32 + lane);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar_rempty[ring]);
+                        if (++ring == raws) ring = 0, turn ^= 1;
+                    }
+                    ok = mbar_wait_warp(v ? &bar_vempty[s] : &bar_kempty[s], ((j / NS) & 1) ^ 1, &s_abort);
                     if (!ok) break;
                     if (codes) {
-                        widen_tile<D, F16>(raw_at(ring), s_mult[ring], to, wi * 32 + lane);
+                        widen_codes<D, F16>(x, to, wi * 32 + lane);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(full);
-                            mbar_arrive(&bar_rempty[ring]);
-                        }
-                        if (++ring == raws) ring = 0, turn ^= 1;
+                        if (lane == 0) mbar_arrive(full);
                     } else if (wi == 0) {
                         if (lane == 0) mbar_arrive_expect_tx(full, C::KV_BYTES);
                         __syncwarp();
@@ -1182,7 +1186,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else {
         // ==================== softmax / epilogue, one thread per query row ====================
-        if constexpr (Q8) reg_inc<kSoftmaxRegs>();
         const int k = (warp - SW) >> 2;            // query tile of this group
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;         // query row == TMEM lane
