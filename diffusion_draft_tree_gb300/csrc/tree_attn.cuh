@@ -582,44 +582,48 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
 // turn codes into the tokens' type between the copy and the tensor core: the kernel's
 // other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
-// A thread's share of a tile of codes [128 keys][D]: 16 codes of every 16th row (D = 64: 32nd),
-// and the factors of their blocks.
+// A thread's share of a tile of codes [128 keys][D]: 16 codes of rows of one group of eight,
+// which are under one scale.  (Shared memory is what these warps wait for: with a
+// factor a row, two broadcast loads more in 18, the 70B-class long context took 3.16 ms.)
 template <int D>
 struct Codes {
-    static constexpr int CH = D / 16;                 // 16-byte chunks of a row
-    static constexpr int STEP = 32 * kWideners / CH;  // rows between a thread's
-    static constexpr int N = BN / STEP;
+    static constexpr int CH = D / 16;    // 16-byte chunks of a row: as many lanes
+    static constexpr int SUB = 8 / CH;   // rows that eight lanes take at once
+    static constexpr int N = BN * CH / (32 * kWideners);
+    static_assert(N * SUB == 8, "eight lanes take eight rows");
     uint4 w[N];
-    uint32_t m[N];
+    uint32_t m;
+    // Lanes of D = 128's second slab are a row ahead or behind: eight lanes then read, and
+    // store, 8 different 16-byte banks (by turns of the halves instead, with selects, 3.14
+    // ms; not at all 3.04).
+    static DDT_DEV int row(int i, int p) {
+        return (i & ~7) + (D == 128 ? p ^ ((i >> 2) & 1) : (i & 7) / CH + p * SUB);
+    }
 };
 // ... from a slot of the ring; thread i of 32 kWideners.
 template <int D>
 DDT_DEV void load_codes(Codes<D>& x, const uint8_t* raw, const uint16_t* mult, int i) {
     using C = Codes<D>;
-    const int c = i % C::CH, r0 = i / C::CH;
+    x.m = mult[i >> 3];
 #pragma unroll
-    for (int p = 0; p < C::N; ++p) {
-        const int r = r0 + p * C::STEP;
-        x.w[p] = *(const uint4*)(raw + r * D + c * 16);
-        x.m[p] = (uint32_t)mult[r >> 3] * 0x10001u;
-    }
+    for (int p = 0; p < C::N; ++p) x.w[p] = *(const uint4*)(raw + C::row(i, p) * D + i % C::CH * 16);
 }
-// ... widened into the tile's [D / 64] swizzled slabs.  The threads of a second slab store
-// their halves the other way round: 8 lanes then store to 8 different 16-byte banks.
+// ... widened into the tile's [D / 64] swizzled slabs.
 template <int D, bool F16>
 DDT_DEV void widen_codes(const Codes<D>& x, uint8_t* tile, int i) {
     using C = Codes<D>;
-    const int c = i % C::CH, r0 = i / C::CH, flip = (c >> 2) & 1, first = (c & 3) * 2;
+    const int c = i % C::CH, first = (c & 3) * 2;
+    const uint32_t m = x.m * 0x10001u;
     uint8_t* to = tile + (c >> 2) * kHalfBytes;
 #pragma unroll
     for (int p = 0; p < C::N; ++p) {
-        const int r = r0 + p * C::STEP;
-        const uint4 a = make_uint4(widen_lo<F16>(x.w[p].x, x.m[p]), widen_hi<F16>(x.w[p].x, x.m[p]),
-                                   widen_lo<F16>(x.w[p].y, x.m[p]), widen_hi<F16>(x.w[p].y, x.m[p]));
-        const uint4 b = make_uint4(widen_lo<F16>(x.w[p].z, x.m[p]), widen_hi<F16>(x.w[p].z, x.m[p]),
-                                   widen_lo<F16>(x.w[p].w, x.m[p]), widen_hi<F16>(x.w[p].w, x.m[p]));
-        *(uint4*)(to + swz(r, first + flip)) = flip ? b : a;
-        *(uint4*)(to + swz(r, first + 1 - flip)) = flip ? a : b;
+        const int r = C::row(i, p);
+        const uint4 a = make_uint4(widen_lo<F16>(x.w[p].x, m), widen_hi<F16>(x.w[p].x, m),
+                                   widen_lo<F16>(x.w[p].y, m), widen_hi<F16>(x.w[p].y, m));
+        const uint4 b = make_uint4(widen_lo<F16>(x.w[p].z, m), widen_hi<F16>(x.w[p].z, m),
+                                   widen_lo<F16>(x.w[p].w, m), widen_hi<F16>(x.w[p].w, m));
+        *(uint4*)(to + swz(r, first)) = a;
+        *(uint4*)(to + swz(r, first + 1)) = b;
     }
 }
 
@@ -924,7 +928,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // the ring, with their keys' factors.  Scales come with the page numbers, 32
             // boxes at a time (lane l the up to 16 bytes of box 32 k + l), a batch ahead of
             // their use: page numbers two ahead.
-            const int per_box_log2 = max(0, 31 - __clz(box) - p.block_log2), per_box = 1 << per_box_log2;
+            const int box_log2 = 31 - __clz(box), per_box = 1 << max(0, box_log2 - p.block_log2);
             auto scales_of = [&](int page, int k, const uint8_t* from) {
                 uint4 y = make_uint4(0u, 0u, 0u, 0u);
                 if (page == num_pages) return y;
@@ -961,8 +965,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (!ok) break;
                     const int mine = v ? ids_v : ids;
                     const uint4 y = v ? v_now : k0;
+                    const uint32_t to = smem_u32(raw_at(ring));
+                    const int key0 = (t_begin + j) * BN;
+#pragma unroll 4
+                    for (int x = 0; x < nb; ++x) {
+                        const int page = __shfl_sync(0xffffffffu, mine, (j * nb + x) & 31);
+                        tma_load_4d_warp(lead, to + x * box * D, v ? &tm_vc : &tm_kc, &bar_rfull[ring], 0,
+                                         (key0 + x * box) & (ps - 1), g, page);
+                    }
+                    // (the copies are on their way while the scales still are)
                     // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
-                    const int src = (j * nb + 4 * lane / box) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
+                    const int src = (j * nb + (4 * lane >> box_log2)) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
                     uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
                     if (per_box > 4) {
                         const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
@@ -973,15 +986,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
-                    __syncwarp();
-                    const uint32_t to = smem_u32(raw_at(ring));
-                    const int key0 = (t_begin + j) * BN;
-#pragma unroll 4
-                    for (int x = 0; x < nb; ++x) {
-                        const int page = __shfl_sync(0xffffffffu, mine, (j * nb + x) & 31);
-                        tma_load_4d_warp(lead, to + x * box * D, v ? &tm_vc : &tm_kc, &bar_rfull[ring], 0,
-                                         (key0 + x * box) & (ps - 1), g, page);
-                    }
                     ++c;
                     if (++ring == raws) ring = 0, turn ^= 1;
                 }

@@ -96,7 +96,8 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
     if (warp == kWarps) {
         // ============================= copy warp =============================
         const int ps = 1 << p.ps_log2, box = min(ps, kTile), nb = kTile / box;
-        const int per_box = 1 << max(0, 31 - __clz(box) - p.block_log2);  // scales of a box
+        const int box_log2 = 31 - __clz(box);
+        const int per_box = 1 << max(0, box_log2 - p.block_log2);  // scales of a box
         const uint32_t lead = elect_one();
         // Page numbers come 32 boxes at a time, lane l holding box 32 k + l of its unit,
         // two batches -- of this unit or the next ones -- ahead; the boxes' scales, up to 16
@@ -169,26 +170,6 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
             const int boxes = tree ? 0 : min(nb, (prefix_of(at) - key0 + box - 1) / box);
             // (of the warp as a whole)
             if (!mbar_wait_warp(&bar_empty[s], ((it / NS) & 1) ^ 1, &s_abort)) { fail(); break; }
-            if (!tree) {
-                // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
-                const int src = (at.tile * nb + 4 * lane / box) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint4 y = v ? vs : ks;
-                    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
-                    if (per_box > 4) {
-                        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
-                                       w3 = __shfl_sync(0xffffffffu, y.w, src);
-                        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
-                    }
-                    const uint32_t m = widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
-                    *(uint2*)&s_mult[s][v][4 * lane] = make_uint2(m, m);
-                }
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_expect_tx(&bar_full[s], tree ? 4 * D * R : 2 * D * boxes * box);
-            __syncwarp();
             const uint32_t dk = smem_u32(base + s * C::STAGE);
             if (tree) {
 #pragma unroll
@@ -205,6 +186,25 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
                     tma_load_4d_warp(lead, dk + C::KV + i * box * D, &tm_vc, &bar_full[s], 0, row, at.g, page);
                 }
             }
+            if (!tree) {  // (the copies are on their way while the scales still are)
+                // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
+                const int src = (at.tile * nb + (4 * lane >> box_log2)) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint4 y = v ? vs : ks;
+                    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
+                    if (per_box > 4) {
+                        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
+                                       w3 = __shfl_sync(0xffffffffu, y.w, src);
+                        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
+                    }
+                    const uint32_t m = widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
+                    *(uint2*)&s_mult[s][v][4 * lane] = make_uint2(m, m);
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bar_full[s], tree ? 4 * D * R : 2 * D * boxes * box);
             issued = it + 1;
         }
         // (where a wait gave up, here or below, no copy may land in memory given back)
