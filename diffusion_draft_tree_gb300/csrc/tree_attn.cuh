@@ -983,7 +983,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
                     }
                     if (!(lane & 1))
-                        s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
+                        s_mult[ring][lane / 2] = (uint16_t)pair_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
                     ++c;
@@ -1423,8 +1423,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tmem_st_wait();
             l += sum;
-            // (the widened rows of an 8-bit cache are numbers, whatever their codes)
-            if (k == 0 && quarter * 32 + 32 > lim_t && (!Q8 || is_tree)) {  // (the warp as a whole)
+            // (bf16 rows of an 8-bit cache are numbers, whatever their codes)
+            if (k == 0 && quarter * 32 + 32 > lim_t && (!Q8 || F16 || is_tree)) {  // (the warp as a whole)
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
                 if (!mbar_wait_warp(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }
