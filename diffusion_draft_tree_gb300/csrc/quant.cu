@@ -21,7 +21,10 @@ namespace ddt {
 namespace {
 
 constexpr int kThreads = 128;  // of the reader; the writers' CTAs have as many or twice
-constexpr int kFill = 16;   // CTAs per SM that fill the GPU
+// CTAs per SM that fill the GPU: a block's heads are cut over CTAs up to that.  An append's
+// CTAs each fill the block's table (prompts of 18K tokens 98 us at 16, 90 at 3); a commit's
+// have none and wait for their rows (128 paths 7.3 us at 3).
+constexpr int kFillAppend = 3, kFill = 16, kFillRead = 8;
 
 struct WriteParams {
     RowsArg q, q_out, k, v;
@@ -48,7 +51,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
     // cos and sin of row r's pair 8 u + e, at [r][e / 4][u][e % 4]
     extern __shared__ __align__(16) float s_cos[];
     __shared__ float s_max[2][kWarps];
-    __shared__ int s_node[DDTREE_MAX_L + 1];
+    __shared__ int s_node[DDTREE_MAX_L + 1], s_page[DDTREE_MAX_L + 1];  // of a path's rows
     __shared__ int s_bad;
     const Q8Args& c = p.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = c.block;
@@ -69,6 +72,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                 const int node = tid ? p.accepted_nodes[(int64_t)x.b * p.L + tid - 1] : 0;
                 const int page = c.table[x.b * c.table_stride + ((P + tid) >> p.page_log2)];
                 s_node[tid] = node;
+                s_page[tid] = page;
                 if (tid && (node < 1 || node > p.N)) bad = ERR_BAD_TREE;
                 else if (page < 0 || page >= c.num_pages) bad = ERR_BAD_PAGE;
             }
@@ -94,7 +98,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
             check_run(p.first, p.at, p.B, p.T, cap, blockIdx.x, p.err, ERR_APPEND | ERR_BAD_INPUT);
         if (!x.ok) return;
     }
-    const int page = c.table[x.b * c.table_stride + (x.p0 >> p.page_log2)];
+    const int page = COMMIT ? s_page[x.token] : c.table[x.b * c.table_stride + (x.p0 >> p.page_log2)];
     const bool there = page >= 0 && page < c.num_pages;
     const int rows = x.hi - x.lo, slot0 = x.p0 & (c.page_size - 1), least = q8_least(c.dtype == 2);
     const int h_first = blockIdx.y * p.chunk;
@@ -346,9 +350,9 @@ int log2_of(int x) {
     return n;
 }
 
-// Heads of a CTA: as many as leave kFill CTAs an SM, at least `least` of them.
-int heads_of(int heads, int64_t slots, int least) {
-    const int64_t fill = (int64_t)num_sms() * kFill, cuts = std::max<int64_t>(1, (fill + slots - 1) / slots);
+// Heads of a CTA: as many as leave per_sm CTAs an SM, at least `least` of them.
+int heads_of(int heads, int64_t slots, int least, int per_sm) {
+    const int64_t fill = (int64_t)num_sms() * per_sm, cuts = std::max<int64_t>(1, (fill + slots - 1) / slots);
     return (int)std::max<int64_t>(std::min(least, heads), (heads + cuts - 1) / cuts);
 }
 
@@ -357,7 +361,7 @@ cudaError_t launch_passes(WriteParams& p, int64_t blocks, cudaStream_t s) {
     p.page_log2 = log2_of(p.cache.page_size);
     p.block_log2 = log2_of(p.cache.block);
     p.heads = p.q.heads + 2 * p.cache.Hkv;
-    p.chunk = heads_of(p.heads, blocks, WARPS);
+    p.chunk = heads_of(p.heads, blocks, WARPS, COMMIT ? kFill : kFillAppend);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)((p.heads + p.chunk - 1) / p.chunk));
     return launch_pdl(write_kernel<T, D, WARPS, PASSES, PAIRED, COMMIT>, grid, dim3(32 * WARPS),
@@ -421,7 +425,7 @@ cudaError_t launch_read_q8(const ReadQ8Args& a, cudaStream_t s) {
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     // (at least one round of a CTA's threads)
     const int tasks = 2 * a.cache.Hkv, one = a.cache.block * a.cache.D / 16;
-    p.chunk = heads_of(tasks, blocks, std::max(1, kThreads / one));
+    p.chunk = heads_of(tasks, blocks, std::max(1, kThreads / one), kFillRead);
     const dim3 grid((unsigned)blocks, (unsigned)((tasks + p.chunk - 1) / p.chunk));
     const bool f16 = a.cache.dtype == 2;
     if (a.cache.D == 128)
