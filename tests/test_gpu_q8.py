@@ -454,8 +454,6 @@ def test_attention_bad_pages_count_as_zeros(cuda_device, N):
     args = attn_case(gen, [400, 90], N, 8, 2, 128, 16, 16, BF16)
     cache = args[1]
     good = cache.page_table.clone()
-    zero = torch.cat([x[:1] for x in (cache.k_pages.view(torch.uint8),)])
-    del zero
     spare = [i for i in range(cache.num_pages) if i not in good.flatten().tolist()][0]
     for x in (cache.k_pages, cache.v_pages):
         x.view(torch.uint8)[spare] = 0

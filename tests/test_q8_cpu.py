@@ -147,8 +147,22 @@ def test_attention_refusals():
     assert _attn(q=_rows(heads=8, ts=1028)) == 1
     assert _attn(B=0) == 1 and _attn(N=-1) == 1 and _attn(scale=0.0) == 1 and _attn(scale=float("nan")) == 1
     assert _attn(N=1025) == 2 and _attn(q=_rows(heads=258, ts=40000)) == 2
-    need = ops.workspace_size(ops.OP_TREE_ATTN_Q8, B=1, N=4, Hq=8, Hkv=2, D=128, cache_cap=64)
-    if need:
-        assert _attn(ws=None) == 1 and _attn(wsb=need - 1) == 1 and _attn(ws=P(0x100080)) == 1
+    need = ops.workspace_size(ops.OP_TREE_ATTN_Q8, B=1, N=0, Hq=8, Hkv=2, D=128, cache_cap=64)
+    assert need > 0  # (few rows: the pieces of cut units)
+    assert _attn(N=0, ws=None) == 1 and _attn(N=0, wsb=need - 1) == 1 and _attn(N=0, ws=P(0x100080)) == 1
     assert ops.workspace_size(ops.OP_TREE_ATTN_Q8, B=0, N=4, Hq=8, Hkv=2, D=128, cache_cap=64) == 0
     assert ops.workspace_size(ops.OP_TREE_ATTN_Q8, B=1, N=4, Hq=7, Hkv=2, D=128, cache_cap=64) == 0
+
+
+def test_the_kernel_for_few_rows_keeps_its_warps_whole_and_drains_its_copies():
+    """The rules of the attention kernels' sources (test_kernel_sources_cpu.py) in the one over an
+    8-bit cache."""
+    import os
+    import re
+    at = os.path.join(os.path.dirname(ops.LIB_PATH), "csrc", "tree_attn_q8_rows.cu")
+    with open(at) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    assert text.count("mbar_wait_warp(") >= 3
+    for m in re.finditer(r"\bmbar_wait\(", text):
+        assert text[:m.start()].rstrip().endswith((";", ")", "{", "}")), text[m.start() - 60:m.end() + 40]
+    assert re.search(r"mbar_wait\(&bar_full\[it % NS\],[^;]*nullptr, 100000000ull\);", text)
