@@ -604,18 +604,22 @@ class QuantCache:
     @classmethod
     def empty(cls, num_pages: int, Hkv: int, page_size: int, D: int, page_table: torch.Tensor,
               block: int = 32, dtype: torch.dtype = torch.bfloat16) -> "QuantCache":
-        """New pages of zeros on the table's device."""
+        """New pages of zeros on the table's device, under the type's least scale: a block that
+        a run enters in its middle keeps the larger of its old scale and the one it needs."""
+        if dtype not in _LEAST_SCALE:
+            raise ValueError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
         if block < 1 or page_size % block:
             raise ValueError(f"block must divide page_size, got {block} and {page_size}")
         dev = page_table.device
         pages = [torch.zeros(num_pages, Hkv, page_size, D, dtype=torch.uint8, device=dev)
                  .view(torch.float8_e4m3fn) for _ in range(2)]
-        scales = [torch.full((num_pages, Hkv, page_size // block), 127, dtype=torch.uint8, device=dev)
-                  for _ in range(2)]
+        scales = [torch.full((num_pages, Hkv, page_size // block), _LEAST_SCALE[dtype],
+                             dtype=torch.uint8, device=dev) for _ in range(2)]
         return cls(*pages, *scales, page_table, dtype)
 
 
 _NO_NORM = (None, -1, -1)
+_LEAST_SCALE = {torch.bfloat16: 127 - 96, torch.float16: 127 - 15}
 
 
 def ddtree_norm_rope(q, k, pos, norm: HeadNorm, rotary: Optional[Rotary] = None, q_out=None,

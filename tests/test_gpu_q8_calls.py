@@ -233,3 +233,11 @@ def test_batches_without_a_token_write_nothing(cuda_device, T):
     assert all(torch.equal(a, b) for a, b in zip(was, held(cache))) and torch.equal(q, q0)
     assert bool((out == 2).all()) and bool((out2 == 2).all())
     ops.ddtree_device_check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_an_empty_cache_has_the_least_scales(cuda_device, dtype):
+    # (a run that enters a block in its middle keeps the larger of the old scale and its own)
+    cache = fresh(3, 2, 16, 64, [[0]], 8, dtype)
+    for s in (cache.k_scales, cache.v_scales):
+        assert bool((s == 127 + qu.LEAST[dtype]).all())

@@ -4,6 +4,7 @@ import ctypes
 import struct
 
 import pytest
+import torch
 
 from diffusion_draft_tree_gb300 import ops
 
@@ -166,3 +167,8 @@ def test_the_kernel_for_few_rows_keeps_its_warps_whole_and_drains_its_copies():
     for m in re.finditer(r"\bmbar_wait\(", text):
         assert text[:m.start()].rstrip().endswith((";", ")", "{", "}")), text[m.start() - 60:m.end() + 40]
     assert re.search(r"mbar_wait\(&bar_full\[it % NS\],[^;]*nullptr, 100000000ull\);", text)
+
+
+def test_an_empty_cache_of_another_type_is_refused():
+    with pytest.raises(ValueError, match="dtype"):
+        ops.QuantCache.empty(3, 2, 16, 64, torch.zeros(1, 1, dtype=torch.int32), dtype=torch.float32)
