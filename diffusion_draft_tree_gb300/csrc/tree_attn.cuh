@@ -582,6 +582,12 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // be lost to the e4m3 range, and a long tail of those is what a sink leaves).  So four warps
 // turn codes into the tokens' type between the copy and the tensor core: the kernel's
 // other parts see 16-bit tiles.  Keys and values are exact there (q8.cuh).
+// A key tile and pair of query tiles (D = 128) needs 2048 cycles of products, and moves 320 KB
+// through shared memory, 2560 cycles at 128 bytes each: 192 KB of operands, 32 in as
+// codes, 32 out and 64 in as it is widened.  Neither is reached: the long context takes
+// about 3300 a tile at 1.9 GHz, the 16-bit cache 2950.  70B-class long context (4 trees of
+// 257 nodes behind 128K) 2.99 to 3.04 ms in bf16, 2.88 in fp16, where the 16-bit cache takes
+// 2.67 to 2.76; without the widening 2.58.  Queries in two e4m3 parts against the codes themselves: 3.46.
 // A thread's share of a tile of codes [128 keys][D]: 16 codes of rows of one group of eight,
 // which are under one scale.  (Shared memory is what these warps wait for: with a
 // factor a row, two broadcast loads more in 18, the 70B-class long context took 3.16 ms.)
@@ -872,7 +878,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint8_t* sr = sv + NS * C::KV_BYTES;         // (8-bit cache) tiles of codes
     const int raws = Raw::SLOTS + (dual ? Raw::MORE : 0);
     auto raw_at = [&](int s) { return s < Raw::SLOTS ? sr + s * Raw::BYTES : sq + C::QT_BYTES + (s - Raw::SLOTS) * Raw::BYTES; };
-    // (every tile of codes is widened when these are written)
+    // (every tile of codes is widened when these are written; s_ml is a cluster's and s_ml1 a
+    // lone tile's, and neither is where rows are left over, whose outputs take this room)
     float2* s_ml = Q8 ? reinterpret_cast<float2*>(sr) : s_ml_own;
     float2* s_ml1 = Q8 ? reinterpret_cast<float2*>(sr) + 2 * BM : s_ml1_own;
 

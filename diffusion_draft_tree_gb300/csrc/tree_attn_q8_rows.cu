@@ -11,6 +11,9 @@
 // products' own affair for K, where Q is loaded in the same order; for V, ldmatrix
 // transposes pairs of codes, and a pair's two elements are two rows of O^T.
 // Warp w takes keys [32 w, 32 w + 32) of a tile.
+//
+// 64 sequences of 512 to 16384, 32 query and 8 KV heads, D = 128: 178 us, 93 % of the measured
+// HBM rate (the tcgen05 kernel 478, its query tile 4 rows of 128; the 16-bit cache 327).
 #include "q8.cuh"
 #include "tree_attn_rows.cuh"
 

@@ -460,8 +460,8 @@ typedef struct {
 
 /* ddtree_rope with the norm of every head before the rotation, in one pass: the
  * same tensors, types, alignment rules and limits.  rot may be NULL: the norm
- * alone.  Norm, rotation and their sums are formed in 32 bits and rounded once.  A
- * token at a negative position is copied as it is. */
+ * alone.  Norm, rotation and their sums are formed in 32 bits and rounded once (squares
+ * too, so elements up to about 2^60).  A token at a negative position is copied as it is. */
 ddtree_status ddtree_norm_rope(const ddtree_rows* q, const ddtree_rows* q_out,
                                const ddtree_rows* k, const ddtree_rows* k_out, int dtype, int T,
                                int D, const int32_t* pos, const ddtree_head_norm* norm,
@@ -509,8 +509,9 @@ typedef struct {
  * codes behind a run's end are left as they are.  Elements are quantised from 32 bits, to
  * the nearest, ties to even.
  * A run whose tokens lie outside 0..T or whose positions lie outside the table is
- * left out, queries too, and recorded; so is the part of a run whose page lies outside
- * the pool (its queries are still written).  The pages written belong to one sequence
+ * left out, queries too, and recorded; where first descends, which is recorded, other runs
+ * may be left out as well.  So is the part of a run whose page lies outside the pool
+ * (its queries are still written).  The pages written belong to one sequence
  * alone.  The caller's lengths are not changed.  T = 0 does nothing.  Every pointer
  * 16-byte aligned, strides of rows multiples of 8 elements.  No workspace. */
 ddtree_status ddtree_append_q8(const ddtree_rows* k, const ddtree_rows* v, int T,
