@@ -183,11 +183,10 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                 if (x.lo > x.p0) old = q8_from_byte(*scale, least);
             }
             float ya[kPasses][8], yb[kPasses][8], most = 0.f;  // first and second elements of pairs
-            float root[kPasses];  // the norm's factor, which may come last: a rotation is linear
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 unpack_pairs<T, 8, PAIRED>(v.a[i], v.b[i], ya[i], yb[i]);
-                root[i] = 1.f;
+                float root = 1.f;  // the norm's factor, which may come last: a rotation is linear
                 if (norm) {
                     float s0 = 0.f, s1 = 0.f;
                     add_squares<8>(ya[i], s0, s1);
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                     s0 += s1;
 #pragma unroll
                     for (int d = LPR / 2; d; d >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, d);
-                    root[i] = rsqrtf(fmaf(s0, 1.f / D, p.norm.eps));
+                    root = rsqrtf(fmaf(s0, 1.f / D, p.norm.eps));
                     scale_vec<8>(ya[i], w[0]);
                     scale_vec<8>(yb[i], w[1]);
                 }
@@ -210,11 +209,15 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                     }
                     turn_vec<8>(ya[i], yb[i], cv, sv);
                 }
+                if (norm) {
+                    scale_by<8>(ya[i], root);
+                    scale_by<8>(yb[i], root);
+                }
                 if constexpr (kind > 0) {
                     float m = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(ya[i][e]), fabsf(yb[i][e])));
-                    most = fmaxf(most, m * root[i]);
+                    most = fmaxf(most, m);
                 }
             }
             if constexpr (kind == 0) {
@@ -223,8 +226,6 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                     if (r_first + i * r_step < rows) {
                         T* row = (T*)p.q_out.data + token[i] * p.q_out.ts + h * p.q_out.hs;
                         Vt a, b;
-                        scale_by<8>(ya[i], root[i]);
-                        scale_by<8>(yb[i], root[i]);
                         pack_pairs<T, 8, PAIRED>(ya[i], yb[i], a, b);
                         *(Vt*)(row + e0) = a;
                         *(Vt*)(row + e1) = b;
@@ -255,8 +256,8 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                     if (r < rows) {
                         uint8_t* row = codes + (x.lo - x.p0 + r) * c.slot_stride;
                         float(&a)[8] = ya[i], (&b)[8] = yb[i];
-                        scale_by<8>(a, root[i] * f);  // (f is a power of two: one rounding)
-                        scale_by<8>(b, root[i] * f);
+                        scale_by<8>(a, f);  // (a power of two, and by itself: times a root it may pass the 32-bit range)
+                        scale_by<8>(b, f);
                         if constexpr (PAIRED) {
                             *(uint4*)(row + e0) = make_uint4(q8_pack4(a[0], b[0], a[1], b[1]), q8_pack4(a[2], b[2], a[3], b[3]),
                                                              q8_pack4(a[4], b[4], a[5], b[5]), q8_pack4(a[6], b[6], a[7], b[7]));

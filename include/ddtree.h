@@ -498,7 +498,8 @@ typedef struct {
  *              outside all runs, the padding of a fixed shape, are not looked at).
  *   at         int32 [B].
  *   rot, norm  the rotation (for the token's position) and norm of keys and queries,
- *              either NULL to leave it out; rot_dim a multiple of 16.
+ *              either NULL to leave it out; rot_dim a multiple of 16.  (Squares in 32 bits, as
+ *              in ddtree_norm_rope: elements up to about 2^60.)
  *   q, q_out   the tokens' queries, normed and rotated in 16 bits, as in ddtree_rope
  *              (q_out is q's own tensor or overlaps no input); both NULL to leave them
  *              out.  Rows of tokens outside all runs stay as they are.
