@@ -1,7 +1,8 @@
 // q8.cuh -- the 8-bit cache's format: e4m3 codes under a power of two for each block of
 // positions of a page and head, and where a run's blocks lie.
 //
-// A code c stands for c * 2^e.  The exponent of a block is the least e at which its
+// A code c stands for c * 2^e, also the two that e4m3 itself has for no number: 480 and -480, as
+// their bits say.  The exponent of a block is the least e at which its
 // largest element is at most 448 * 2^e (448 = 1.75 * 2^8 is the largest code), so that its
 // significand is found by a power of two alone: x * 2^-e is exact, the one rounding is to
 // the code, and c * 2^e is exact in bf16 always and in fp16 from e = -15 (the smallest
@@ -57,6 +58,10 @@ DDT_DEV uint32_t q8_moved(uint32_t w, float factor) {
 // numbers as they are.)  Four instructions a pair: a byte permute puts a code under a
 // byte of its sign bit eight times, a shift brings both to their places, a mask
 // takes the sign bits between them away.
+// All 256 codes are numbers here, 0x7F and 0xFF +-480 as their bits say.  (fp16 has a conversion
+// of pairs of codes, which takes those two for NaN and forgets their signs; it left the product
+// alone to do: tree attention over fp16 then took 2.86 ms for 2.99 (70B-class long context) and
+// 490 us for 533 (ragged serving).)
 //
 // What that product takes for a block's scale byte, as the type's bits.
 template <bool F16>
@@ -78,31 +83,11 @@ template <bool F16>
 DDT_DEV uint32_t widen_even(uint32_t w, uint32_t factors) { return widen<F16, 0xa280>(w, factors); }
 template <bool F16>
 DDT_DEV uint32_t widen_odd(uint32_t w, uint32_t factors) { return widen<F16, 0xb391>(w, factors); }
-
-// Codes 0, 1 and codes 2, 3 of a word as pairs in their order.  fp16 has a conversion of such
-// pairs, which leaves the product with the scale alone: in tree attention's widening warps,
-// which share their scheduler with the softmax, 2.88 ms for 2.99 (70B-class long context),
-// 500 us for 534 (ragged serving), though 22.9 for 22.4 (7 small trees).
-//
-// What their product takes for a block's scale byte.
+// Codes 0, 1 and codes 2, 3 of a word as pairs in their order.
 template <bool F16>
-DDT_DEV uint32_t pair_factor(uint32_t byte) {
-    if constexpr (!F16) return widen_factor<F16>(byte);
-    const int e = q8_from_byte(byte, q8_least(F16));
-    return e > -15 ? (uint32_t)(15 + e) << 10 : 0x200u;
-}
-template <bool F16, bool HI>
-DDT_DEV uint32_t widen_pair(uint32_t w, uint32_t factors) {
-    if constexpr (!F16) return widen<F16, HI ? 0xb3a2u : 0x9180u>(w, factors);
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(HI ? w >> 16 : w)));
-    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(factors));
-    return r;
-}
+DDT_DEV uint32_t widen_lo(uint32_t w, uint32_t factors) { return widen<F16, 0x9180>(w, factors); }
 template <bool F16>
-DDT_DEV uint32_t widen_lo(uint32_t w, uint32_t factors) { return widen_pair<F16, false>(w, factors); }
-template <bool F16>
-DDT_DEV uint32_t widen_hi(uint32_t w, uint32_t factors) { return widen_pair<F16, true>(w, factors); }
+DDT_DEV uint32_t widen_hi(uint32_t w, uint32_t factors) { return widen<F16, 0xb3a2>(w, factors); }
 
 // A run's tokens first[b] .. first[b + 1] - 1 become positions at[b] .. of sequence b.  Whether
 // it is one that no call may carry out: outside the T tokens or the table's positions.

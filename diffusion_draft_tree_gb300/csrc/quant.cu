@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
                 const RowsArg& out = is_v ? p.v_out : p.k_out;
                 uint16_t* row = (uint16_t*)out.data + (int64_t)(x.token + r - r_lo) * out.ts +
                                 (is_v ? t - c.Hkv : t) * out.hs + (i & (CH - 1)) * 16;
-                const uint32_t m = pair_factor<F16>(f[k]) * 0x10001u;
+                const uint32_t m = widen_factor<F16>(f[k]) * 0x10001u;
                 *(uint4*)row = make_uint4(widen_lo<F16>(w[k].x, m), widen_hi<F16>(w[k].x, m),
                                           widen_lo<F16>(w[k].y, m), widen_hi<F16>(w[k].y, m));
                 *(uint4*)(row + 8) = make_uint4(widen_lo<F16>(w[k].z, m), widen_hi<F16>(w[k].z, m),

@@ -586,7 +586,7 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
 // through shared memory, 2560 cycles at 128 bytes each: 192 KB of operands, 32 in as
 // codes, 32 out and 64 in as it is widened.  Neither is reached: the long context takes
 // about 3300 a tile at 1.9 GHz, the 16-bit cache 2950.  70B-class long context (4 trees of
-// 257 nodes behind 128K) 2.99 to 3.04 ms in bf16, 2.88 in fp16, where the 16-bit cache takes
+// 257 nodes behind 128K) 2.99 to 3.07 ms in bf16 and fp16, where the 16-bit cache takes
 // 2.67 to 2.76; without the widening 2.58.  Queries in two e4m3 parts against the codes themselves: 3.46.
 // A thread's share of a tile of codes [128 keys][D]: 16 codes of rows of one group of eight,
 // which are under one scale.  (Shared memory is what these warps wait for: with a
@@ -990,7 +990,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
                     }
                     if (!(lane & 1))
-                        s_mult[ring][lane / 2] = (uint16_t)pair_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
+                        s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
                     ++c;
@@ -1430,8 +1430,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tmem_st_wait();
             l += sum;
-            // (bf16 rows of an 8-bit cache are numbers, whatever their codes)
-            if (k == 0 && quarter * 32 + 32 > lim_t && (!Q8 || F16 || is_tree)) {  // (the warp as a whole)
+            // (rows of an 8-bit cache are numbers, whatever their codes)
+            if (k == 0 && quarter * 32 + 32 > lim_t && (!Q8 || is_tree)) {  // (the warp as a whole)
                 // key r of this tile is past the sequence: zero its V row so that
                 // uninitialised cache memory (possibly NaN) cannot reach O.
                 if (!mbar_wait_warp(&bar_vfull[s], (j / NS) & 1, &s_abort)) { fail(); ok = false; break; }

@@ -476,8 +476,8 @@ ddtree_status ddtree_norm_rope(const ddtree_rows* q, const ddtree_rows* q_out,
  * Scales: the writers choose x - 127 as the least e at which the block's largest
  * element is at most 448 * 2^e, from -96 (bf16 tokens) or -15 (fp16) to 7; elements beyond
  * 448 * 2^7 become that.  A byte outside this range counts as the range's nearer end.
- * Codes 0x7F and 0xFF are no numbers: no writer makes them of finite elements, and none may
- * stand at a position that a call reads (its results for that head are undefined then).
+ * Codes 0x7F and 0xFF, which e4m3 has for NaN, stand for 480 and -480 times the scale in every
+ * call; no writer makes them of finite elements.
  * D in {64, 128}; page_size a power of two of at least 8; block a power of two, 8 to
  * min(page_size, DDTREE_MAX_Q8_BLOCK); max_pages * page_size at most 2^30. */
 typedef struct {

@@ -5,6 +5,7 @@ import torch
 
 from diffusion_draft_tree_gb300 import ops
 from tests import q8_util as qu
+from tests.test_gpu_q8 import attn_case, check
 
 pytestmark = pytest.mark.gpu
 BF16, FP16 = torch.bfloat16, torch.float16
@@ -41,3 +42,52 @@ def test_append_under_a_norm_of_any_eps(cuda_device, dtype, size, eps, rows):
     off = ref.abs() * qu.norm_off(64)
     qu.check_16(q, ref, off, dtype, "queries")
     qu.check_written(before[0], after[0], None, cache.page_table.cpu(), 32, 32, dtype, [(0, 0, ref.cpu(), off.cpu())])
+
+
+def _with_nan_codes(args, share):
+    """Some of the live codes 0x7F and 0xFF."""
+    cache, plen = args[1], args[4]
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    page, live = cache.page_size, torch.zeros(cache.num_pages, cache.page_size, dtype=torch.bool, device="cuda")
+    for b, P in enumerate(plen.tolist()):
+        pos = torch.arange(P, device="cuda")
+        live[cache.page_table[b].long()[pos // page], pos % page] = True
+    for codes in (raw(cache.k_pages), raw(cache.v_pages)):
+        hit = (torch.rand(codes.shape, generator=gen, device="cuda") < share) & live[:, None, :, None]
+        sign = torch.randint(0, 2, codes.shape, generator=gen, device="cuda", dtype=torch.uint8)
+        codes.copy_(torch.where(hit, 0x7F + 0x80 * sign, codes))
+    assert bool((raw(cache.k_pages)[live[:, None].expand(-1, cache.Hkv, -1)] == 0xFF).any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("lens,N,Hq,Hkv,D,page,block", [
+    ([300, 45], 0, 4, 1, 128, 16, 16), ([500, 7], 3, 8, 2, 64, 64, 32), ([300, 1000], 40, 4, 2, 128, 32, 8),
+    ([700], 64, 8, 2, 64, 16, 16), ([260] * 20, 64, 32, 8, 128, 64, 64), ([200] * 24, 70, 32, 8, 64, 128, 32)])
+def test_the_codes_of_no_number_are_480_in_every_form(cuda_device, dtype, lens, N, Hq, Hkv, D, page, block):
+    args = attn_case(torch.Generator().manual_seed(N + D), lens, N, Hq, Hkv, D, page, block, dtype, spread=0.5)
+    _with_nan_codes(args, 0.02)
+    cache = args[1]
+    check(args, scale=0.03)
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    k, v = (torch.empty(starts[-1], Hkv, D, dtype=dtype, device="cuda") for _ in range(2))
+    ops.ddtree_read_q8(cache, ints(starts), ints([0] * len(lens)), k, v)
+    ops.ddtree_device_check()
+    for got, codes, scales in ((k, cache.k_pages, cache.k_scales), (v, cache.v_pages, cache.v_scales)):
+        val = qu.values64(codes, scales, dtype)
+        for b, n in enumerate(lens):
+            pos = torch.arange(n, device="cuda")
+            assert torch.equal(got[starts[b]:starts[b + 1]].double(), val[cache.page_table[b].long()[pos // page], :, pos % page])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_the_codes_of_no_number_move_with_their_block(cuda_device, dtype):
+    cache = ops.QuantCache.empty(1, 1, 16, 64, ints([[0]]), block=16, dtype=dtype)
+    for c, s in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+        raw(c)[0, 0, 0], raw(c)[0, 0, 1] = 0x7F, 0xFF
+        s.fill_(127)
+    k = torch.full((1, 1, 64), 448.0 * 4, dtype=dtype, device="cuda")
+    ops.ddtree_append_q8(k, k.clone(), ints([0, 1]), ints([2]), cache)
+    ops.ddtree_device_check()
+    for c, s in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+        assert s.item() == 129
+        assert bool((c[0, 0, 0].float() == 120).all()) and bool((c[0, 0, 1].float() == -120).all())
