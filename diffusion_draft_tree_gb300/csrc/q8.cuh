@@ -22,6 +22,12 @@ namespace {
 constexpr int kQ8Most = 7;
 __host__ __device__ constexpr int q8_least(bool f16) { return f16 ? -15 : -96; }
 
+// The largest of three numbers, NaN if one of them is.
+DDT_DEV float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 DDT_DEV float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
 // The exponent of a block whose largest element is amax >= 0.
 DDT_DEV int q8_exponent(float amax, int least) {

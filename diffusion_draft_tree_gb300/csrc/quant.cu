@@ -10,8 +10,9 @@
 // two, the next head's loads in flight meanwhile.  A head is one warp's where its rows fit
 // the passes that a whole block takes the CTA (a decoding step's single row always does),
 // so that warps go on without each other, and the CTA's otherwise, which then meets
-// once a head.  18.2K tokens of ragged prompts, normed and turned: 89 us, 68 % of the measured
-// HBM rate; one token each of 16 sequences 3.2 us, a launch.
+// once a head.  18.2K tokens of ragged prompts, normed and turned: 91 us, 67 % of the measured
+// HBM rate; one token each of 16 sequences 3.2 us, a launch.  A NaN is found by the maxima (89.5 us
+// without that) and recorded.
 #include <type_traits>
 
 #include "q8.cuh"
@@ -216,8 +217,8 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                 if constexpr (kind > 0) {
                     float m = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(ya[i][e]), fabsf(yb[i][e])));
-                    most = fmaxf(most, m);
+                    for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(ya[i][e]), fabsf(yb[i][e]));
+                    most = max_nan(most, m, m);
                 }
             }
             if constexpr (kind == 0) {
@@ -231,7 +232,15 @@ __global__ void __launch_bounds__(32 * kWarps, (kPasses == 2 ? 16 : 24) / kWarps
                         *(Vt*)(row + e1) = b;
                     }
             } else {
-                most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (not negative)
+                uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));  // (not negative; NaN is above inf)
+                if (bits > 0x7f800000u) {  // (rare) a NaN, which the scale goes without
+                    if (lane == 0) record_error(p.err, (COMMIT ? ERR_COMMIT : ERR_APPEND) | ERR_BAD_INPUT);
+                    most = 0.f;
+                    for (int i = 0; i < kPasses; ++i)
+                        for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(ya[i][e]), fabsf(yb[i][e])));
+                    bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+                }
+                most = __uint_as_float(bits);
                 if (whole) {
                     if (lane == 0) s_max[turn][warp] = most;
                     __syncthreads();  // (and every thread has read the old scale)

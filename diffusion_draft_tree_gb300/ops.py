@@ -647,7 +647,7 @@ def ddtree_append_q8(k, v, first, at, cache: QuantCache, rotary: Optional[Rotary
     """Quantises runs of tokens into the cache: tokens first[b] .. first[b + 1] - 1 (first int32
     [B + 1]) become positions at[b].. (int32 [B]) of sequence b, k normed and rotated on the
     way if a norm and a rotary are given, and their queries q likewise, in place unless
-    q_out is given."""
+    q_out is given.  A NaN among keys or values is recorded for ddtree_device_check."""
     turns, where = (None, None) if rotary is None else (rotary._c, rotary._index)
     st = _ddtree.append_q8(cache._c, cache._index, cache.B, k, v, first, at, turns, where,
                            *(_NO_NORM if norm is None else norm._c), q, q_out,

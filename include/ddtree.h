@@ -477,7 +477,8 @@ ddtree_status ddtree_norm_rope(const ddtree_rows* q, const ddtree_rows* q_out,
  * element is at most 448 * 2^e, from -96 (bf16 tokens) or -15 (fp16) to 7; elements beyond
  * 448 * 2^7 become that.  A byte outside this range counts as the range's nearer end.
  * Codes 0x7F and 0xFF, which e4m3 has for NaN, stand for 480 and -480 times the scale in every
- * call; no writer makes them of finite elements.
+ * call; the writers make 0x7F of a NaN alone, which they record (as bad input), and choose the
+ * scale without it.
  * D in {64, 128}; page_size a power of two of at least 8; block a power of two, 8 to
  * min(page_size, DDTREE_MAX_Q8_BLOCK); max_pages * page_size at most 2^30. */
 typedef struct {
@@ -512,7 +513,8 @@ typedef struct {
  * A run whose tokens lie outside 0..T or whose positions lie outside the table is
  * left out, queries too, and recorded; where first descends, which is recorded, other runs
  * may be left out as well.  So is the part of a run whose page lies outside the pool
- * (its queries are still written).  The pages written belong to one sequence
+ * (its queries are still written).  A key or value that is NaN, or becomes it by the norm,
+ * is recorded as bad input, its row still written.  The pages written belong to one sequence
  * alone.  The caller's lengths are not changed.  T = 0 does nothing.  Every pointer
  * 16-byte aligned, strides of rows multiples of 8 elements.  No workspace. */
 ddtree_status ddtree_append_q8(const ddtree_rows* k, const ddtree_rows* v, int T,

@@ -91,3 +91,72 @@ def test_the_codes_of_no_number_move_with_their_block(cuda_device, dtype):
     for c, s in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
         assert s.item() == 129
         assert bool((c[0, 0, 0].float() == 120).all()) and bool((c[0, 0, 1].float() == -120).all())
+
+
+def _recorded():
+    with pytest.raises(ops.DDTreeError) as e:
+        ops.ddtree_device_check()
+    return e.value.detail
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("at,n,block,D", [(0, 1, 16, 64), (5, 3, 16, 128), (0, 40, 32, 64), (3, 130, 64, 128)])
+@pytest.mark.parametrize("half", [0, 1])
+def test_a_nan_among_keys_or_values_is_recorded(cuda_device, dtype, at, n, block, D, half):
+    """... and everything but its own code is what it is with a zero there."""
+    gen = torch.Generator().manual_seed(n)
+    new = lambda: ops.QuantCache.empty(4, 2, 64, D, ints([[3, 1, 2]]), block=block, dtype=dtype)  # noqa: E731
+    kv = [torch.randn(n, 2, D, generator=gen).to(dtype).cuda() for _ in range(2)]
+    hit = (n - 1, 1, 7)
+    kv[half][hit] = 0
+    clean, dirty = new(), new()
+    ops.ddtree_append_q8(*kv, ints([0, n]), ints([at]), clean)
+    ops.ddtree_device_check()
+    for bad in (float("nan"), -float("nan")):
+        kv[half][hit] = bad
+        ops.ddtree_append_q8(*kv, ints([0, n]), ints([at]), dirty)
+        assert _recorded() == 0x06000005
+    pos = at + n - 1
+    for i, (a, b) in enumerate(zip(snap(clean), snap(dirty))):
+        got, want = raw(b[0]).clone(), raw(a[0])
+        if i == half:
+            one = (int(clean.page_table[0, pos // 64]), 1, pos % 64, 7)
+            assert int(got[one]) & 0x7F == 0x7F
+            got[one] = want[one]
+        assert torch.equal(got, want) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_norm_that_makes_no_number_is_recorded(cuda_device, dtype):
+    k = torch.randn(3, 1, 64).to(dtype).cuda()
+    cache = ops.QuantCache.empty(1, 1, 16, 64, ints([[0]]), block=16, dtype=dtype)
+    ops.ddtree_append_q8(k, k, ints([0, 3]), ints([0]), cache, norm=ops.HeadNorm())
+    ops.ddtree_device_check()
+    k[1, 0, 0] = float("inf")
+    ops.ddtree_append_q8(k, torch.zeros_like(k), ints([0, 3]), ints([0]), cache, norm=ops.HeadNorm())
+    assert _recorded() == 0x06000005
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_nan_on_an_accepted_path_is_recorded(cuda_device, dtype):
+    kt, vt = (torch.randn(2, 5, 2, 64).to(dtype).cuda() for _ in range(2))
+    args = (ints([2, 1]), ints([[1, 3], [2, -1]]), ints([4, 15]))
+    cache = ops.QuantCache.empty(4, 2, 16, 64, ints([[0, 1], [2, 3]]), block=8, dtype=dtype)
+    kt[0, 2], vt[1, 4] = float("nan"), float("nan")  # not accepted
+    ops.ddtree_commit_q8(cache, kt, vt, *args)
+    ops.ddtree_device_check()
+    vt[1, 2, 1, 5] = float("nan")
+    ops.ddtree_commit_q8(cache, kt, vt, *args)
+    assert _recorded() == 0x05000005
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_infinities_are_the_largest_code_of_the_largest_scale(cuda_device, dtype):
+    cache = ops.QuantCache.empty(1, 1, 16, 64, ints([[0]]), block=16, dtype=dtype)
+    k = torch.ones(2, 1, 64).to(dtype).cuda()
+    k[1, 0, :2] = torch.tensor([float("inf"), -float("inf")])
+    ops.ddtree_append_q8(k, k.clone(), ints([0, 2]), ints([0]), cache)
+    ops.ddtree_device_check()
+    out, _ = (torch.empty_like(k) for _ in range(2))
+    ops.ddtree_read_q8(cache, ints([0, 2]), ints([0]), out, _)
+    assert out[1, 0, :2].tolist() == [57344.0, -57344.0]
