@@ -108,21 +108,33 @@ struct RunBlock {
 };
 // Runs cover their blocks by slots: sequence b has slots first[b] / S + 2 b and up, two more
 // than its tokens fill, as n tokens touch at most (n - 2) / S + 2 blocks.  The slots'
-// starts are known without adding up the runs before, so a CTA finds its own by halving.
+// starts are known without adding up the runs before, so a CTA finds its own by halving.  Where
+// `first` descends the starts do too, and halving may miss some of a run's slots: the starts it
+// meets on its way to a run are the same from every slot, so each CTA of the run sees from
+// them whether all of its slots get here, and none takes it up otherwise.
 DDT_DEV RunBlock run_block(const int32_t* first, const int32_t* at, int B, int T, int block_log2, int64_t cap,
-                           int64_t slot) {
+                           int slot) {
     const int S = 1 << block_log2;
     int lo = 0, hi = B - 1;  // the last sequence whose slots start at or before this one
+    auto start_of = [&](int f, int b) { return (min(f, T) >> block_log2) + 2 * b; };  // (at most run_slots)
+    int before = INT32_MIN, after = INT32_MAX;  // starts met on the way: the last and the first
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)(first[mid] >> block_log2) + 2 * (int64_t)mid <= slot) lo = mid;
-        else hi = mid - 1;
+        const int start = start_of(first[mid], mid);
+        const bool here = start <= slot;
+        lo = here ? mid : lo;
+        hi = here ? hi : mid - 1;
+        before = max(before, here ? start : INT32_MIN);
+        after = min(after, here ? INT32_MAX : start);
     }
     RunBlock x{};
     x.b = lo;
     const int f = first[lo], n = first[lo + 1] - f, p = at[lo];
-    const int64_t j = slot - ((int64_t)(f >> block_log2) + 2 * (int64_t)lo);
+    const int start = start_of(f, lo);
+    const int64_t j = (int64_t)slot - start;
     if (j < 0 || n == 0 || run_bad(f, n, p, T, cap)) return x;
+    const int last = ((p + n - 1) >> block_log2) - (p >> block_log2);  // its last slot
+    if (before > start || (int64_t)start + last >= after) return x;
     x.p0 = (int)min((int64_t)(p & -S) + j * S, (int64_t)INT32_MAX - S);
     x.lo = max(x.p0, p);
     x.hi = min(x.p0 + S, p + n);

@@ -512,7 +512,7 @@ typedef struct {
  * the nearest, ties to even.
  * A run whose tokens lie outside 0..T or whose positions lie outside the table is
  * left out, queries too, and recorded; where first descends, which is recorded, other runs
- * may be left out as well.  So is the part of a run whose page lies outside the pool
+ * may be left out as well, each as a whole.  So is the part of a run whose page lies outside the pool
  * (its queries are still written).  A key or value that is NaN, or becomes it by the norm,
  * is recorded as bad input, its row still written.  The pages written belong to one sequence
  * alone.  The caller's lengths are not changed.  T = 0 does nothing.  Every pointer

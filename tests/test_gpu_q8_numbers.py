@@ -160,3 +160,44 @@ def test_infinities_are_the_largest_code_of_the_largest_scale(cuda_device, dtype
     out, _ = (torch.empty_like(k) for _ in range(2))
     ops.ddtree_read_q8(cache, ints([0, 2]), ints([0]), out, _)
     assert out[1, 0, :2].tolist() == [57344.0, -57344.0]
+
+
+@pytest.mark.parametrize("first", [[0, 100, 50, 150], [0, 90, 20, 150, 150], [100, 40, 120, 10, 150], [0, 150, 0, 150, 3, 140],
+                                   [0, 20, 120, 60, 61, 62, 63, 150], [140, 100, 60, 20, 150]])
+@pytest.mark.parametrize("at0", [0, 13])
+def test_where_first_descends_a_run_is_carried_out_as_a_whole_or_not_at_all(cuda_device, first, at0):
+    B, T, S, D = len(first) - 1, 150, 16, 64
+    table = torch.randperm(B * 3, generator=torch.Generator().manual_seed(B)).view(B, 3).tolist()
+    cache = ops.QuantCache.empty(3 * B, 1, 64, D, ints(table), block=S)
+    k = torch.ones(T, 1, D, dtype=BF16, device="cuda")
+    q = torch.full((T, 2, D), 2.0, dtype=BF16, device="cuda")
+    at = [at0 + b for b in range(B)]
+    calls = []
+    for b in range(B):  # (queries of a run show in rows that runs may share: one sequence's q at a time)
+        f = [first[b], first[b + 1]]
+        calls.append(f[0] <= f[1])
+    q_out = torch.zeros_like(q)
+    ops.ddtree_append_q8(k, k.clone(), ints(first), ints(at), cache, q=q, q_out=q_out)
+    assert _recorded() == 0x06000005
+    carried = []
+    for b, good in enumerate(calls):
+        n = first[b + 1] - first[b]
+        pos = torch.arange(192, device="cuda")
+        codes = raw(cache.k_pages)[ints(table)[b].long()[pos // 64], 0, pos % 64]
+        wrote = (codes != 0).any(-1)
+        if good and bool(wrote.any()):
+            assert wrote.nonzero().flatten().tolist() == list(range(at[b], at[b] + n))
+            assert bool((q_out[first[b]:first[b + 1]] == 2).all())
+            carried.append(b)
+        else:
+            assert not bool(wrote.any())
+    rows = set()
+    for b in carried:
+        rows |= set(range(first[b], first[b + 1]))
+    assert (q_out == 2).all(-1).all(-1).nonzero().flatten().tolist() == sorted(rows)
+    out = [torch.zeros_like(k) for _ in range(2)]
+    for c in (cache.k_pages, cache.v_pages):
+        raw(c).fill_(0x38)
+    ops.ddtree_read_q8(cache, ints(first), ints(at), *out)
+    assert _recorded() == 0x07000005
+    assert (out[0] != 0).all(-1).all(-1).nonzero().flatten().tolist() == sorted(rows)
