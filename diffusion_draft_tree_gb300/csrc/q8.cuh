@@ -95,6 +95,31 @@ DDT_DEV uint32_t widen_lo(uint32_t w, uint32_t factors) { return widen<F16, 0x91
 template <bool F16>
 DDT_DEV uint32_t widen_hi(uint32_t w, uint32_t factors) { return widen<F16, 0xb3a2>(w, factors); }
 
+// Attention's copy warps hold a box of positions (a page, or as much of it as a key tile takes) a
+// lane: its page number and the up to 16 bytes of its scales, a power of two of them.  `from`:
+// the scale of the box's first position.
+DDT_DEV uint4 box_scales(const uint8_t* from, int per_box) {
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (per_box == 1) y.x = __ldg(from);
+    else if (per_box == 2) y.x = __ldg((const uint16_t*)from);
+    else if (per_box == 4) y.x = __ldg((const uint32_t*)from);
+    else if (per_box == 8) *(uint2*)&y = __ldg((const uint2*)from);
+    else y = __ldg((const uint4*)from);
+    return y;
+}
+// The scale byte of keys 4 l .. 4 l + 3 of a tile for lane l (a block is 8 keys or more), the tile's
+// boxes held by the lanes from `first` on; warp-collective.
+DDT_DEV uint32_t tile_scale(const uint4& y, int first, int box_log2, int block_log2, int per_box, int lane) {
+    const int src = (first + (4 * lane >> box_log2)) & 31, byte = (4 * lane & ((1 << box_log2) - 1)) >> block_log2;
+    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
+    if (per_box > 4) {
+        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
+                       w3 = __shfl_sync(0xffffffffu, y.w, src);
+        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
+    }
+    return (word >> (8 * (byte & 3))) & 0xffu;
+}
+
 // A run's tokens first[b] .. first[b + 1] - 1 become positions at[b] .. of sequence b.  Whether
 // it is one that no call may carry out: outside the T tokens or the table's positions.
 DDT_DEV bool run_bad(int f, int n, int p, int T, int64_t cap) {

@@ -456,7 +456,10 @@ __device__ __noinline__ void left_rows(const LeftArgs& a) {
             }
         }
         const float b0 = m0 == -INFINITY ? 0.f : m0 - kLift<F16>, b1 = m1 == -INFINITY ? 0.f : m1 - kLift<F16>;
-        uint32_t pw[8];  // rounded to the cache's type and turned: keys by twos of row lane / 4
+        // Rounded to the cache's type, as the tensor core takes both factors of a product in one
+        // (half a step a weight, independent ones, where the output is rounded once more at the end),
+        // and turned: keys by twos of row lane / 4.
+        uint32_t pw[8];
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb) {
             const float e0 = fast_exp2(x[kb >> 1][2 * (kb & 1)] - b0), e1 = fast_exp2(x[kb >> 1][2 * (kb & 1) + 1] - b1);
@@ -635,7 +638,9 @@ DDT_DEV void widen_codes(const Codes<D>& x, uint8_t* tile, int i) {
 
 // One CTA = one (sequence b, KV head g, pair of 128-row query tiles, KV split).
 // Warp 0: TMA producer.  Warp 1: TMEM owner and MMA issuer.  Warps 2-5: softmax
-// of query tile 0; warps 6-9: softmax of query tile 1.  Per KV tile j the
+// of query tile 0; warps 6-9: softmax of query tile 1; warps 10 and 11, where there are any:
+// the rows left over.  Over an 8-bit cache warps 2 and 3 take the rows left over (without any
+// they idle), 4-7 and 8-11 are the softmax groups, and 12-15 widen codes.  Per KV tile j the
 // tensor core runs S_k = Q_k K_j^T into TMEM columns [128k, 128k+128); softmax
 // group k reads S_k, writes P_k (bf16) over the first 64 of those columns, and
 // the tensor core runs O_k += P_k V_j with P_k read straight from TMEM.  While
@@ -937,16 +942,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // their use: page numbers two ahead.
             const int box_log2 = 31 - __clz(box), per_box = 1 << max(0, box_log2 - p.block_log2);
             auto scales_of = [&](int page, int k, const uint8_t* from) {
-                uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                if (page == num_pages) return y;
+                if (page == num_pages) return make_uint4(0u, 0u, 0u, 0u);
                 const int slot = (t_begin * BN + (k * 32 + lane) * box) & (ps - 1);
-                const uint8_t* at = from + ((((int64_t)page * p.Hkv + g) << p.per_page_log2) + (slot >> p.block_log2));
-                if (per_box == 1) y.x = __ldg(at);
-                else if (per_box == 2) y.x = __ldg((const uint16_t*)at);
-                else if (per_box == 4) y.x = __ldg((const uint32_t*)at);
-                else if (per_box == 8) *(uint2*)&y = __ldg((const uint2*)at);
-                else y = __ldg((const uint4*)at);
-                return y;
+                return box_scales(from + ((((int64_t)page * p.Hkv + g) << p.per_page_log2) + (slot >> p.block_log2)), per_box);
             };
             int id1 = checked(next_ids, 1);
             next_ids = ids_of(2);
@@ -971,7 +969,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ok = mbar_wait_warp(&bar_rempty[ring], turn ^ 1, &s_abort);
                     if (!ok) break;
                     const int mine = v ? ids_v : ids;
-                    const uint4 y = v ? v_now : k0;
                     const uint32_t to = smem_u32(raw_at(ring));
                     const int key0 = (t_begin + j) * BN;
 #pragma unroll 4
@@ -981,16 +978,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                          (key0 + x * box) & (ps - 1), g, page);
                     }
                     // (the copies are on their way while the scales still are)
-                    // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
-                    const int src = (j * nb + (4 * lane >> box_log2)) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
-                    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
-                    if (per_box > 4) {
-                        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
-                                       w3 = __shfl_sync(0xffffffffu, y.w, src);
-                        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
-                    }
-                    if (!(lane & 1))
-                        s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu);
+                    const uint32_t x = tile_scale(v ? v_now : k0, j * nb, box_log2, p.block_log2, per_box, lane);
+                    if (!(lane & 1)) s_mult[ring][lane / 2] = (uint16_t)widen_factor<F16>(x);
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[ring], Raw::BYTES);
                     ++c;

@@ -124,16 +124,9 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
             return p.num_pages;
         };
         auto scales_of = [&](int page, const Batch& y, const uint8_t* from) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (page == p.num_pages) return v;
+            if (page == p.num_pages) return make_uint4(0u, 0u, 0u, 0u);
             const int slot = (int)((((int64_t)y.k * 32 + lane) * box) & (ps - 1));
-            const uint8_t* f = from + ((((int64_t)page * p.Hkv + y.x.g) << p.per_page_log2) + (slot >> p.block_log2));
-            if (per_box == 1) v.x = __ldg(f);
-            else if (per_box == 2) v.x = __ldg((const uint16_t*)f);
-            else if (per_box == 4) v.x = __ldg((const uint32_t*)f);
-            else if (per_box == 8) *(uint2*)&v = __ldg((const uint2*)f);
-            else v = __ldg((const uint4*)f);
-            return v;
+            return box_scales(from + ((((int64_t)page * p.Hkv + y.x.g) << p.per_page_log2) + (slot >> p.block_log2)), per_box);
         };
         auto advance = [&](Batch& y) {
             if (y.left <= 0) return;
@@ -190,18 +183,10 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
                 }
             }
             if (!tree) {  // (the copies are on their way while the scales still are)
-                // the factors of keys 4 l .. 4 l + 3 (a block is 8 keys or more)
-                const int src = (at.tile * nb + (4 * lane >> box_log2)) & 31, byte = (4 * lane & (box - 1)) >> p.block_log2;
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    const uint4 y = v ? vs : ks;
-                    uint32_t word = __shfl_sync(0xffffffffu, y.x, src);
-                    if (per_box > 4) {
-                        const uint32_t w1 = __shfl_sync(0xffffffffu, y.y, src), w2 = __shfl_sync(0xffffffffu, y.z, src),
-                                       w3 = __shfl_sync(0xffffffffu, y.w, src);
-                        word = byte < 4 ? word : byte < 8 ? w1 : byte < 12 ? w2 : w3;
-                    }
-                    const uint32_t m = widen_factor<F16>((word >> (8 * (byte & 3))) & 0xffu) * 0x10001u;
+                    const uint32_t m = widen_factor<F16>(tile_scale(v ? vs : ks, at.tile * nb, box_log2, p.block_log2,
+                                                                    per_box, lane)) * 0x10001u;
                     *(uint2*)&s_mult[s][v][4 * lane] = make_uint2(m, m);
                 }
             }
@@ -255,7 +240,8 @@ tree_attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid
 
         // The weights of KG groups of 16 keys from their scores, the maxima and sums; keys
         // 16 kg + gl (+ 8: [2], [3]) of rows 2 cl, 2 cl + 1.  pw: the right operand, two
-        // words a group.
+        // words a group: weights rounded to the tokens' type, as a product takes both factors in
+        // one (half a step a weight, independent ones; the output is rounded once more at the end).
         auto weigh = [&](auto& x, auto& pw) {
             constexpr int KG = sizeof(x[0]) / sizeof(x[0][0]);
 #pragma unroll
