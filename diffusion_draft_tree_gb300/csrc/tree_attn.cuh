@@ -2003,7 +2003,11 @@ Plan plan_few(const Plan& base, Tiles t, long units, int sms, Active active) {
 // four times the least and every cluster size that is resident at once is
 // scored, in microseconds measured on GB300 (D = 128): a key tile takes a pair
 // of query tiles 1.5, a single one 1.2; an exchange 1 and 0.035 a row.  (D = 64, whose
-// rows are half as long, goes by the same figures.)
+// rows are half as long, goes by the same figures.  So does an 8-bit cache, whose key
+// tiles take longer: all plans of six shapes timed -- 8 KV heads, G = 4, a tree of 65 nodes
+// behind 2K (15.2 us; the next best plan 16.2) and four behind 4K (42.8; 55.8), 257 behind 8K
+// (54.7; 59.0), 33 behind 32K (52.1; 55.6), G = 8, two of 129 behind 1K (22.6; 28.1), 4 KV heads,
+// G = 7, D = 64, seven of 22 (17.3; 18.7) -- the one taken was the fastest of each.)
 struct PagedPlan : Plan {
     int npt, single;
 };
@@ -2044,17 +2048,20 @@ PagedPlan plan_paged_few(int B, int N, int G, int Hkv, Tiles t, int sms, Active 
 // sequences (80 units taken along, of 152 SMs) 26 / 35, 59 / 88, 120 / 149, 173 / 176, 220 / 214;
 // 12 (96 units) at 65, 95 and 126 tiles 157 / 171, 212 / 179, 266 / 251; 14 (112 units) at 33 and
 // 65 tiles 105 / 90, 180 / 175.
+// Over an 8-bit cache the rows are always taken along: a lone tile waits for its widening,
+// a pair has two softmax groups to fill the time.  The same lists, 10 sequences
+// 43 / 35, 118 / 101, 184 / 191, 247 / 200, 305 / 278; D = 64 at 9, 33, 65 tiles 35 / 24, 93 / 65, 143 / 129.
 constexpr int kLoneTiles = 80;
 struct ManyPlan : Plan {
     int left;
 };
-ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms) {
+ManyPlan plan_paged_many(int B, int N, int Hq, int Hkv, Tiles t, int sms, bool q8 = false) {
     ManyPlan pl{};
     (Plan&)pl = plan_base(N, Hq, Hkv);
     const int G = Hq / Hkv, left = (N + 1 - (pl.mtiles - 1) * (BM / G)) * G;
     if (plan_units(pl, B, Hkv) < sms) return pl;  // few units (smax = 0)
     const long along = (long)B * Hkv * (pl.mpairs - 1);  // units if the pairs take them
-    const bool short_wave = pl.mpairs == 2 && along * 10 < sms * 7L && t.prefix + t.tree <= kLoneTiles;
+    const bool short_wave = !q8 && pl.mpairs == 2 && along * 10 < sms * 7L && t.prefix + t.tree <= kLoneTiles;
     if (pl.mtiles > 1 && pl.mtiles % 2 && left <= kLeftRows && !short_wave) {
         --pl.mtiles;
         --pl.mpairs;

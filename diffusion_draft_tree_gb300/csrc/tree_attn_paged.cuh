@@ -26,7 +26,7 @@ cudaError_t launch_mode(const Args& a, cudaStream_t s) {
     const int G = Hq / Hkv, R = a.N + 1;
     const Tiles t = max_tiles(a.N, cap);
     const int sms = num_sms();
-    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms);
+    const ManyPlan many = plan_paged_many(a.B, a.N, Hq, Hkv, t, sms, is_q8(MODE));
     PagedPlan pl{};
     if (many.smax) {
         (Plan&)pl = many;

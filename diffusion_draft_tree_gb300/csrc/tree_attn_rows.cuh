@@ -15,7 +15,11 @@ constexpr int kWarps = 4;       // computing warps
 constexpr int kThreadsR = 32 * (kWarps + 1);
 constexpr int kMaxSeqs = 1024;  // sequences whose tile counts a CTA adds up
 // A batch of at most kSmallRuns tiles a CTA is cut at unit borders instead, where
-// runs of kMaxRun tiles suffice for that.
+// runs of kMaxRun tiles suffice for that.  Over an 8-bit cache, whose tiles are of 128 keys, the
+// rule is kept for want of a clear winner (bf16, 8 KV heads, G = 4; us, cut at unit borders / anywhere):
+// N = 0, D = 128, 16 sequences of 500 11.9 / 12.5, 32 of 300 11.7 / 12.9, 4 of 4K 13.9 / 14.0, but one of 500
+// 10.3 / 8.7, of 2K 11.3 / 9.7, 64 of 500 25.5 / 22.0; N = 3, 16 of 500 15.8 / 18.5, 4 of 4K 17.9 / 19.1,
+// one of 2K 13.2 / 12.1; batches of long lists the same.
 constexpr int kSmallRuns = 16, kMinRun = 3, kMaxRun = 24;
 
 struct ParamsR {

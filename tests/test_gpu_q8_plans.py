@@ -91,6 +91,9 @@ def _lens(B, hi):
     (20, 64, 4, 8, 128, 64, 16, BF16, 9000, 1, 2),     # one pair: pieces alone
     (20, 64, 4, 8, 64, 32, 32, BF16, 9000, 1, 2),
     (100, 64, 4, 2, 64, 64, 32, BF16, 8500, 1, 2),     # too many sequences to rank
+    (10, 64, 4, 8, 128, 64, 32, BF16, 900, 1, 1),      # few units and short lists: one part
+    (10, 32, 8, 8, 64, 16, 8, FP16, 3000, 1, 1),
+    (12, 128, 2, 8, 128, 32, 32, BF16, 8300, 1, 2),
     (40, 32, 4, 8, 128, 16, 16, BF16, 700, None, 1),   # (two tiles: none is left over)
 ])
 def test_rows_left_over_join(cuda_device, B, N, G, Hkv, D, page, block, dtype, hi, pairs, pieces):
@@ -100,7 +103,7 @@ def test_rows_left_over_join(cuda_device, B, N, G, Hkv, D, page, block, dtype, h
     else:
         per = 128 // G
         assert (N + 1) % per * G <= 8 and (N + 1) // per == 2 * pairs
-        left = B * Hkv * pieces * pairs * 8 * (D + 4) * 4
+        left = B * Hkv * pieces * pairs * 8 * (D + 4) * 4 if pieces * pairs > 1 else 0
         assert _size(args) >= left + (B * Hkv * 2 * pairs * 2 * 128 * D * 4 if pieces > 1 else 0)
     _check(args, *_runs(args))
 
