@@ -137,3 +137,35 @@ def test_more_rows_than_few_in_a_large_batch(cuda_device, N, G):
     """17 to 32 rows of a KV head."""
     args = _case(N, _lens(64, 900), N, G, 8, 128, 16, 16, BF16)
     _check(args, *_runs(args, 2))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("N,G,D", [(15, 1, 128), (15, 1, 64), (7, 2, 128), (4, 3, 64), (0, 16, 64), (8, 1, 128), (1, 4, 64)])
+def test_as_many_rows_as_few_rows_take(cuda_device, dtype, N, G, D):
+    """8, 9, 15 and 16 rows of a KV head, whole trees and roots alone."""
+    args = _case(N + G, [0, 1, 127, 128, 129, 700, 2500], N, G, 3, D, 16, 8, dtype)
+    _check(args, *_runs(args, 2))
+
+
+@pytest.mark.parametrize("N", [0, 40])
+def test_keys_and_values_in_one_tensor(cuda_device, N):
+    """Pages of keys and values side by side: written, read and attended like pages apart."""
+    B, Hkv, G, D, page, block, P = 3, 2, 4, 128, 32, 16, 150
+    table = torch.randperm(20, generator=torch.Generator().manual_seed(3))[:15].view(B, 5).int().cuda()
+    apart = ops.QuantCache.empty(20, Hkv, page, D, table, block=block)
+    both = torch.zeros(20, 2, Hkv, page, D, dtype=torch.uint8, device="cuda").view(qu.E4M3)
+    scales = [x.clone() for x in (apart.k_scales, apart.v_scales)]
+    side = ops.QuantCache(both[:, 0], both[:, 1], *scales, table)
+    k, v = (torch.randn(B * P, Hkv, D, device="cuda").to(BF16) for _ in range(2))
+    runs, at = torch.arange(0, B * P + 1, P, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    q, kt, vt = (torch.randn(B, N + 1, h, D, device="cuda").to(BF16) for h in (Hkv * G, Hkv, Hkv))
+    mask, n = pu.tree(torch.Generator().manual_seed(4), B, N, [N] * B)
+    got = []
+    for cache in (apart, side):
+        ops.ddtree_append_q8(k, v, runs, at, cache)
+        out, lse = ops.tree_attn_q8(q, cache, kt, vt, at + P, n.cuda(), mask.cuda())
+        rows = [torch.empty_like(k) for _ in range(2)]
+        ops.ddtree_read_q8(cache, runs, at, *rows)
+        got.append((out, lse, *rows, cache.k_scales, cache.v_scales))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    ops.ddtree_device_check()
